@@ -112,6 +112,22 @@ def lib() -> ctypes.CDLL:
         L.bitlinear_forward_lut_plan.argtypes = [i64, i64, i64, p]
         L.bitlinear_forward_subln_plan.restype = c_int
         L.bitlinear_forward_subln_plan.argtypes = [i64, i64, i64, c_int, p]
+        for name in ("bitlinear_mxfp4_codes_bytes", "bitlinear_mxfp4_scales_bytes",
+                     "bitlinear_layernorm_backward_ws_bytes"):
+            getattr(L, name).restype = i64
+            getattr(L, name).argtypes = [i64, i64]
+        L.bitlinear_quantize_mxfp4.restype = c_int
+        L.bitlinear_quantize_mxfp4.argtypes = [p, c_int, i64, i64, p, p, p, p]
+        L.bitlinear_forward_mxfp4.restype = c_int
+        L.bitlinear_forward_mxfp4.argtypes = [p, p, p, p, i64, i64, i64, p, c_int, p]
+        L.bitlinear_forward_mxfp4_fused_ws_bytes.restype = i64
+        L.bitlinear_forward_mxfp4_fused_ws_bytes.argtypes = [i64, i64, i64, c_int]
+        L.bitlinear_forward_mxfp4_fused.restype = c_int
+        L.bitlinear_forward_mxfp4_fused.argtypes = [p, p, p, c_int, i64, i64, i64, p, c_int, p, i64, p]
+        L.bitlinear_layernorm.restype = c_int
+        L.bitlinear_layernorm.argtypes = [p, c_int, i64, i64, p, p, f32, p, p, p, p]
+        L.bitlinear_layernorm_backward.restype = c_int
+        L.bitlinear_layernorm_backward.argtypes = [p, p, c_int, i64, i64, p, p, p, p, p, p, p, i64, p]
         _lib = L
     return _lib
 
@@ -128,7 +144,10 @@ EXPORTED_SYMBOLS = (
     "bitlinear_forward_lut_plan", "bitlinear_kb_pad", "bitlinear_packed_bytes_binary",
     "bitlinear_quantize_weights_binary", "bitlinear_forward_binary", "bitlinear_forward_binary_plan",
     "bitlinear_quantize_weights_noalloc", "bitlinear_forward_ws_bytes", "bitlinear_forward_ws",
-    "bitlinear_forward_ws_plan", "bitlinear_probe_prefill_occupancy",
+    "bitlinear_forward_ws_plan", "bitlinear_probe_prefill_occupancy", "bitlinear_mxfp4_codes_bytes",
+    "bitlinear_mxfp4_scales_bytes", "bitlinear_quantize_mxfp4", "bitlinear_forward_mxfp4",
+    "bitlinear_forward_mxfp4_fused_ws_bytes", "bitlinear_forward_mxfp4_fused", "bitlinear_layernorm",
+    "bitlinear_layernorm_backward_ws_bytes", "bitlinear_layernorm_backward",
 )
 
 MAX_GROUP = 8
@@ -885,3 +904,221 @@ class BitLinear:
     def __call__(self, x):
         y, _, _ = forward_fused(self.packed, self.gamma, x.contiguous(), self.n, self.k)
         return y
+
+
+def _dtype_code(t, name: str) -> int:
+    import torch
+
+    if t == torch.float32:
+        return BL_F32
+    if t == torch.bfloat16:
+        return BL_BF16
+    raise ValueError(f"{name} must be float32 or bfloat16")
+
+
+def _buffer(t, name: str, shape, dtype, dev):
+    """`t` checked to be a contiguous tensor of this shape, type and device, or a new one."""
+    import torch
+
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if t.device != dev or t.dtype != dtype or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}")
+    return t
+
+
+def _bytes_at_least(t, name: str, nbytes: int, dev):
+    """`t` checked to be a contiguous uint8 tensor of at least nbytes on dev."""
+    import torch
+
+    if t.device != dev or t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() < nbytes:
+        raise ValueError(f"{name} must be a contiguous uint8 tensor of at least {nbytes} bytes on {dev}")
+
+
+def _call(fn: str, dev, *args) -> None:
+    """The library call on dev's current stream, with dev the current device."""
+    import torch
+
+    if torch.cuda.current_device() == dev.index:
+        st = getattr(lib(), fn)(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = getattr(lib(), fn)(*args, _stream(dev))
+    _check(fn, st)
+
+
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _require_rows(t, name: str) -> int:
+    """A contiguous GPU matrix of fp32 or bf16 rows; returns its bl_dtype."""
+    _require_cuda(t, name)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    if t.numel() == 0:
+        raise ValueError(f"{name} must not be empty")
+    return _dtype_code(t.dtype, name)
+
+
+def mxfp4_codes_bytes(rows: int, k: int) -> int:
+    """Bytes of the MXFP4 codes of a rows x k matrix (16-row x 128-column tiles of 1024 bytes)."""
+    return -(-rows // 16) * -(-k // 128) * 1024 if rows >= 1 and k >= 1 else -1
+
+
+def mxfp4_scales_bytes(rows: int, k: int) -> int:
+    """Bytes of the MXFP4 block scales of a rows x k matrix."""
+    return -(-rows // 16) * -(-k // 512) * 256 if rows >= 1 and k >= 1 else -1
+
+
+def quantize_mxfp4(x, codes=None, scales=None, values=None, want_values: bool = False):
+    """MXFP4 quantisation of x[R][K] (fp32 or bf16) on the GPU: blocks of 32 columns share a
+    power of two, each element is a 4-bit float (weights and activations alike).
+
+    Returns ``(codes uint8, scales uint8)`` in the layout of bitlinear.h, plus ``values``
+    ([R][K] of x's type, what the codes stand for) when ``want_values`` is set or ``values``
+    is given."""
+    import torch
+
+    dt = _require_rows(x, "x")
+    r, k = x.shape
+    dev = x.device
+    nc, ns = mxfp4_codes_bytes(r, k), mxfp4_scales_bytes(r, k)
+    if codes is None:
+        codes = torch.empty(nc, dtype=torch.uint8, device=dev)
+    _bytes_at_least(codes, "codes", nc, dev)
+    if scales is None:
+        scales = torch.empty(ns, dtype=torch.uint8, device=dev)
+    _bytes_at_least(scales, "scales", ns, dev)
+    if want_values or values is not None:
+        values = _buffer(values, "values", (r, k), x.dtype, dev)
+    _call("bitlinear_quantize_mxfp4", dev, x.data_ptr(), dt, r, k, codes.data_ptr(), scales.data_ptr(), _ptr(values))
+    return (codes, scales, values) if values is not None else (codes, scales)
+
+
+def forward_mxfp4(codes, scales, xcodes, xscales, m: int, n: int, k: int, y=None, out_dtype=None):
+    """y[M][N] = Xv Wv^T of MXFP4 activations (xcodes, xscales: M rows) and weights (codes,
+    scales: N rows), both of K columns, accumulated in fp32; y in ``out_dtype`` (fp32, or
+    bf16), or in that of the given ``y``."""
+    import torch
+
+    dev = codes.device
+    for t, name in ((codes, "codes"), (scales, "scales"), (xcodes, "xcodes"), (xscales, "xscales")):
+        _require_cuda(t, name)
+    _bytes_at_least(codes, "codes", mxfp4_codes_bytes(n, k), dev)
+    _bytes_at_least(scales, "scales", mxfp4_scales_bytes(n, k), dev)
+    _bytes_at_least(xcodes, "xcodes", mxfp4_codes_bytes(m, k), dev)
+    _bytes_at_least(xscales, "xscales", mxfp4_scales_bytes(m, k), dev)
+    out_dtype = out_dtype or (y.dtype if y is not None else torch.float32)
+    ydt = _dtype_code(out_dtype, "out_dtype")
+    y = _buffer(y, "y", (max(m, 0), max(n, 0)), out_dtype, dev)
+    _call("bitlinear_forward_mxfp4", dev, codes.data_ptr(), scales.data_ptr(), xcodes.data_ptr(), xscales.data_ptr(),
+          m, n, k, y.data_ptr(), ydt)
+    return y
+
+
+def forward_mxfp4_fused_ws_bytes(m: int, n: int, k: int, dtype: str = "bf16") -> int:
+    """Workspace bytes bitlinear_forward_mxfp4_fused needs for (M, N, K) (0: none)."""
+    v = int(lib().bitlinear_forward_mxfp4_fused_ws_bytes(m, n, k, BL_BF16 if dtype == "bf16" else BL_F32))
+    if v < 0:
+        raise ValueError(f"invalid shape {(m, n, k)}")
+    return v
+
+
+def forward_mxfp4_fused(codes, scales, x, n: int, k: int, y=None, workspace=None, out_dtype=None):
+    """Quantise x[M][K] (fp32 or bf16) to MXFP4 and apply MXFP4 weights (codes, scales: N
+    rows) in one call; y[M][N] as forward_mxfp4.  A workspace of at least
+    forward_mxfp4_fused_ws_bytes is allocated unless one is given."""
+    import torch
+
+    dt = _require_rows(x, "x")
+    if x.shape[1] != k:
+        raise ValueError("x must be [tokens, K]")
+    m = x.shape[0]
+    dev = x.device
+    _require_cuda(codes, "codes")
+    _require_cuda(scales, "scales")
+    _bytes_at_least(codes, "codes", mxfp4_codes_bytes(n, k), dev)
+    _bytes_at_least(scales, "scales", mxfp4_scales_bytes(n, k), dev)
+    out_dtype = out_dtype or (y.dtype if y is not None else torch.float32)
+    ydt = _dtype_code(out_dtype, "out_dtype")
+    y = _buffer(y, "y", (m, max(n, 0)), out_dtype, dev)
+    need = max(0, int(lib().bitlinear_forward_mxfp4_fused_ws_bytes(m, n, k, dt)))
+    if workspace is not None:
+        _bytes_at_least(workspace, "workspace", need, dev)
+    elif need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _call("bitlinear_forward_mxfp4_fused", dev, codes.data_ptr(), scales.data_ptr(), x.data_ptr(), dt, m, n, k,
+          y.data_ptr(), ydt, _ptr(workspace), workspace.numel() if workspace is not None else 0)
+    return y
+
+
+def _vector(t, name: str, n: int, dev):
+    """`t` (may be None) checked to be a contiguous fp32 vector of n elements on dev."""
+    import torch
+
+    if t is not None and (t.device != dev or t.dtype != torch.float32 or not t.is_contiguous() or
+                          tuple(t.shape) != (n,)):
+        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {(n,)} on {dev}")
+    return t
+
+
+def layernorm(x, weight=None, bias=None, eps: float = 1e-5, y=None, mean=None, rstd=None):
+    """Layer normalisation of the rows of x[M][K] (fp32 or bf16) with fp32 weight and bias
+    (None: ones, zeros).  Returns ``(y, mean fp32 [M], rstd fp32 [M])``; y has x's type."""
+    import torch
+
+    dt = _require_rows(x, "x")
+    m, k = x.shape
+    dev = x.device
+    _vector(weight, "weight", k, dev)
+    _vector(bias, "bias", k, dev)
+    y = _buffer(y, "y", (m, k), x.dtype, dev)
+    mean = _buffer(mean, "mean", (m,), torch.float32, dev)
+    rstd = _buffer(rstd, "rstd", (m,), torch.float32, dev)
+    _call("bitlinear_layernorm", dev, x.data_ptr(), dt, m, k, _ptr(weight), _ptr(bias), eps, y.data_ptr(),
+          mean.data_ptr(), rstd.data_ptr())
+    return y, mean, rstd
+
+
+def layernorm_backward_ws_bytes(m: int, k: int) -> int:
+    """Workspace bytes bitlinear_layernorm_backward needs for dweight and dbias of x[M][K]."""
+    v = int(lib().bitlinear_layernorm_backward_ws_bytes(m, k))
+    if v < 0:
+        raise ValueError(f"invalid shape {(m, k)}")
+    return v
+
+
+def layernorm_backward(dy, x, weight, mean, rstd, dx=None, dweight=None, dbias=None, workspace=None,
+                       want_params: bool = True):
+    """Gradients of layernorm: dy and x [M][K], weight fp32 [K] (None: ones), mean and rstd
+    from the forward call.  Returns ``(dx, dweight, dbias)``, or ``dx`` alone with
+    ``want_params=False``; dx has x's type, the others are fp32 and overwritten.  A workspace
+    of at least layernorm_backward_ws_bytes is allocated unless one is given."""
+    import torch
+
+    dt = _require_rows(x, "x")
+    m, k = x.shape
+    dev = x.device
+    if _require_rows(dy, "dy") != dt or dy.shape != x.shape or dy.device != dev:
+        raise ValueError("dy must have x's shape, type and device")
+    _vector(weight, "weight", k, dev)
+    if mean is None or rstd is None:
+        raise ValueError("mean and rstd of the forward call are needed")
+    _vector(mean, "mean", m, dev)
+    _vector(rstd, "rstd", m, dev)
+    dx = _buffer(dx, "dx", (m, k), x.dtype, dev)
+    if want_params:
+        dweight = _buffer(dweight, "dweight", (k,), torch.float32, dev)
+        dbias = _buffer(dbias, "dbias", (k,), torch.float32, dev)
+        need = max(0, int(lib().bitlinear_layernorm_backward_ws_bytes(m, k)))
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        else:
+            _bytes_at_least(workspace, "workspace", need, dev)
+    else:
+        dweight = dbias = None
+    _call("bitlinear_layernorm_backward", dev, dy.data_ptr(), x.data_ptr(), dt, m, k, _ptr(weight), mean.data_ptr(),
+          rstd.data_ptr(), dx.data_ptr(), _ptr(dweight), _ptr(dbias), _ptr(workspace),
+          workspace.numel() if workspace is not None else 0)
+    return (dx, dweight, dbias) if want_params else dx

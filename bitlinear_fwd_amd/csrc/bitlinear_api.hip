@@ -5,6 +5,8 @@
 #include "bl_internal.h"
 #include "gemv_lut.h"
 #include "binary.h"
+#include "layernorm.h"
+#include "mxfp4.h"
 
 namespace {
 
@@ -20,8 +22,18 @@ bool use_decode(int64_t M, int64_t N, int64_t K) { return M <= kDecodeMaxM || bl
 
 int hip_status(hipError_t e) { return e == hipSuccess ? BL_OK : BL_ERR_HIP; }
 
+bool dtype_ok(int dt) { return dt == BL_F32 || dt == BL_BF16; }
+uintptr_t dtype_align(int dt) { return dt == BL_F32 ? 4 : 2; }
+// rows x K of an MXFP4 matrix or a layer norm
+bool rows_ok(int64_t R, int64_t K) { return R >= 1 && K >= 1 && R < kMaxDim && K <= kMaxK; }
+
 // eps of the sub-layer normalisation: finite and >= 0 (NaN fails both comparisons)
 bool eps_ok(float eps) { return eps >= 0.0f && eps <= 3.4028234663852886e38f; }
+
+// Sizes of an MXFP4 product: both matrices addressable, and a launchable number of tiles.
+bool mx_product_ok(int64_t M, int64_t N, int64_t K) {
+  return M <= kMaxCount / K && N <= kMaxCount / K && bl::mx_row_blocks(M) <= (int64_t(1) << 30) / bl::mx_row_blocks(N);
+}
 
 int grouped_impl(const bl_matrix* mats, int count, const void* X, int dt, int64_t M, int64_t K, const float* gain,
                  float eps, int8_t* Xq, float* absmax, void* stream, bool norm);
@@ -124,6 +136,84 @@ int bitlinear_forward_ws(const uint8_t* packed, const float* gamma, const int8_t
     return BL_ERR_INVALID_ARG;
   return hip_status(bl::launch_gemm_ws(packed, gamma, Xq, absmax, M, N, K, Y, acc, workspace,
                                        static_cast<hipStream_t>(stream)));
+}
+
+int64_t bitlinear_mxfp4_codes_bytes(int64_t R, int64_t K) { return (R < 1 || K < 1) ? -1 : bl::mx_codes_bytes(R, K); }
+int64_t bitlinear_mxfp4_scales_bytes(int64_t R, int64_t K) {
+  return (R < 1 || K < 1) ? -1 : bl::mx_scales_bytes(R, K);
+}
+
+int bitlinear_quantize_mxfp4(const void* X, int dt, int64_t R, int64_t K, uint8_t* codes, uint8_t* scales,
+                             void* values, void* stream) {
+  if (!X || !codes || !scales || !rows_ok(R, K)) return BL_ERR_INVALID_ARG;
+  if (!dtype_ok(dt) || R > kMaxCount / K) return BL_ERR_UNSUPPORTED;
+  if (!aligned(X, dtype_align(dt)) || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(values, dtype_align(dt)))
+    return BL_ERR_INVALID_ARG;
+  return hip_status(
+      bl::launch_mx_quant(X, dt == BL_BF16, R, K, codes, scales, values, static_cast<hipStream_t>(stream)));
+}
+
+int bitlinear_forward_mxfp4(const uint8_t* codes, const uint8_t* scales, const uint8_t* xcodes,
+                            const uint8_t* xscales, int64_t M, int64_t N, int64_t K, void* Y, int ydt, void* stream) {
+  if (!codes || !scales || !xcodes || !xscales || !Y || !rows_ok(M, K) || !rows_ok(N, K)) return BL_ERR_INVALID_ARG;
+  if (!mx_product_ok(M, N, K) || !dtype_ok(ydt)) return BL_ERR_UNSUPPORTED;
+  if (!aligned(codes, 16) || !aligned(scales, 4) || !aligned(xcodes, 16) || !aligned(xscales, 4) ||
+      !aligned(Y, dtype_align(ydt)))
+    return BL_ERR_INVALID_ARG;
+  return hip_status(bl::launch_mx_decode(codes, scales, xcodes, xscales, M, N, K, Y, ydt == BL_BF16,
+                                         static_cast<hipStream_t>(stream)));
+}
+
+int64_t bitlinear_forward_mxfp4_fused_ws_bytes(int64_t M, int64_t N, int64_t K, int dt) {
+  if (!rows_ok(M, K) || !rows_ok(N, K) || !dtype_ok(dt)) return -1;
+  return bl::mx_codes_bytes(M, K) + bl::mx_scales_bytes(M, K);
+}
+
+int bitlinear_forward_mxfp4_fused(const uint8_t* codes, const uint8_t* scales, const void* X, int dt, int64_t M,
+                                  int64_t N, int64_t K, void* Y, int ydt, void* workspace, int64_t ws_bytes,
+                                  void* stream) {
+  if (!codes || !scales || !X || !Y || !rows_ok(M, K) || !rows_ok(N, K)) return BL_ERR_INVALID_ARG;
+  if (!mx_product_ok(M, N, K) || !dtype_ok(dt) || !dtype_ok(ydt)) return BL_ERR_UNSUPPORTED;
+  if (!aligned(codes, 16) || !aligned(scales, 4) || !aligned(X, dtype_align(dt)) || !aligned(Y, dtype_align(ydt)))
+    return BL_ERR_INVALID_ARG;
+  const int64_t need = bitlinear_forward_mxfp4_fused_ws_bytes(M, N, K, dt);
+  if (need > 0 && (!workspace || !aligned(workspace, 16) || ws_bytes < need)) return BL_ERR_INVALID_ARG;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  uint8_t* xcodes = static_cast<uint8_t*>(workspace);
+  uint8_t* xscales = xcodes + bl::mx_codes_bytes(M, K);
+  const hipError_t e = bl::launch_mx_quant(X, dt == BL_BF16, M, K, xcodes, xscales, nullptr, s);
+  if (e != hipSuccess) return BL_ERR_HIP;
+  return hip_status(bl::launch_mx_decode(codes, scales, xcodes, xscales, M, N, K, Y, ydt == BL_BF16, s));
+}
+
+int bitlinear_layernorm(const void* X, int dt, int64_t M, int64_t K, const float* weight, const float* bias,
+                        float eps, void* Y, float* mean, float* rstd, void* stream) {
+  if (!X || !Y || !rows_ok(M, K) || !eps_ok(eps) || eps == 0.0f) return BL_ERR_INVALID_ARG;
+  if (!dtype_ok(dt) || M > kMaxCount / K) return BL_ERR_UNSUPPORTED;
+  if (!aligned(X, dtype_align(dt)) || !aligned(Y, dtype_align(dt)) || !aligned(weight, 4) || !aligned(bias, 4) ||
+      !aligned(mean, 4) || !aligned(rstd, 4))
+    return BL_ERR_INVALID_ARG;
+  return hip_status(bl::launch_layernorm(X, dt == BL_BF16, M, K, weight, bias, eps, Y, mean, rstd,
+                                         static_cast<hipStream_t>(stream)));
+}
+
+int64_t bitlinear_layernorm_backward_ws_bytes(int64_t M, int64_t K) {
+  return rows_ok(M, K) ? bl::plan_layernorm_backward(M, K).ws_bytes : -1;
+}
+
+int bitlinear_layernorm_backward(const void* dY, const void* X, int dt, int64_t M, int64_t K, const float* weight,
+                                 const float* mean, const float* rstd, void* dX, float* dW, float* dB,
+                                 void* workspace, int64_t ws_bytes, void* stream) {
+  if (!dY || !X || !mean || !rstd || (!dX && !dW && !dB) || !rows_ok(M, K)) return BL_ERR_INVALID_ARG;
+  if (!dtype_ok(dt) || M > kMaxCount / K) return BL_ERR_UNSUPPORTED;
+  if (!aligned(dY, dtype_align(dt)) || !aligned(X, dtype_align(dt)) || !aligned(dX, dtype_align(dt)) ||
+      !aligned(weight, 4) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(dW, 4) || !aligned(dB, 4))
+    return BL_ERR_INVALID_ARG;
+  if ((dW || dB) &&
+      (!workspace || !aligned(workspace, 16) || ws_bytes < bitlinear_layernorm_backward_ws_bytes(M, K)))
+    return BL_ERR_INVALID_ARG;
+  return hip_status(bl::launch_layernorm_backward(dY, X, dt == BL_BF16, M, K, weight, mean, rstd, dX, dW, dB,
+                                                  static_cast<float*>(workspace), static_cast<hipStream_t>(stream)));
 }
 
 int bitlinear_probe_prefill_occupancy(int32_t out[4]) {

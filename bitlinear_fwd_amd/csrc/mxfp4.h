@@ -1,0 +1,128 @@
+// Microscaled 4-bit floating point (MXFP4): layout, conversions and launchers shared by the
+// quantiser, the decode kernel and the GEMM.
+//
+// A block is 32 consecutive columns of a row.  Its scale byte e stands for 2^(e - 127) (255:
+// NaN), its 32 codes for magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6 with a sign bit.
+//
+// Layout of a matrix of R rows and K columns: 1024-byte tiles of 16 rows x 128 columns, tile
+// (rb, c) at (rb * ceil(K / 128) + c) * 1024; in a tile, row r's block b (columns 32b ..
+// 32b + 31) is the 16 bytes at 16 * (16 b + r), low nibble first.  So lane l of a wave that
+// loads 16 bytes at 16 l holds row l % 16, block l / 16: exactly the operand of
+// v_mfma_scale_f32_16x16x128_f8f6f4 (and, two tiles taken together, of the 32x32x64 form).
+// The scales of four tiles 4 c4 .. 4 c4 + 3 sit in one 32-bit word per lane, tile 4 c4 + t in
+// byte t, the words of (rb, c4) at ((rb * ceil(K / 512) + c4) * 64 + l) * 4: one wave load per
+// four tiles, and the instruction's byte select picks the tile.
+#pragma once
+#include "bl_internal.h"
+
+namespace bl {
+
+constexpr int kMxRows = 16;        // rows of a tile
+constexpr int kMxCols = 128;       // columns of a tile
+constexpr int kMxTileBytes = 1024;
+constexpr int kMxGroupCols = 512;  // columns that share a word of scales (four tiles)
+
+inline int64_t mx_row_blocks(int64_t r) { return (r + kMxRows - 1) / kMxRows; }
+inline int64_t mx_tiles(int64_t k) { return (k + kMxCols - 1) / kMxCols; }
+inline int64_t mx_groups(int64_t k) { return (k + kMxGroupCols - 1) / kMxGroupCols; }
+inline int64_t mx_codes_bytes(int64_t r, int64_t k) { return mx_row_blocks(r) * mx_tiles(k) * kMxTileBytes; }
+inline int64_t mx_scales_bytes(int64_t r, int64_t k) { return mx_row_blocks(r) * mx_groups(k) * 256; }
+
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v2f __attribute__((ext_vector_type(2)));
+
+// acc += A B of one tile pair: A's 16 rows x 128 columns (lane l: row l % 16, block l / 16) by
+// B's, the scales in bytes TA and TB of sa and sb.  acc[i] of lane l is the sum for A's row
+// 4 (l / 16) + i and B's row l % 16.
+template <int TA, int TB>
+__device__ __forceinline__ v4f mx_mfma(v4i a, v4i b, v4f acc, int sa, int sb) {
+  const v8i wa = __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1);
+  const v8i wb = __builtin_shufflevector(b, b, 0, 1, 2, 3, -1, -1, -1, -1);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wa, wb, acc, 4, 4, TA, sa, TB, sb);
+}
+
+// Scale byte of a block whose largest magnitude has the fp32 bits `bits` (sign cleared): the
+// power of two of that magnitude over 4, the grid's largest power (2^-127 at least); 255 where
+// the block holds a NaN or an infinity.
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t bits) {
+  const uint32_t field = bits >> 23;
+  if (field == 255) return 255;
+  return field < 2 ? 0 : field - 2;
+}
+
+// The fp32 number 2^(e - 127), e < 255 (e = 0: the subnormal 2^-127).
+__device__ __forceinline__ float mx_scale(uint32_t e) { return __uint_as_float(e ? e << 23 : 0x00400000u); }
+
+// Eight consecutive elements of a row as fp32; elements past n are 0.  Whole groups are read 16
+// bytes at a time at any alignment (the target's global loads need none).
+__device__ __forceinline__ void load8(const float* p, int64_t n, float (&v)[8]) {
+  if (n >= 8) {
+    __builtin_memcpy(v, p, 32);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : 0.0f;
+  }
+}
+__device__ __forceinline__ void load8(const uint16_t* p, int64_t n, float (&v)[8]) {
+  uint32_t w[4];
+  if (n >= 8) {
+    __builtin_memcpy(w, p, 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = (2 * i < n ? (uint32_t)p[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)p[2 * i + 1] << 16 : 0u);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+// fp32 to bf16 bits, to nearest with ties to even (NaN stays NaN: a quiet bit is set).
+__device__ __forceinline__ uint32_t bf16_bits(float f) {
+  const uint32_t u = __float_as_uint(f);
+  if ((u & 0x7fffffffu) > 0x7f800000u) return (u >> 16) | 0x40u;
+  return (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
+}
+
+// Eight fp32 values to a row; only the first n are written.
+__device__ __forceinline__ void store8(float* p, int64_t n, const float (&v)[8]) {
+  if (n >= 8) {
+    __builtin_memcpy(p, v, 32);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = v[i];
+  }
+}
+__device__ __forceinline__ void store8(uint16_t* p, int64_t n, const float (&v)[8]) {
+  if (n >= 8) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = bf16_bits(v[2 * i]) | bf16_bits(v[2 * i + 1]) << 16;
+    __builtin_memcpy(p, w, 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = (uint16_t)bf16_bits(v[i]);
+  }
+}
+
+// Launchers (sizes and pointers validated by the C ABI).
+hipError_t launch_mx_quant(const void* X, int bf16, int64_t R, int64_t K, uint8_t* codes, uint8_t* scales,
+                           void* values, hipStream_t s);
+hipError_t launch_mx_decode(const uint8_t* codes, const uint8_t* scales, const uint8_t* xcodes,
+                            const uint8_t* xscales, int64_t M, int64_t N, int64_t K, void* Y, int ybf16,
+                            hipStream_t s);
+
+// Launch plan of the decode kernel.
+struct MxDecodePlan {
+  int waves = 4;       // waves per workgroup; they split the column groups
+  int tg = 1;          // token groups of 16 per workgroup
+  int64_t gx = 0, gy = 0;
+};
+MxDecodePlan plan_mx_decode(int64_t M, int64_t N, int64_t K);
+
+}  // namespace bl

@@ -340,6 +340,93 @@ int bitlinear_forward_binary(const uint8_t* packed, const float* beta, const int
 int bitlinear_forward_binary_plan(int64_t M, int64_t N, int64_t K, int32_t out[6]);
 
 /*
+ * Microscaled 4-bit floating point (MXFP4), the 4-bit format the gfx950 matrix cores take
+ * directly: a quantiser for weights and activations alike, and the product of two matrices
+ * held in it.  Per row, a block of 32 consecutive columns shares one power of two; every
+ * element is a 4-bit float (magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign):
+ *   e = max(E - 2, 0), E the fp32 exponent field of the block's largest magnitude;
+ *   code = the sign in bit 3 and, in bits 0..2, the index of the magnitude nearest to
+ *          |x| / 2^(e - 127) (< 8), a tie going to the even index and everything above the
+ *          grid to 6; the value it stands for is +-magnitude * 2^(e - 127).
+ * Everything but that rounding is exact, so codes, scales and values do not depend on the
+ * implementation.  The last block of a row may be shorter.  A block with a NaN or an
+ * infinity gets the scale byte 255 and zero codes: its values are NaN, and so is every
+ * output of a product that reads it.  (These calls do define non-finite inputs.)
+ *
+ * Layout for R rows and K columns.  Codes: 1024-byte tiles of 16 rows x 128 columns, tile
+ * (rb, c) at (rb * ceil(K / 128) + c) * 1024; in it row r's block b (32 columns) is the 16
+ * bytes at 16 * (16 b + r), column 32 b + i in bits 4 (i % 2) .. +3 of byte i / 2.  Scales:
+ * the byte of row r, block b of tile (rb, c) at ((rb * ceil(K / 512) + c / 4) * 64 + 16 b +
+ * r) * 4 + c % 4.  Rows and columns of the padding hold zero codes and zero scale bytes;
+ * bitlinear_quantize_mxfp4 writes them, and the products rely on the columns' (those of the
+ * rows change no output).
+ *
+ * bitlinear_quantize_mxfp4:
+ *   X       [R][K] fp32 (dt = BL_F32) or bf16 (dt = BL_BF16), row-major, element-aligned.
+ *   codes   out: bitlinear_mxfp4_codes_bytes(R, K) bytes, 16-byte aligned.
+ *   scales  out: bitlinear_mxfp4_scales_bytes(R, K) bytes, 4-byte aligned.
+ *   values  out (nullable): [R][K] of type dt, the values the codes stand for (each is exact
+ *           in either type): x after a round trip through the format.
+ * bitlinear_forward_mxfp4: Y[m][n] = sum_k Xv[m][k] Wv[n][k], Xv and Wv the values of the M
+ *   token rows (xcodes, xscales) and the N weight rows (codes, scales), accumulated in fp32.
+ *   Y       out: [M][N] fp32 (ydt = BL_F32) or bf16 (BL_BF16, rounded once at the end, ties
+ *           to even), row-major, element-aligned.
+ *   codes and xcodes 16-byte aligned, scales and xscales 4-byte aligned.
+ * bitlinear_forward_mxfp4_fused: the same of an un-quantised X[M][K] (fp32 or bf16): the
+ *   results of bitlinear_quantize_mxfp4 followed by bitlinear_forward_mxfp4.
+ *   workspace  device memory of at least bitlinear_forward_mxfp4_fused_ws_bytes(M, N, K, dt)
+ *           bytes, 16-byte aligned; may be null where that is 0.  Its contents on entry do
+ *           not matter and nothing carries over.  Calls that share a workspace must not
+ *           overlap.
+ * Limits: 1 <= R, M, N < 2^31, 1 <= K <= 2^24 (else BL_ERR_INVALID_ARG); BL_ERR_UNSUPPORTED
+ * for other types, for R * K > 2^40 and for products of more than 2^30 output tiles of 16
+ * x 16.  Buffers of one call must not overlap.
+ */
+int64_t bitlinear_mxfp4_codes_bytes(int64_t R, int64_t K);  /* -1 for arguments < 1 */
+int64_t bitlinear_mxfp4_scales_bytes(int64_t R, int64_t K); /* -1 for arguments < 1 */
+int bitlinear_quantize_mxfp4(const void* X, int dt, int64_t R, int64_t K, uint8_t* codes, uint8_t* scales,
+                             void* values, void* stream);
+int bitlinear_forward_mxfp4(const uint8_t* codes, const uint8_t* scales, const uint8_t* xcodes,
+                            const uint8_t* xscales, int64_t M, int64_t N, int64_t K, void* Y, int ydt, void* stream);
+int64_t bitlinear_forward_mxfp4_fused_ws_bytes(int64_t M, int64_t N, int64_t K, int dt);
+int bitlinear_forward_mxfp4_fused(const uint8_t* codes, const uint8_t* scales, const void* X, int dt, int64_t M,
+                                  int64_t N, int64_t K, void* Y, int ydt, void* workspace, int64_t ws_bytes,
+                                  void* stream);
+
+/*
+ * Layer normalisation with centring and bias, the full form of the norm in front of the
+ * quantisers (bitlinear_subln_* is the form without centring, fused into the int8 one), and
+ * its gradients.  Over each row:
+ *     mean = sum_k x / K,  rstd = 1 / sqrt(sum_k (x - mean)^2 / K + eps),
+ *     y = (x - mean) * rstd * weight[k] + bias[k].
+ *   X, Y    [M][K] of type dt (BL_F32 or BL_BF16), row-major, element-aligned.
+ *   weight, bias  fp32 [K] (nullable: ones, zeros).
+ *   mean, rstd    out (nullable): fp32 [M], what the backward pass takes.
+ *   eps     finite and > 0 (BL_ERR_INVALID_ARG otherwise).
+ * Sums are taken in fp32 or more; y is rounded to dt once.  A row with a NaN or an infinity,
+ * or whose squares overflow fp32, has outputs that are not meaningful; other rows are not
+ * affected by it.
+ *
+ * bitlinear_layernorm_backward: with xhat = (x - mean) * rstd and g = dy * weight,
+ *     dx = rstd * (g - sum_k g / K - xhat * sum_k (g * xhat) / K),
+ *     dweight[k] = sum_m dy * xhat,  dbias[k] = sum_m dy.
+ *   dY, X, dX  [M][K] of type dt; mean, rstd fp32 [M] from the forward call.
+ *   dX, dW, dB out, each nullable (at least one not null); dW and dB fp32 [K], overwritten.
+ *   workspace  at least bitlinear_layernorm_backward_ws_bytes(M, K) bytes, 16-byte aligned,
+ *           for the partial sums of dW and dB; may be null if both are.  Contents on entry do
+ *           not matter; calls that share one must not overlap.
+ * The sums over the rows are taken in an order fixed by M and K: results are reproducible bit
+ * for bit.  Limits: 1 <= M < 2^31, 1 <= K <= 2^24, M * K <= 2^40 (BL_ERR_UNSUPPORTED beyond
+ * the last).  Buffers of one call must not overlap.
+ */
+int bitlinear_layernorm(const void* X, int dt, int64_t M, int64_t K, const float* weight, const float* bias,
+                        float eps, void* Y, float* mean, float* rstd, void* stream);
+int64_t bitlinear_layernorm_backward_ws_bytes(int64_t M, int64_t K); /* -1 for invalid sizes */
+int bitlinear_layernorm_backward(const void* dY, const void* X, int dt, int64_t M, int64_t K, const float* weight,
+                                 const float* mean, const float* rstd, void* dX, float* dW, float* dB,
+                                 void* workspace, int64_t ws_bytes, void* stream);
+
+/*
  * Host-only description of the launch bitlinear_forward would make for (M, N, K); no
  * device work.  out[0] = kernel (1 = decode, 2 = prefill), out[1] = workgroups,
  * out[2] = threads per workgroup, out[3] = decode: 16-row output blocks per workgroup,

@@ -1,0 +1,170 @@
+"""Layer normalisation and its gradients on the GPU against the plain 64-bit forms."""
+import numpy as np
+import pytest
+import torch
+
+import bitlinear_fwd_amd as bl
+import mxfp4_reference as ref
+from gpu_helpers import acts_host_f32, host
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+U = 2.0 ** -24
+
+# one element, rows shared by a wave, by 256 and by 1024 threads, longer rows; odd sizes around each
+SIZES = [(1, 1), (3, 7), (2, 8), (5, 64), (9, 513), (4, 2048), (3, 2049), (7, 2560), (6, 5000), (5, 8192), (2, 8193),
+         (3, 28672), (2, 32768), (2, 32775), (1, 100003), (700, 40), (1030, 257), (530, 2560)]
+
+
+def data(m, k, dtype, seed, offset=0.5):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    x = (torch.randn((m, k), generator=g, device=DEV) * 2 + offset).to(DT[dtype])
+    w = 1 + 0.2 * torch.randn(k, generator=g, device=DEV)
+    b = 0.3 * torch.randn(k, generator=g, device=DEV)
+    dy = torch.randn((m, k), generator=g, device=DEV).to(DT[dtype])
+    return x, w, b, dy
+
+
+def rounded(tol, want, dtype):
+    """The bound with the one rounding to dtype on top."""
+    return tol + (2.0 ** -8 if dtype == "bf16" else 2.0 ** -24) * (np.abs(want) + tol)
+
+
+def within(got, want, tol, what):
+    bad = ~(np.abs(got.astype(np.float64) - want) <= tol)
+    assert not bad.any(), (what, int(bad.sum()), np.argwhere(bad)[:3].tolist(), got[bad][:3], want[bad][:3])
+
+
+def check_forward(x, w, b, eps, dtype):
+    m, k = x.shape
+    y, mean, rstd = bl.layernorm(x, w, b, eps)
+    xh = acts_host_f32(x).astype(np.float64)
+    wh, bh = (None if w is None else host(w)), (None if b is None else host(b))
+    wy, wm, wr = ref.layernorm(xh, wh, bh, eps)
+    # a row sum: at most 64 roundings on the way of any term (32 in a thread, 6 in a wave, 16 over waves)
+    d = 64 * U * np.abs(xh).mean(1)
+    within(host(mean), wm, d + U * np.abs(wm), "mean")
+    # the variance moves by d^2 for a mean off by d, and by its own sum's roundings
+    rel = 0.5 * (72 * U + d * d * wr * wr) + 4 * U
+    within(host(rstd), wr, rel * wr, "rstd")
+    a = np.abs(wy - (0 if bh is None else bh))
+    ww = 1.0 if wh is None else np.abs(wh)
+    tol = ww * (wr * (d + U * np.abs(xh).max(1)))[:, None] * (1 + rel)[:, None] + a * (rel + 6 * U)[:, None]
+    tol = tol + 2 * U * (a + (0 if bh is None else np.abs(bh)))
+    within(acts_host_f32(y), wy, rounded(tol, wy, dtype), "y")
+    return y, mean, rstd
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("m,k", SIZES)
+def test_layernorm(m, k, dtype):
+    print(f"case: layernorm M={m} K={k} {dtype}", flush=True)
+    x, w, b, _ = data(m, k, dtype, seed=m + k)
+    check_forward(x, w, b, 1e-5, dtype)
+    check_forward(x, None, b, 1e-2, dtype)
+    check_forward(x, w, None, 1e-5, dtype)
+    check_forward(x, None, None, 1e-12, dtype)
+
+
+@pytest.mark.parametrize("k", [33, 1000, 2560, 20000, 40000])
+def test_layernorm_large_mean_and_constant_rows(k):
+    """A mean a thousand times the spread; a constant row (variance 0); a zero row."""
+    x, w, b, _ = data(6, k, "f32", seed=k, offset=2000.0)
+    x[2] = 3.0
+    x[3] = 0.0
+    y, mean, rstd = check_forward(x, w, b, 1e-5, "f32")
+    assert torch.equal(y[3], b) and float(mean[3]) == 0.0
+    assert abs(float(rstd[3]) - 1e-5 ** -0.5) < 1e-4
+
+
+def check_backward(dy, x, w, mean, rstd, dtype):
+    dx, dw, db = bl.layernorm_backward(dy, x, w, mean, rstd)
+    wx, ww, wb, tx, tw, tb = ref.layernorm_backward(acts_host_f32(dy), acts_host_f32(x), None if w is None else host(w),
+                                                    host(mean), host(rstd))
+    within(acts_host_f32(dx), wx, rounded(tx, wx, dtype), "dx")
+    within(host(dw), ww, tw + U * np.abs(ww), "dweight")
+    within(host(db), wb, tb + U * np.abs(wb), "dbias")
+    return dx, dw, db
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("m,k", SIZES + [(3000, 72), (2050, 9000)])
+def test_layernorm_backward(m, k, dtype):
+    print(f"case: layernorm_backward M={m} K={k} {dtype}", flush=True)
+    x, w, b, dy = data(m, k, dtype, seed=m + k)
+    _, mean, rstd = bl.layernorm(x, w, b, 1e-5)
+    dx, dw, db = check_backward(dy, x, w, mean, rstd, dtype)
+    check_backward(dy, x, None, mean, rstd, dtype)
+    only = bl.layernorm_backward(dy, x, w, mean, rstd, want_params=False)
+    assert torch.equal(only, dx)
+    again = bl.layernorm_backward(dy, x, w, mean, rstd)
+    assert torch.equal(again[0], dx) and torch.equal(again[1], dw) and torch.equal(again[2], db)
+
+
+@pytest.mark.parametrize("m,k", [(5, 100), (40, 2560), (3, 9000), (70, 40000)])
+def test_layernorm_backward_subsets(m, k):
+    """Each output alone through the C ABI equals the same output of the full call, and the others
+    are not written."""
+    x, w, b, dy = data(m, k, "f32", seed=k)
+    _, mean, rstd = bl.layernorm(x, w, b, 1e-5)
+    full = bl.layernorm_backward(dy, x, w, mean, rstd)
+    ws = torch.empty(bl.layernorm_backward_ws_bytes(m, k), dtype=torch.uint8, device=DEV)
+    s = torch.cuda.current_stream().cuda_stream
+    for i, shape in enumerate([(m, k), (k,), (k,)]):
+        out = torch.full(shape, 5.0, device=DEV)
+        ptr = [None, None, None]
+        ptr[i] = out.data_ptr()
+        st = bl.lib().bitlinear_layernorm_backward(dy.data_ptr(), x.data_ptr(), bl.BL_F32, m, k, w.data_ptr(),
+                                                   mean.data_ptr(), rstd.data_ptr(), *ptr, ws.data_ptr(), ws.numel(), s)
+        assert st == bl.BL_OK
+        assert torch.equal(out, full[i])
+
+
+def test_layernorm_nonfinite_rows_stay_apart():
+    for k in (100, 3000, 40000):
+        x, w, b, dy = data(5, k, "f32", seed=k)
+        clean, mean, rstd = bl.layernorm(x, w, b, 1e-5)
+        gclean = bl.layernorm_backward(dy, x, w, mean, rstd, want_params=False)
+        x[1, k - 1] = float("nan")
+        x[3, 0] = float("inf")
+        y, mean, rstd = bl.layernorm(x, w, b, 1e-5)
+        dx = bl.layernorm_backward(dy, x, w, mean, rstd, want_params=False)
+        for r in (0, 2, 4):
+            assert torch.equal(y[r], clean[r]) and torch.equal(dx[r], gclean[r])
+        assert torch.isnan(y[1]).all() and torch.isnan(dx[1]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_layernorm_unaligned_rows(dtype):
+    """Rows that start at odd elements: an odd row length in storage that starts one element in."""
+    m, k = 9, 2563
+    x, w, b, dy = data(m, k, dtype, seed=4)
+
+    def moved(t):
+        flat = torch.empty(t.numel() + 1, dtype=t.dtype, device=DEV)
+        flat[1:] = t.reshape(-1)
+        return flat[1:].view(t.shape)
+
+    y, mean, rstd = check_forward(moved(x), moved(w), moved(b), 1e-5, dtype)
+    check_backward(moved(dy), moved(x), moved(w), moved(mean), moved(rstd), dtype)
+
+
+def test_layernorm_argument_errors():
+    x, w, b, dy = data(4, 64, "f32", seed=1)
+    _, mean, rstd = bl.layernorm(x, w, b)
+    for bad in (lambda: bl.layernorm(x.half(), w, b), lambda: bl.layernorm(x.t(), None, None),
+                lambda: bl.layernorm(x, w[:-1], b), lambda: bl.layernorm(x, w.bfloat16(), b),
+                lambda: bl.layernorm(x, w, b, y=torch.empty(4, 63, device=DEV)),
+                lambda: bl.layernorm(x[:0], w, b),
+                lambda: bl.layernorm_backward(dy.bfloat16(), x, w, mean, rstd),
+                lambda: bl.layernorm_backward(dy[:3], x, w, mean, rstd),
+                lambda: bl.layernorm_backward(dy, x, w, None, rstd),
+                lambda: bl.layernorm_backward(dy, x, w, mean[:3], rstd),
+                lambda: bl.layernorm_backward(dy, x, w, mean, rstd,
+                                              workspace=torch.empty(8, dtype=torch.uint8, device=DEV))):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(bl.BitLinearError):
+        bl.layernorm(x, w, b, eps=0.0)

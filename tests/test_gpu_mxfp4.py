@@ -1,0 +1,238 @@
+"""MXFP4 on the GPU against the plain 64-bit forms: codes, scales and values bit for bit, products
+within a bound on fp32 sums (and bit for bit where every partial sum is an fp32 number)."""
+import numpy as np
+import pytest
+import torch
+
+import bitlinear_fwd_amd as bl
+import mxfp4_reference as ref
+from gpu_helpers import acts_host_f32, check_equal, host
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def outliers(m, k, seed, dtype=torch.float32):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    x = torch.randn((m, k), generator=g, device=DEV)
+    return torch.where(torch.rand((m, k), generator=g, device=DEV) < 0.01, x * 30, x).to(dtype)
+
+
+def check_quantized(x):
+    r, k = x.shape
+    codes = torch.full((bl.mxfp4_codes_bytes(r, k) + 64,), 0xA5, dtype=torch.uint8, device=DEV)
+    scales = torch.full((bl.mxfp4_scales_bytes(r, k) + 64,), 0xA5, dtype=torch.uint8, device=DEV)
+    _, _, values = bl.quantize_mxfp4(x, codes=codes, scales=scales, want_values=True)
+    plain = bl.quantize_mxfp4(x)
+    q, s, v = ref.quantize(acts_host_f32(x))
+    want, wsc = ref.pack(q, s, k)
+    check_equal(host(codes)[:want.size], want, "codes")
+    check_equal(host(scales)[:wsc.size], wsc, "scales")
+    assert (host(codes)[want.size:] == 0xA5).all() and (host(scales)[wsc.size:] == 0xA5).all()
+    check_equal(host(plain[0]), want, "codes without values")
+    check_equal(host(plain[1]), wsc, "scales without values")
+    got = acts_host_f32(values).astype(np.float64)
+    assert values.dtype == x.dtype
+    check_equal(np.isnan(got), np.isnan(v), "NaN values")
+    check_equal(np.nan_to_num(got), np.nan_to_num(v), "values")
+    check_equal(np.signbit(got) & ~np.isnan(got), np.signbit(v) & ~np.isnan(v), "signs")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("r,k", [(1, 1), (1, 31), (3, 32), (16, 128), (17, 129), (15, 511), (33, 513), (5, 1000),
+                                 (64, 2560), (2, 6912), (37, 7001)])
+def test_quantize(r, k, dtype):
+    print(f"case: quantize_mxfp4 R={r} K={k} {dtype}", flush=True)
+    check_quantized(outliers(r, k, seed=r + k, dtype=DT[dtype]))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_quantize_wide_range_and_nonfinite(dtype):
+    """Blocks over the whole exponent range (subnormals and the largest numbers), zero rows, signed
+    zeros, and blocks with a NaN or an infinity among finite ones."""
+    g = np.random.default_rng(3)
+    x = (g.normal(size=(40, 160)) * np.exp2(g.integers(-150, 127, size=(40, 5)).repeat(32, 1))).astype(np.float32)
+    x[0] = 0.0
+    x[1] = -0.0
+    x[2, 7], x[3, 40], x[4, 100] = np.nan, np.inf, -np.inf
+    x[5, :32] = 3.4e38
+    x[6, :32] = 1e-45
+    x[7, :64] = np.float32(2.0 ** -126)
+    check_quantized(torch.from_numpy(x).to(DEV).to(DT[dtype]))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_quantize_borders(dtype):
+    """Magnitudes at, just under and just over every border between neighbouring grid values, at
+    several scales, in blocks whose largest magnitude fixes the scale."""
+    rows = []
+    for e in (-120, -3, 0, 1, 90):
+        for border in (0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0, 7.0):
+            v = torch.tensor([border], dtype=DT[dtype])
+            bits = v.view(torch.int16 if dtype == "bf16" else torch.int32)
+            near = torch.cat([(bits + d).view(DT[dtype]) for d in (-1, 0, 1)]).float()
+            row = torch.zeros(32)
+            row[:3], row[3:6], row[31] = near, -near, 4.0
+            rows.append(torch.ldexp(row, torch.tensor(e)))
+    check_quantized(torch.stack(rows).to(DT[dtype]).to(DEV))
+
+
+def test_quantize_every_bf16_value():
+    """Every bf16 bit pattern, 31 of them and one fixed magnitude to a block."""
+    bits = np.arange(65536, dtype=np.uint32)
+    pad = np.zeros(-(-65536 // 31) * 31, dtype=np.uint32)
+    pad[:65536] = bits
+    rows = np.zeros((len(pad) // 31, 32), dtype=np.uint32)
+    rows[:, :31] = pad.reshape(-1, 31)
+    rows[:, 31] = 0x40C0  # 6.0
+    x = torch.from_numpy(rows.astype(np.uint16).view(np.int16)).view(torch.bfloat16).to(DEV)
+    check_quantized(x)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_quantize_unaligned_source(dtype):
+    """A source that starts at an odd element of its storage."""
+    flat = outliers(1, 1 + 19 * 333, seed=9, dtype=DT[dtype]).view(-1)
+    check_quantized(flat[1:].view(19, 333))
+
+
+def product_bound(xv, wv, k):
+    """|error| of an fp32 sum of the K exact products: every product is an fp32 number times powers
+    of two; each matrix instruction adds 128 of them to its accumulator, off by at most 2^-22 of the
+    magnitudes it adds, ceil(K / 128) of them in a chain, then up to 16 partial sums."""
+    return (-(-k // 128) + 20) * 2.0 ** -22 * (np.abs(xv) @ np.abs(wv).T)
+
+
+def check_product(y, xv, wv, k):
+    want = xv @ wv.T
+    got = acts_host_f32(y).astype(np.float64)
+    tol = product_bound(xv, wv, k)
+    if y.dtype == torch.bfloat16:
+        tol = tol + 2.0 ** -8 * (np.abs(want) + tol)
+    bad = ~(np.abs(got - want) <= tol)
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4].tolist(), got[bad][:4], want[bad][:4])
+
+
+def quantized(x):
+    """Codes and scales from the GPU quantiser, the values from the plain form."""
+    codes, scales = bl.quantize_mxfp4(x)
+    return codes, scales, ref.quantize(acts_host_f32(x))[2]
+
+
+PRODUCTS = [(1, 16, 32), (1, 1, 1), (2, 17, 33), (1, 6912, 2560), (3, 100, 513), (8, 640, 2560), (15, 333, 1000),
+            (16, 2560, 6912), (17, 64, 128), (31, 50, 640), (33, 1003, 777), (48, 48, 4096), (64, 2560, 2560),
+            (65, 96, 256), (100, 1000, 1500), (128, 256, 512), (200, 130, 2570), (257, 515, 1029), (300, 1024, 2048)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("m,n,k", PRODUCTS)
+def test_forward(m, n, k, dtype):
+    print(f"case: forward_mxfp4 M={m} N={n} K={k} {dtype}", flush=True)
+    x, w = outliers(m, k, seed=m + 1, dtype=DT[dtype]), outliers(n, k, seed=n + 2) * 0.02
+    xc, xs, xv = quantized(x)
+    wc, ws, wv = quantized(w)
+    y = torch.full((m + 2, n), 777.0, dtype=DT[dtype], device=DEV)
+    bl.forward_mxfp4(wc, ws, xc, xs, m, n, k, y=y[:m])
+    check_product(y[:m], xv, wv, k)
+    assert (y[m:] == 777.0).all()  # rows behind the last token are left alone
+    f = bl.forward_mxfp4_fused(wc, ws, x, n, k, out_dtype=DT[dtype])
+    check_product(f, xv, wv, k)
+    again = bl.forward_mxfp4_fused(wc, ws, x, n, k, out_dtype=DT[dtype])
+    assert torch.equal(f, again)
+
+
+def grid_matrix(r, k, seed, shift=0):
+    """Values on the grid times 2^shift, a 4 or a 6 in every block: quantised without error."""
+    g = np.random.default_rng(seed)
+    v = g.choice(ref.GRID, size=(r, k)) * g.choice([-1.0, 1.0], size=(r, k))
+    v[:, ::32] = g.choice([4.0, -6.0], size=v[:, ::32].shape)
+    return torch.from_numpy((v * 2.0 ** shift).astype(np.float32)).to(DEV)
+
+
+@pytest.mark.parametrize("m,n,k", PRODUCTS + [(5, 40, 28672), (70, 90, 28672), (150, 70, 4100)])
+def test_forward_exact_sums(m, n, k):
+    """All scales equal and every partial sum a multiple of 1/4 below 2^22: the product is exact, so
+    any wrong element, scale or index shows."""
+    print(f"case: forward_mxfp4 exact M={m} N={n} K={k}", flush=True)
+    x, w = grid_matrix(m, k, m), grid_matrix(n, k, n + 1, shift=-5)
+    wc, ws = bl.quantize_mxfp4(w)
+    xc, xs = bl.quantize_mxfp4(x)
+    want = host(x).astype(np.float64) @ host(w).astype(np.float64).T
+    check_equal(host(bl.forward_mxfp4(wc, ws, xc, xs, m, n, k)).astype(np.float64), want, "y")
+    check_equal(host(bl.forward_mxfp4_fused(wc, ws, x, n, k)).astype(np.float64), want, "fused y")
+    xb = x.to(torch.bfloat16)  # grid values are bf16 numbers
+    check_equal(host(bl.forward_mxfp4_fused(wc, ws, xb, n, k)).astype(np.float64), want, "fused bf16 y")
+
+
+@pytest.mark.parametrize("m", [1, 7, 16, 20, 64, 130])
+def test_forward_block_scales(m):
+    """One block per row pair at its own power of two: each output is one product of scales."""
+    k, n = 640, 48
+    x = torch.zeros((m, k), device=DEV)
+    w = torch.zeros((n, k), device=DEV)
+    for i in range(m):
+        x[i, 32 * (i % 20):32 * (i % 20) + 32] = 2.0 ** (i % 60 - 30)
+    for j in range(n):
+        w[j] = torch.tensor([2.0 ** ((j + b) % 40 - 20) for b in range(20)], device=DEV).repeat_interleave(32)
+    wc, ws = bl.quantize_mxfp4(w)
+    want = host(x).astype(np.float64) @ host(w).astype(np.float64).T
+    check_equal(host(bl.forward_mxfp4_fused(wc, ws, x, n, k)).astype(np.float64), want, "y")
+
+
+@pytest.mark.parametrize("m", [1, 4, 16, 40, 100, 200])
+def test_forward_nonfinite(m):
+    """A NaN or an infinity spoils its token's row of the output, or its weight's column, and
+    nothing else."""
+    n, k = 70, 600
+    x, w = grid_matrix(m, k, 5), grid_matrix(n, k, 6)
+    clean = bl.forward_mxfp4_fused(*bl.quantize_mxfp4(w), x, n, k)
+    x[m - 1, 599] = float("inf")
+    w[33, 64] = float("nan")
+    wc, ws = bl.quantize_mxfp4(w)
+    for y in (bl.forward_mxfp4_fused(wc, ws, x, n, k), bl.forward_mxfp4(wc, ws, *bl.quantize_mxfp4(x), m, n, k)):
+        bad = torch.zeros((m, n), dtype=torch.bool, device=DEV)
+        bad[m - 1], bad[:, 33] = True, True
+        assert torch.equal(torch.isnan(y), bad)
+        assert torch.equal(y[~bad], clean[~bad])
+
+
+def test_forward_zero_rows_and_large_scales():
+    """All-zero tokens give zeros; scales at both ends of their range cancel."""
+    n, k = 33, 256
+    w = torch.full((n, k), 2.0 ** -100, device=DEV)
+    x = torch.zeros((3, k), device=DEV)
+    x[1] = 2.0 ** 100
+    x[2] = -(2.0 ** 90)
+    y = host(bl.forward_mxfp4_fused(*bl.quantize_mxfp4(w), x, n, k))
+    assert (y[0] == 0).all() and (y[1] == k).all() and (y[2] == -k / 1024).all()
+
+
+def test_forward_argument_errors():
+    w, x = torch.randn(32, 256, device=DEV), torch.randn(4, 256, device=DEV)
+    wc, ws = bl.quantize_mxfp4(w)
+    xc, xs = bl.quantize_mxfp4(x)
+    with pytest.raises(ValueError):
+        bl.forward_mxfp4(wc[:-1], ws, xc, xs, 4, 32, 256)
+    with pytest.raises(ValueError):
+        bl.forward_mxfp4(wc, ws, xc, xs, 17, 32, 256)
+    with pytest.raises(ValueError):
+        bl.forward_mxfp4(wc, ws, xc, xs, 4, 32, 256, out_dtype=torch.float16)
+    with pytest.raises(ValueError):
+        bl.forward_mxfp4(wc, ws, xc, xs, 4, 32, 256, y=torch.empty(4, 33, device=DEV))
+    with pytest.raises(ValueError):
+        bl.forward_mxfp4_fused(wc, ws, x.half(), 32, 256)
+    with pytest.raises(ValueError):
+        bl.forward_mxfp4_fused(wc, ws, x.t(), 32, 4)
+    with pytest.raises(ValueError):
+        bl.forward_mxfp4_fused(wc, ws, x, 32, 255)
+    with pytest.raises(ValueError):
+        bl.quantize_mxfp4(x[:, ::2])
+    with pytest.raises(ValueError):
+        bl.quantize_mxfp4(x[:0])
+    with pytest.raises(bl.BitLinearError):
+        bl.forward_mxfp4(wc, ws, xc, xs, 0, 32, 256)
+    with pytest.raises(ValueError):  # a workspace that is too small
+        bl.forward_mxfp4_fused(wc, ws, torch.randn(700, 256, device=DEV), 32, 256,
+                               workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
