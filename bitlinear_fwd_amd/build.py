@@ -13,7 +13,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libbitlinear.so")
 SOURCES = ["bitlinear_api.hip", "weight_quant.hip", "act_quant.hip", "gemv.hip", "gemv_lut.hip", "gemv_bin.hip",
-           "gemm.hip", "probes.hip", "mxfp4_quant.hip", "mxfp4_decode.hip", "layernorm.hip"]
+           "gemm.hip", "probes.hip", "mxfp4_quant.hip", "mxfp4_decode.hip",
+           "mxfp4_gemm.hip", "layernorm.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

@@ -30,6 +30,14 @@ bool rows_ok(int64_t R, int64_t K) { return R >= 1 && K >= 1 && R < kMaxDim && K
 // eps of the sub-layer normalisation: finite and >= 0 (NaN fails both comparisons)
 bool eps_ok(float eps) { return eps >= 0.0f && eps <= 3.4028234663852886e38f; }
 
+constexpr int kMxDecodeMaxM = 64;  // tokens of an MXFP4 product that the decode kernel takes
+hipError_t mx_forward(const uint8_t* codes, const uint8_t* scales, const uint8_t* xcodes, const uint8_t* xscales,
+                      int64_t M, int64_t N, int64_t K, void* Y, int ydt, hipStream_t s) {
+  return M <= kMxDecodeMaxM
+             ? bl::launch_mx_decode(codes, scales, xcodes, xscales, M, N, K, Y, ydt == BL_BF16, s)
+             : bl::launch_mx_gemm(codes, scales, xcodes, xscales, M, N, K, Y, ydt == BL_BF16, s);
+}
+
 // Sizes of an MXFP4 product: both matrices addressable, and a launchable number of tiles.
 bool mx_product_ok(int64_t M, int64_t N, int64_t K) {
   return M <= kMaxCount / K && N <= kMaxCount / K && bl::mx_row_blocks(M) <= (int64_t(1) << 30) / bl::mx_row_blocks(N);
@@ -160,8 +168,8 @@ int bitlinear_forward_mxfp4(const uint8_t* codes, const uint8_t* scales, const u
   if (!aligned(codes, 16) || !aligned(scales, 4) || !aligned(xcodes, 16) || !aligned(xscales, 4) ||
       !aligned(Y, dtype_align(ydt)))
     return BL_ERR_INVALID_ARG;
-  return hip_status(bl::launch_mx_decode(codes, scales, xcodes, xscales, M, N, K, Y, ydt == BL_BF16,
-                                         static_cast<hipStream_t>(stream)));
+  return hip_status(
+      mx_forward(codes, scales, xcodes, xscales, M, N, K, Y, ydt, static_cast<hipStream_t>(stream)));
 }
 
 int64_t bitlinear_forward_mxfp4_fused_ws_bytes(int64_t M, int64_t N, int64_t K, int dt) {
@@ -183,7 +191,7 @@ int bitlinear_forward_mxfp4_fused(const uint8_t* codes, const uint8_t* scales, c
   uint8_t* xscales = xcodes + bl::mx_codes_bytes(M, K);
   const hipError_t e = bl::launch_mx_quant(X, dt == BL_BF16, M, K, xcodes, xscales, nullptr, s);
   if (e != hipSuccess) return BL_ERR_HIP;
-  return hip_status(bl::launch_mx_decode(codes, scales, xcodes, xscales, M, N, K, Y, ydt == BL_BF16, s));
+  return hip_status(mx_forward(codes, scales, xcodes, xscales, M, N, K, Y, ydt, s));
 }
 
 int bitlinear_layernorm(const void* X, int dt, int64_t M, int64_t K, const float* weight, const float* bias,

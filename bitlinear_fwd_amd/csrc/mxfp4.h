@@ -125,4 +125,14 @@ struct MxDecodePlan {
 };
 MxDecodePlan plan_mx_decode(int64_t M, int64_t N, int64_t K);
 
+// Launch plan of the GEMM: square output tiles.
+struct MxGemmPlan {
+  int64_t side = 256;  // 256 or 128
+  int64_t tiles_m = 0, tiles_n = 0;
+};
+MxGemmPlan plan_mx_gemm(int64_t M, int64_t N, int64_t K);
+hipError_t launch_mx_gemm(const uint8_t* codes, const uint8_t* scales, const uint8_t* xcodes,
+                          const uint8_t* xscales, int64_t M, int64_t N, int64_t K, void* Y, int ybf16,
+                          hipStream_t s);
+
 }  // namespace bl
