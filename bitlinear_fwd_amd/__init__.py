@@ -906,45 +906,51 @@ class BitLinear:
         return y
 
 
+# The calls below take a few microseconds of host time each, so their checks read every attribute
+# once and allocate nothing that the caller has given.
+
+
 def _dtype_code(t, name: str) -> int:
     import torch
 
-    if t == torch.float32:
-        return BL_F32
     if t == torch.bfloat16:
         return BL_BF16
+    if t == torch.float32:
+        return BL_F32
     raise ValueError(f"{name} must be float32 or bfloat16")
 
 
-def _buffer(t, name: str, shape, dtype, dev):
-    """`t` checked to be a contiguous tensor of this shape, type and device, or a new one."""
-    import torch
-
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    if t.device != dev or t.dtype != dtype or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}")
+def _given(t, name: str, shape, dtype, index: int):
+    """`t`, an output or vector given by the caller, checked: contiguous, of this shape (a
+    tuple), type and device."""
+    if t.get_device() != index or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on cuda:{index}")
     return t
 
 
-def _bytes_at_least(t, name: str, nbytes: int, dev):
-    """`t` checked to be a contiguous uint8 tensor of at least nbytes on dev."""
+def _bytes_at_least(t, name: str, nbytes: int, index: int) -> int:
+    """The address of `t`, checked to be a contiguous uint8 tensor of at least nbytes on the
+    device."""
     import torch
 
-    if t.device != dev or t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() < nbytes:
-        raise ValueError(f"{name} must be a contiguous uint8 tensor of at least {nbytes} bytes on {dev}")
+    if t.get_device() != index or t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() < nbytes:
+        raise ValueError(f"{name} must be a contiguous uint8 tensor of at least {nbytes} bytes on cuda:{index}")
+    return t.data_ptr()
 
 
-def _call(fn: str, dev, *args) -> None:
-    """The library call on dev's current stream, with dev the current device."""
+def _call(fn: str, index: int, *args) -> None:
+    """The library call on the device's current stream, with the device the current one."""
     import torch
 
-    if torch.cuda.current_device() == dev.index:
-        st = getattr(lib(), fn)(*args, _stream(dev))
+    f = getattr(_lib or lib(), fn)
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if torch._C._cuda_getDevice() == index:
+        st = f(*args, stream)
     else:
-        with torch.cuda.device(dev):
-            st = getattr(lib(), fn)(*args, _stream(dev))
-    _check(fn, st)
+        with torch.cuda.device(index):
+            st = f(*args, stream)
+    if st != BL_OK:
+        _check(fn, st)
 
 
 def _ptr(t):
@@ -953,7 +959,10 @@ def _ptr(t):
 
 def _require_rows(t, name: str) -> int:
     """A contiguous GPU matrix of fp32 or bf16 rows; returns its bl_dtype."""
-    _require_cuda(t, name)
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
     if t.numel() == 0:
@@ -963,12 +972,12 @@ def _require_rows(t, name: str) -> int:
 
 def mxfp4_codes_bytes(rows: int, k: int) -> int:
     """Bytes of the MXFP4 codes of a rows x k matrix (16-row x 128-column tiles of 1024 bytes)."""
-    return -(-rows // 16) * -(-k // 128) * 1024 if rows >= 1 and k >= 1 else -1
+    return ((rows + 15) >> 4) * ((k + 127) >> 7) << 10 if rows >= 1 and k >= 1 else -1
 
 
 def mxfp4_scales_bytes(rows: int, k: int) -> int:
     """Bytes of the MXFP4 block scales of a rows x k matrix."""
-    return -(-rows // 16) * -(-k // 512) * 256 if rows >= 1 and k >= 1 else -1
+    return ((rows + 15) >> 4) * ((k + 511) >> 9) << 8 if rows >= 1 and k >= 1 else -1
 
 
 def quantize_mxfp4(x, codes=None, scales=None, values=None, want_values: bool = False):
@@ -982,38 +991,47 @@ def quantize_mxfp4(x, codes=None, scales=None, values=None, want_values: bool = 
 
     dt = _require_rows(x, "x")
     r, k = x.shape
-    dev = x.device
+    dev = x.get_device()
     nc, ns = mxfp4_codes_bytes(r, k), mxfp4_scales_bytes(r, k)
     if codes is None:
-        codes = torch.empty(nc, dtype=torch.uint8, device=dev)
-    _bytes_at_least(codes, "codes", nc, dev)
+        codes = torch.empty(nc, dtype=torch.uint8, device=x.device)
     if scales is None:
-        scales = torch.empty(ns, dtype=torch.uint8, device=dev)
-    _bytes_at_least(scales, "scales", ns, dev)
-    if want_values or values is not None:
-        values = _buffer(values, "values", (r, k), x.dtype, dev)
-    _call("bitlinear_quantize_mxfp4", dev, x.data_ptr(), dt, r, k, codes.data_ptr(), scales.data_ptr(), _ptr(values))
+        scales = torch.empty(ns, dtype=torch.uint8, device=x.device)
+    if values is not None:
+        _given(values, "values", (r, k), x.dtype, dev)
+    elif want_values:
+        values = torch.empty_like(x)
+    _call("bitlinear_quantize_mxfp4", dev, x.data_ptr(), dt, r, k, _bytes_at_least(codes, "codes", nc, dev),
+          _bytes_at_least(scales, "scales", ns, dev), _ptr(values))
     return (codes, scales, values) if values is not None else (codes, scales)
+
+
+def _product_output(y, out_dtype, m: int, n: int, like):
+    """(y, its bl_dtype) of a product: the caller's or a new one on like's device."""
+    import torch
+
+    if y is not None:
+        dtype = out_dtype or y.dtype
+        ydt = _dtype_code(dtype, "out_dtype")
+        return _given(y, "y", (m, n), dtype, like.get_device()), ydt
+    dtype = out_dtype or torch.float32
+    ydt = _dtype_code(dtype, "out_dtype")
+    return torch.empty((max(m, 0), max(n, 0)), dtype=dtype, device=like.device), ydt
 
 
 def forward_mxfp4(codes, scales, xcodes, xscales, m: int, n: int, k: int, y=None, out_dtype=None):
     """y[M][N] = Xv Wv^T of MXFP4 activations (xcodes, xscales: M rows) and weights (codes,
     scales: N rows), both of K columns, accumulated in fp32; y in ``out_dtype`` (fp32, or
     bf16), or in that of the given ``y``."""
-    import torch
-
-    dev = codes.device
-    for t, name in ((codes, "codes"), (scales, "scales"), (xcodes, "xcodes"), (xscales, "xscales")):
-        _require_cuda(t, name)
-    _bytes_at_least(codes, "codes", mxfp4_codes_bytes(n, k), dev)
-    _bytes_at_least(scales, "scales", mxfp4_scales_bytes(n, k), dev)
-    _bytes_at_least(xcodes, "xcodes", mxfp4_codes_bytes(m, k), dev)
-    _bytes_at_least(xscales, "xscales", mxfp4_scales_bytes(m, k), dev)
-    out_dtype = out_dtype or (y.dtype if y is not None else torch.float32)
-    ydt = _dtype_code(out_dtype, "out_dtype")
-    y = _buffer(y, "y", (max(m, 0), max(n, 0)), out_dtype, dev)
-    _call("bitlinear_forward_mxfp4", dev, codes.data_ptr(), scales.data_ptr(), xcodes.data_ptr(), xscales.data_ptr(),
-          m, n, k, y.data_ptr(), ydt)
+    dev = codes.get_device()
+    if dev < 0:
+        raise ValueError("codes must be a GPU tensor")
+    ptrs = (_bytes_at_least(codes, "codes", mxfp4_codes_bytes(n, k), dev),
+            _bytes_at_least(scales, "scales", mxfp4_scales_bytes(n, k), dev),
+            _bytes_at_least(xcodes, "xcodes", mxfp4_codes_bytes(m, k), dev),
+            _bytes_at_least(xscales, "xscales", mxfp4_scales_bytes(m, k), dev))
+    y, ydt = _product_output(y, out_dtype, m, n, codes)
+    _call("bitlinear_forward_mxfp4", dev, *ptrs, m, n, k, y.data_ptr(), ydt)
     return y
 
 
@@ -1032,35 +1050,21 @@ def forward_mxfp4_fused(codes, scales, x, n: int, k: int, y=None, workspace=None
     import torch
 
     dt = _require_rows(x, "x")
+    m = x.shape[0]
     if x.shape[1] != k:
         raise ValueError("x must be [tokens, K]")
-    m = x.shape[0]
-    dev = x.device
-    _require_cuda(codes, "codes")
-    _require_cuda(scales, "scales")
-    _bytes_at_least(codes, "codes", mxfp4_codes_bytes(n, k), dev)
-    _bytes_at_least(scales, "scales", mxfp4_scales_bytes(n, k), dev)
-    out_dtype = out_dtype or (y.dtype if y is not None else torch.float32)
-    ydt = _dtype_code(out_dtype, "out_dtype")
-    y = _buffer(y, "y", (m, max(n, 0)), out_dtype, dev)
-    need = max(0, int(lib().bitlinear_forward_mxfp4_fused_ws_bytes(m, n, k, dt)))
+    dev = x.get_device()
+    wc = _bytes_at_least(codes, "codes", mxfp4_codes_bytes(n, k), dev)
+    ws = _bytes_at_least(scales, "scales", mxfp4_scales_bytes(n, k), dev)
+    y, ydt = _product_output(y, out_dtype, m, n, x)
+    need = (_lib or lib()).bitlinear_forward_mxfp4_fused_ws_bytes(m, n, k, dt)
     if workspace is not None:
         _bytes_at_least(workspace, "workspace", need, dev)
-    elif need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _call("bitlinear_forward_mxfp4_fused", dev, codes.data_ptr(), scales.data_ptr(), x.data_ptr(), dt, m, n, k,
-          y.data_ptr(), ydt, _ptr(workspace), workspace.numel() if workspace is not None else 0)
+    elif need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    _call("bitlinear_forward_mxfp4_fused", dev, wc, ws, x.data_ptr(), dt, m, n, k, y.data_ptr(), ydt,
+          _ptr(workspace), workspace.numel() if workspace is not None else 0)
     return y
-
-
-def _vector(t, name: str, n: int, dev):
-    """`t` (may be None) checked to be a contiguous fp32 vector of n elements on dev."""
-    import torch
-
-    if t is not None and (t.device != dev or t.dtype != torch.float32 or not t.is_contiguous() or
-                          tuple(t.shape) != (n,)):
-        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {(n,)} on {dev}")
-    return t
 
 
 def layernorm(x, weight=None, bias=None, eps: float = 1e-5, y=None, mean=None, rstd=None):
@@ -1070,12 +1074,14 @@ def layernorm(x, weight=None, bias=None, eps: float = 1e-5, y=None, mean=None, r
 
     dt = _require_rows(x, "x")
     m, k = x.shape
-    dev = x.device
-    _vector(weight, "weight", k, dev)
-    _vector(bias, "bias", k, dev)
-    y = _buffer(y, "y", (m, k), x.dtype, dev)
-    mean = _buffer(mean, "mean", (m,), torch.float32, dev)
-    rstd = _buffer(rstd, "rstd", (m,), torch.float32, dev)
+    dev, f32 = x.get_device(), torch.float32
+    if weight is not None:
+        _given(weight, "weight", (k,), f32, dev)
+    if bias is not None:
+        _given(bias, "bias", (k,), f32, dev)
+    y = torch.empty_like(x) if y is None else _given(y, "y", (m, k), x.dtype, dev)
+    mean = torch.empty(m, dtype=f32, device=x.device) if mean is None else _given(mean, "mean", (m,), f32, dev)
+    rstd = torch.empty(m, dtype=f32, device=x.device) if rstd is None else _given(rstd, "rstd", (m,), f32, dev)
     _call("bitlinear_layernorm", dev, x.data_ptr(), dt, m, k, _ptr(weight), _ptr(bias), eps, y.data_ptr(),
           mean.data_ptr(), rstd.data_ptr())
     return y, mean, rstd
@@ -1099,25 +1105,27 @@ def layernorm_backward(dy, x, weight, mean, rstd, dx=None, dweight=None, dbias=N
 
     dt = _require_rows(x, "x")
     m, k = x.shape
-    dev = x.device
-    if _require_rows(dy, "dy") != dt or dy.shape != x.shape or dy.device != dev:
-        raise ValueError("dy must have x's shape, type and device")
-    _vector(weight, "weight", k, dev)
+    dev, f32 = x.get_device(), torch.float32
     if mean is None or rstd is None:
         raise ValueError("mean and rstd of the forward call are needed")
-    _vector(mean, "mean", m, dev)
-    _vector(rstd, "rstd", m, dev)
-    dx = _buffer(dx, "dx", (m, k), x.dtype, dev)
+    _given(dy, "dy", (m, k), x.dtype, dev)
+    _given(mean, "mean", (m,), f32, dev)
+    _given(rstd, "rstd", (m,), f32, dev)
+    if weight is not None:
+        _given(weight, "weight", (k,), f32, dev)
+    dx = torch.empty_like(x) if dx is None else _given(dx, "dx", (m, k), x.dtype, dev)
     if want_params:
-        dweight = _buffer(dweight, "dweight", (k,), torch.float32, dev)
-        dbias = _buffer(dbias, "dbias", (k,), torch.float32, dev)
-        need = max(0, int(lib().bitlinear_layernorm_backward_ws_bytes(m, k)))
+        dweight = (torch.empty(k, dtype=f32, device=x.device) if dweight is None
+                   else _given(dweight, "dweight", (k,), f32, dev))
+        dbias = (torch.empty(k, dtype=f32, device=x.device) if dbias is None
+                 else _given(dbias, "dbias", (k,), f32, dev))
+        need = (_lib or lib()).bitlinear_layernorm_backward_ws_bytes(m, k)
         if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = torch.empty(max(need, 0), dtype=torch.uint8, device=x.device)
         else:
             _bytes_at_least(workspace, "workspace", need, dev)
     else:
-        dweight = dbias = None
+        dweight = dbias = workspace = None
     _call("bitlinear_layernorm_backward", dev, dy.data_ptr(), x.data_ptr(), dt, m, k, _ptr(weight), mean.data_ptr(),
           rstd.data_ptr(), dx.data_ptr(), _ptr(dweight), _ptr(dbias), _ptr(workspace),
           workspace.numel() if workspace is not None else 0)

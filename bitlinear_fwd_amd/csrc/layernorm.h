@@ -10,8 +10,9 @@ hipError_t launch_layernorm(const void* X, int bf16, int64_t M, int64_t K, const
 // Launch plan of the backward pass: how many partial rows of the weight and bias gradients the
 // first launch writes, and the bytes they take.
 struct LnBwdPlan {
-  int lanes = 0;        // threads that share a row: 64, 256, or 0 for the long-row form
-  int groups = 0;       // groups of 8 elements per thread (row form)
+  int rows = 0;         // rows of a workgroup at once (0: the long-row form)
+  int threads = 0;      // that share a row
+  int groups = 0;       // of 8 elements per thread
   int64_t wgs = 0;      // workgroups of the first launch
   int64_t parts = 0;    // partial rows
   int64_t ws_bytes = 0;

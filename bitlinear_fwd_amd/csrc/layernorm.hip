@@ -23,68 +23,156 @@
 namespace bl {
 namespace {
 
-constexpr int kMaxGroups = 4;          // groups of 8 elements a thread holds
-constexpr int64_t kMaxGrid = 1 << 20;  // workgroups of a launch; rows beyond are walked over
+constexpr int64_t kMaxGrid = 1 << 20;    // workgroups of a launch; rows beyond are walked over
+constexpr int64_t kCUs = 256;
+constexpr int kFewRows = 4;
 
-// Sum of each v[] over the kTh threads that share a row; every thread gets it.  64 threads are a
-// wave; more are the whole workgroup, through LDS (red: kN values per wave).
+// Sum of each v[] over the threads that share a row; every thread gets it.  kTh 64: a wave.  Else
+// through LDS (red: kN values per wave of the row), with all threads of the workgroup taking part:
+// kTh threads, or kTh -1: `threads` of them, this one the i0-th.
 template <int kTh, int kN, typename F>
-__device__ __forceinline__ void row_sum(F (&v)[kN], F* red) {
+__device__ __forceinline__ void row_sum(F (&v)[kN], F* red, int i0 = threadIdx.x, int threads = kTh) {
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) {
 #pragma unroll
     for (int j = 0; j < kN; ++j) v[j] += __shfl_xor(v[j], off, 64);
   }
-  if constexpr (kTh > 64) {
+  if constexpr (kTh != 64) {
     __syncthreads();  // the values of the sum before have been read
     if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-      for (int j = 0; j < kN; ++j) red[(threadIdx.x >> 6) * kN + j] = v[j];
+      for (int j = 0; j < kN; ++j) red[(i0 >> 6) * kN + j] = v[j];
     }
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < kN; ++j) {
-      v[j] = red[j];
+    for (int j = 0; j < kN; ++j) v[j] = red[j];
+#pragma unroll 4
+    for (int w = 1; w < threads >> 6; ++w) {
 #pragma unroll
-      for (int w = 1; w < kTh / 64; ++w) v[j] += red[w * kN + j];
+      for (int j = 0; j < kN; ++j) v[j] += red[w * kN + j];
     }
   }
 }
 
-// kTh threads per row, kG groups of 8 elements per thread (thread i takes group i, i + kTh, ...).
-template <typename T, int kTh, int kG>
-__global__ __launch_bounds__(kTh == 64 ? 256 : kTh) void k_layernorm(const T* __restrict__ X, int64_t M, int64_t K,
-                                                                     const float* __restrict__ weight,
-                                                                     const float* __restrict__ bias, float eps,
-                                                                     T* __restrict__ Y, float* __restrict__ mean_out,
-                                                                     float* __restrict__ rstd_out) {
-  __shared__ float red[kTh / 64];
-  constexpr int kRows = kTh == 64 ? 4 : 1;  // rows of a workgroup
-  const int i0 = kTh == 64 ? (threadIdx.x & 63) : threadIdx.x;
-  for (int64_t row = (int64_t)blockIdx.x * kRows + (kTh == 64 ? threadIdx.x >> 6 : 0); row < M;
-       row += (int64_t)gridDim.x * kRows) {
-    float v[kG][8];
-    float sum[1] = {0.0f};
+// Eight elements as they are in memory, so that the next row's loads can be in flight while this
+// one is worked on: widen8 makes fp32 of them.
+template <typename T>
+struct Raw8 {
+  uint32_t w[2 * sizeof(T)];
+};
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_raw8(const T* p, int64_t n) {
+  Raw8<T> r;
+  if (n >= 8) {
+    __builtin_memcpy(r.w, p, 8 * sizeof(T));
+  } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.w[i] = i < n ? __float_as_uint(p[i]) : 0u;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      r.w[i] = (2 * i < n ? (uint32_t)p[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)p[2 * i + 1] << 16 : 0u);
+  }
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void widen8(const Raw8<T>& r, float (&v)[8]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r.w[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(r.w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(r.w[i] & 0xffff0000u);
+    }
+  }
+}
+
+// store8 past the caches: for outputs larger than they hold.
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+typedef v4u v4u_unaligned __attribute__((aligned(2)));
+template <typename T>
+__device__ __forceinline__ void stream8(T* p, int64_t n, const float (&v)[8]) {
+  if (n < 8) {
+    store8(p, n, v);
+  } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      v4u w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(v[4 * h + i]);
+      __builtin_nontemporal_store(w, reinterpret_cast<v4u_unaligned*>(p + 4 * h));
+    }
+  } else {
+    v4u w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = bf16_bits(v[2 * i]) | bf16_bits(v[2 * i + 1]) << 16;
+    __builtin_nontemporal_store(w, reinterpret_cast<v4u_unaligned*>(p));
+  }
+}
+
+// One row per wave (kWave) or per workgroup, kG groups of 8 elements per thread (thread i of the T
+// that share the row takes groups i, i + T, ...).  A workgroup walks over rows with the next row's
+// loads in flight and (kHold) weight and bias in registers: read for every row they are four
+// times a bf16 row's bytes.
+template <typename T, bool kWave, int kG, bool kHold>
+__global__ __launch_bounds__(kWave ? 256 : 1024) void k_layernorm(const T* __restrict__ X, int64_t M, int64_t K,
+                                                                  const float* __restrict__ weight,
+                                                                  const float* __restrict__ bias, float eps,
+                                                                  T* __restrict__ Y, float* __restrict__ mean_out,
+                                                                  float* __restrict__ rstd_out) {
+  __shared__ float red[16];
+  constexpr int kTh = kWave ? 64 : -1;
+  const int threads = kWave ? 64 : blockDim.x;
+  const int i0 = kWave ? threadIdx.x & 63 : threadIdx.x;
+  const int64_t step = (int64_t)gridDim.x * (kWave ? 4 : 1);
+  int64_t row = kWave ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  Raw8<T> raw[kG];
+  auto fetch = [&](int64_t r) {
 #pragma unroll
     for (int g = 0; g < kG; ++g) {
-      const int64_t col = 8 * (int64_t)(i0 + g * kTh);
-      load8(X + row * K + col, K - col, v[g]);
+      const int64_t col = 8 * (int64_t)(i0 + g * threads);
+      raw[g] = load_raw8(X + r * K + col, r < M ? K - col : 0);
+    }
+  };
+  fetch(row);
+  float w[kG][8], b[kG][8];
+  auto params = [&](int g) {
+    const int64_t col = 8 * (int64_t)(i0 + g * threads);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      w[g][i] = 1.0f;
+      b[g][i] = 0.0f;
+    }
+    if (weight) load8(weight + col, K - col, w[g]);
+    if (bias) load8(bias + col, K - col, b[g]);
+  };
+  if constexpr (kHold) {
+#pragma unroll
+    for (int g = 0; g < kG; ++g) params(g);
+  }
+  for (; row < M; row += step) {
+    float v[kG][8], sum[1] = {0.0f}, sq[1] = {0.0f};
+#pragma unroll
+    for (int g = 0; g < kG; ++g) {
+      widen8(raw[g], v[g]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum[0] += v[g][i];
     }
-    row_sum<kTh, 1>(sum, red);
+    fetch(row + step);
+    row_sum<kTh, 1>(sum, red, i0, threads);
     const float mean = sum[0] / (float)K;
-    float sq[1] = {0.0f};
 #pragma unroll
     for (int g = 0; g < kG; ++g) {
-      const int64_t col = 8 * (int64_t)(i0 + g * kTh);
+      const int64_t col = 8 * (int64_t)(i0 + g * threads);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         v[g][i] = col + i < K ? v[g][i] - mean : 0.0f;
         sq[0] += v[g][i] * v[g][i];
       }
     }
-    row_sum<kTh, 1>(sq, red);
+    row_sum<kTh, 1>(sq, red, i0, threads);
     const float rstd = 1.0f / sqrtf(sq[0] / (float)K + eps);
     if (i0 == 0) {
       if (mean_out) mean_out[row] = mean;
@@ -92,17 +180,14 @@ __global__ __launch_bounds__(kTh == 64 ? 256 : kTh) void k_layernorm(const T* __
     }
 #pragma unroll
     for (int g = 0; g < kG; ++g) {
-      const int64_t col = 8 * (int64_t)(i0 + g * kTh);
-      float w[8], b[8];
-      if (weight) load8(weight + col, K - col, w);
-      if (bias) load8(bias + col, K - col, b);
+      const int64_t col = 8 * (int64_t)(i0 + g * threads);
+      if constexpr (!kHold) params(g);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[g][i] *= rstd;
-        if (weight) v[g][i] *= w[i];
-        if (bias) v[g][i] += b[i];
-      }
-      store8(Y + row * K + col, K - col, v[g]);
+      for (int i = 0; i < 8; ++i) v[g][i] = v[g][i] * rstd * w[g][i] + b[g][i];
+      if constexpr (kWave || kG > 1)
+        stream8(Y + row * K + col, K - col, v[g]);
+      else
+        store8(Y + row * K + col, K - col, v[g]);
     }
   }
 }
@@ -158,22 +243,21 @@ __global__ __launch_bounds__(1024) void k_layernorm_long(const T* __restrict__ X
   }
 }
 
-// One workgroup's rows: dX, and (kSums) one partial row of dw at part[p][0][K] and of db at
-// part[p][1][K], p the workgroup.
-template <typename T, int kTh, int kG, bool kSums>
-__global__ __launch_bounds__(256) void k_layernorm_bwd(const T* __restrict__ dY, const T* __restrict__ X, int64_t M,
-                                                       int64_t K, const float* __restrict__ weight,
-                                                       const float* __restrict__ mean_in,
-                                                       const float* __restrict__ rstd_in, T* __restrict__ dX,
-                                                       float* __restrict__ part) {
-  __shared__ float red[2 * (kTh / 64)];
-  constexpr int kRows = kTh == 64 ? 4 : 1;
-  const int i0 = kTh == 64 ? (threadIdx.x & 63) : threadIdx.x;
-  const int64_t walker = (int64_t)blockIdx.x * kRows + (kTh == 64 ? threadIdx.x >> 6 : 0);
+// A workgroup's rows, `rows` at once by `threads` threads each (kWave: a wave each): dX, and
+// (kSums) one partial row of dw at part[p][0][K] and of db at part[p][1][K], p the workgroup.
+template <typename T, bool kWave, int kG, bool kSums>
+__global__ __launch_bounds__(kG == 1 ? 1024 : 768) void k_layernorm_bwd(
+    const T* __restrict__ dY, const T* __restrict__ X, int64_t M, int64_t K, int rows, int threads,
+    const float* __restrict__ weight, const float* __restrict__ mean_in, const float* __restrict__ rstd_in,
+    T* __restrict__ dX, float* __restrict__ part) {
+  __shared__ float red[32];        // two values per wave
+  extern __shared__ float sums[];  // [2][8 kG][threads] where rows > 1
+  const int sub = kWave ? threadIdx.x >> 6 : threadIdx.x / threads;
+  const int i0 = kWave ? threadIdx.x & 63 : threadIdx.x - sub * threads;
   float dw[kG][8], db[kG][8], w[kG][8];
 #pragma unroll
   for (int g = 0; g < kG; ++g) {
-    const int64_t col = 8 * (int64_t)(i0 + g * kTh);
+    const int64_t col = 8 * (int64_t)(i0 + g * threads);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       dw[g][i] = 0.0f;
@@ -182,16 +266,31 @@ __global__ __launch_bounds__(256) void k_layernorm_bwd(const T* __restrict__ dY,
     }
     if (weight) load8(weight + col, K - col, w[g]);
   }
-  for (int64_t row = walker; row < M; row += (int64_t)gridDim.x * kRows) {
-    float x[kG][8], d[kG][8];
-    const float mean = mean_in[row], rstd = rstd_in[row];
-    float c[2] = {0.0f, 0.0f};
+  Raw8<T> rx[kG], rd[kG];
+  float rmean = 0.0f, rrstd = 0.0f;
+  auto fetch = [&](int64_t row) {  // rows past the last count as zeros, which add nothing to a sum
+    const bool in = row < M;
 #pragma unroll
     for (int g = 0; g < kG; ++g) {
-      const int64_t col = 8 * (int64_t)(i0 + g * kTh);
-      load8(X + row * K + col, K - col, x[g]);
-      load8(dY + row * K + col, K - col, d[g]);
+      const int64_t col = 8 * (int64_t)(i0 + g * threads), left = in ? K - col : 0;
+      rx[g] = load_raw8(X + row * K + col, left);
+      rd[g] = load_raw8(dY + row * K + col, left);
     }
+    rmean = in ? mean_in[row] : 0.0f;
+    rrstd = in ? rstd_in[row] : 0.0f;
+  };
+  const int64_t first = (int64_t)blockIdx.x * rows, step = (int64_t)gridDim.x * rows;
+  fetch(first + sub);
+  for (int64_t r0 = first; r0 < M; r0 += step) {  // the same trips for every thread: barriers inside
+    float x[kG][8], d[kG][8];
+    const float mean = rmean, rstd = rrstd;
+#pragma unroll
+    for (int g = 0; g < kG; ++g) {
+      widen8(rx[g], x[g]);
+      widen8(rd[g], d[g]);
+    }
+    fetch(r0 + step + sub);
+    float c[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int g = 0; g < kG; ++g) {
 #pragma unroll
@@ -207,46 +306,45 @@ __global__ __launch_bounds__(256) void k_layernorm_bwd(const T* __restrict__ dY,
       }
     }
     if (dX) {
-      row_sum<kTh, 2>(c, red);
+      row_sum<kWave ? 64 : -1, 2>(c, red + 2 * sub * (threads >> 6), i0, threads);
       c[0] /= (float)K;
       c[1] /= (float)K;
+      const int64_t row = r0 + sub;
 #pragma unroll
       for (int g = 0; g < kG; ++g) {
-        const int64_t col = 8 * (int64_t)(i0 + g * kTh);
+        const int64_t col = 8 * (int64_t)(i0 + g * threads);
 #pragma unroll
         for (int i = 0; i < 8; ++i) d[g][i] = rstd * (d[g][i] - c[0] - x[g][i] * c[1]);
-        store8(dX + row * K + col, K - col, d[g]);
+        store8(dX + row * K + col, row < M ? K - col : 0, d[g]);
       }
     }
   }
-  if constexpr (kSums) {
-    if constexpr (kTh == 64) {  // the four waves' sums, added in wave order: one partial row per workgroup
-      __shared__ float sums[2][kG * 8][64];
+  if constexpr (kSums) {  // the rows' sums, added in order: one partial row per workgroup
+    const int plane = 8 * kG * threads;
+    for (int v = 0; v < (rows > 1 ? rows : 0); ++v) {
+      if (sub == v) {
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        if ((int)(threadIdx.x >> 6) == v) {
+        for (int g = 0; g < kG; ++g) {
 #pragma unroll
-          for (int g = 0; g < kG; ++g) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              if (v > 0) {
-                dw[g][i] = sums[0][8 * g + i][i0] + dw[g][i];
-                db[g][i] = sums[1][8 * g + i][i0] + db[g][i];
-              }
-              if (v < 3) {
-                sums[0][8 * g + i][i0] = dw[g][i];
-                sums[1][8 * g + i][i0] = db[g][i];
-              }
+          for (int i = 0; i < 8; ++i) {
+            const int at = (8 * g + i) * threads + i0;
+            if (v > 0) {
+              dw[g][i] = sums[at] + dw[g][i];
+              db[g][i] = sums[plane + at] + db[g][i];
+            }
+            if (v < rows - 1) {
+              sums[at] = dw[g][i];
+              sums[plane + at] = db[g][i];
             }
           }
         }
-        __syncthreads();
       }
-      if (threadIdx.x < 192) return;
+      __syncthreads();
     }
+    if (sub < rows - 1) return;
 #pragma unroll
     for (int g = 0; g < kG; ++g) {
-      const int64_t col = 8 * (int64_t)(i0 + g * kTh);
+      const int64_t col = 8 * (int64_t)(i0 + g * threads);
       store8(part + 2 * (int64_t)blockIdx.x * K + col, K - col, dw[g]);
       store8(part + (2 * (int64_t)blockIdx.x + 1) * K + col, K - col, db[g]);
     }
@@ -316,41 +414,26 @@ __global__ __launch_bounds__(256) void k_layernorm_bwd_cols(const T* __restrict_
   store8(part + (2 * (int64_t)blockIdx.y + 1) * K + col, K - col, db);
 }
 
-// dw and db: the sums of the partial rows.  A workgroup takes 64 columns of one of the two; its
-// four waves take every fourth partial row and are added in order.
-__global__ __launch_bounds__(256) void k_layernorm_bwd_sum(const float* __restrict__ part, int64_t parts, int64_t K,
-                                                           float* __restrict__ dW, float* __restrict__ dB) {
-  __shared__ float red[4][64];
+// dw and db: the sums of the partial rows.  A workgroup takes 32 columns of one of the two; its 32
+// half waves take every 32nd partial row, all loads in flight, and are added in order.
+__global__ __launch_bounds__(1024) void k_layernorm_bwd_sum(const float* __restrict__ part, int64_t parts, int64_t K,
+                                                            float* __restrict__ dW, float* __restrict__ dB) {
+  __shared__ float red[32][33];
   float* out = blockIdx.y ? dB : dW;
   if (!out) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t col = (int64_t)blockIdx.x * 64 + lane;
+  const int lane = threadIdx.x & 31, half = threadIdx.x >> 5;
+  const int64_t col = (int64_t)blockIdx.x * 32 + lane;
   float s = 0.0f;
   if (col < K) {
-    for (int64_t p = wave; p < parts; p += 4) s += part[(2 * p + blockIdx.y) * K + col];
+    const float* p = part + blockIdx.y * K + col;
+#pragma unroll 8
+    for (int64_t r = half; r < parts; r += 32) s += p[2 * r * K];
   }
-  red[wave][lane] = s;
+  red[half][lane] = s;
   __syncthreads();
-  if (wave == 0 && col < K) out[col] = red[0][lane] + red[1][lane] + red[2][lane] + red[3][lane];
-}
-
-// Threads that share a row of K elements (0: the long-row form).
-int row_threads(int64_t K, int64_t most) {
-  for (int64_t th : {64, 256, 1024})
-    if (th <= most && K <= th * 8 * kMaxGroups) return (int)th;
-  return 0;
-}
-
-template <typename T, int kTh>
-void launch_rows(int groups, int64_t M, int64_t K, const T* x, const float* w, const float* b, float eps, T* y,
-                 float* mean, float* rstd, hipStream_t s) {
-  const int64_t rows = kTh == 64 ? 4 : 1;
-  const dim3 grid((unsigned)std::min<int64_t>((M + rows - 1) / rows, kMaxGrid)), block(kTh == 64 ? 256 : kTh);
-  switch (groups) {
-    case 1: k_layernorm<T, kTh, 1><<<grid, block, 0, s>>>(x, M, K, w, b, eps, y, mean, rstd); break;
-    case 2: k_layernorm<T, kTh, 2><<<grid, block, 0, s>>>(x, M, K, w, b, eps, y, mean, rstd); break;
-    case 3: k_layernorm<T, kTh, 3><<<grid, block, 0, s>>>(x, M, K, w, b, eps, y, mean, rstd); break;
-    default: k_layernorm<T, kTh, 4><<<grid, block, 0, s>>>(x, M, K, w, b, eps, y, mean, rstd); break;
+  if (half == 0 && col < K) {
+    for (int h = 1; h < 32; ++h) s += red[h][lane];
+    out[col] = s;
   }
 }
 
@@ -359,25 +442,29 @@ void launch_fwd(const void* X, int64_t M, int64_t K, const float* w, const float
                 float* rstd, hipStream_t s) {
   const T* x = static_cast<const T*>(X);
   T* y = static_cast<T*>(Y);
-  const int th = row_threads(K, 1024);
-  const int groups = th ? (int)((K + 8 * th - 1) / (8 * th)) : 0;
-  if (th == 64)
-    launch_rows<T, 64>(groups, M, K, x, w, b, eps, y, mean, rstd, s);
-  else if (th == 256)
-    launch_rows<T, 256>(groups, M, K, x, w, b, eps, y, mean, rstd, s);
-  else if (th == 1024)
-    launch_rows<T, 1024>(groups, M, K, x, w, b, eps, y, mean, rstd, s);
+  auto go = [&](auto wave, auto gc, int waves, int resident) {  // resident: waves that a compute unit holds
+    constexpr bool kWave = decltype(wave)::value;
+    constexpr int kG = decltype(gc)::value, rows = kWave ? 4 : 1;
+    const int64_t most = kCUs * std::max(1, resident / waves);
+    k_layernorm<T, kWave, kG, kG <= 2><<<dim3((unsigned)std::min<int64_t>((M + rows - 1) / rows, most)), 64 * waves, 0,
+                                        s>>>(x, M, K, w, b, eps, y, mean, rstd);
+  };
+  const std::integral_constant<int, 1> one;
+  const std::integral_constant<int, 2> two;
+  const std::integral_constant<int, 4> four;
+  auto waves = [&](int groups) { return (int)((K + 512 * groups - 1) / (512 * groups)); };
+  if (K <= 512)
+    go(std::true_type{}, one, 4, 32);
+  else if (K <= 1024)
+    go(std::true_type{}, two, 4, 20);
+  else if (K <= 8192 && M <= kCUs * kFewRows)
+    go(std::false_type{}, one, waves(1), 32);
+  else if (K <= 16384)
+    go(std::false_type{}, two, waves(2), 20);
+  else if (K <= 32768)
+    go(std::false_type{}, four, waves(4), 16);
   else
     k_layernorm_long<T><<<dim3((unsigned)std::min(M, kMaxGrid)), 1024, 0, s>>>(x, M, K, w, b, eps, y, mean, rstd);
-}
-
-template <typename T, int kTh, int kG>
-void launch_bwd_rows(const LnBwdPlan& p, int64_t M, int64_t K, const T* dy, const T* x, const float* w,
-                     const float* mean, const float* rstd, T* dx, float* part, hipStream_t s) {
-  if (part)
-    k_layernorm_bwd<T, kTh, kG, true><<<dim3((unsigned)p.wgs), 256, 0, s>>>(dy, x, M, K, w, mean, rstd, dx, part);
-  else
-    k_layernorm_bwd<T, kTh, kG, false><<<dim3((unsigned)p.wgs), 256, 0, s>>>(dy, x, M, K, w, mean, rstd, dx, part);
 }
 
 template <typename T>
@@ -385,7 +472,7 @@ void launch_bwd(const LnBwdPlan& p, const void* dY, const void* X, int64_t M, in
                 const float* mean, const float* rstd, void* dX, float* part, hipStream_t s) {
   const T *dy = static_cast<const T*>(dY), *x = static_cast<const T*>(X);
   T* dx = static_cast<T*>(dX);
-  if (p.lanes == 0) {
+  if (p.rows == 0) {
     if (dx)
       k_layernorm_bwd_long<T><<<dim3((unsigned)std::min(M, kMaxGrid)), 1024, 0, s>>>(dy, x, M, K, w, mean, rstd, dx);
     if (part)
@@ -393,21 +480,25 @@ void launch_bwd(const LnBwdPlan& p, const void* dY, const void* X, int64_t M, in
                                                                                                   rstd, part);
     return;
   }
-  auto go = [&](auto th, auto g) {
-    launch_bwd_rows<T, decltype(th)::value, decltype(g)::value>(p, M, K, dy, x, w, mean, rstd, dx, part, s);
-  };
-  auto by_groups = [&](auto th) {
-    switch (p.groups) {
-      case 1: go(th, std::integral_constant<int, 1>{}); break;
-      case 2: go(th, std::integral_constant<int, 2>{}); break;
-      case 3: go(th, std::integral_constant<int, 3>{}); break;
-      default: go(th, std::integral_constant<int, 4>{}); break;
+  auto go = [&](auto wave, auto gc) {
+    constexpr bool kWave = decltype(wave)::value;
+    constexpr int kG = decltype(gc)::value;
+    const dim3 grid((unsigned)p.wgs), block((unsigned)(p.rows * p.threads));
+    if (part) {
+      const size_t lds = p.rows > 1 ? 2 * 8 * kG * p.threads * sizeof(float) : 0;
+      k_layernorm_bwd<T, kWave, kG, true><<<grid, block, lds, s>>>(dy, x, M, K, p.rows, p.threads, w, mean, rstd, dx,
+                                                                   part);
+    } else {
+      k_layernorm_bwd<T, kWave, kG, false><<<grid, block, 0, s>>>(dy, x, M, K, p.rows, p.threads, w, mean, rstd, dx,
+                                                                  nullptr);
     }
   };
-  if (p.lanes == 64)
-    by_groups(std::integral_constant<int, 64>{});
+  if (p.threads == 64)
+    go(std::true_type{}, std::integral_constant<int, 1>{});
+  else if (p.groups == 1)
+    go(std::false_type{}, std::integral_constant<int, 1>{});
   else
-    by_groups(std::integral_constant<int, 256>{});
+    go(std::false_type{}, std::integral_constant<int, 2>{});
 }
 
 }  // namespace
@@ -423,11 +514,14 @@ hipError_t launch_layernorm(const void* X, int bf16, int64_t M, int64_t K, const
 
 LnBwdPlan plan_layernorm_backward(int64_t M, int64_t K) {
   LnBwdPlan p;
-  p.lanes = row_threads(K, 256);
-  if (p.lanes) {
-    const int64_t rows = p.lanes == 64 ? 4 : 1;
-    p.groups = (int)((K + 8 * p.lanes - 1) / (8 * p.lanes));
-    p.wgs = std::min<int64_t>((M + rows - 1) / rows, 512);
+  // one group of 8 elements per thread up to 16 waves a row, and as many rows as 16 waves hold (one
+  // workgroup to a compute unit, so one partial row each); two groups and one row up to 12 waves
+  if (K <= 12288) {
+    p.groups = K <= 8192 ? 1 : 2;
+    const int waves = (int)((K + 512 * p.groups - 1) / (512 * p.groups));
+    p.threads = 64 * waves;
+    p.rows = p.groups == 1 ? (int)std::min<int64_t>(16 / waves, M) : 1;
+    p.wgs = std::min<int64_t>((M + p.rows - 1) / p.rows, kCUs);
     p.parts = p.wgs;
   } else {
     p.parts = std::min<int64_t>(M, 64);
@@ -446,7 +540,7 @@ hipError_t launch_layernorm_backward(const void* dY, const void* X, int bf16, in
   else
     launch_bwd<float>(p, dY, X, M, K, weight, mean, rstd, dX, part, s);
   if (part)
-    k_layernorm_bwd_sum<<<dim3((unsigned)((K + 63) / 64), 2), 256, 0, s>>>(part, p.parts, K, dW, dB);
+    k_layernorm_bwd_sum<<<dim3((unsigned)((K + 31) / 32), 2), 1024, 0, s>>>(part, p.parts, K, dW, dB);
   return hipGetLastError();
 }
 
