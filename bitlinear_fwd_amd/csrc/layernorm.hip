@@ -107,7 +107,7 @@ __device__ __forceinline__ void stream8(T* p, int64_t n, const float (&v)[8]) {
   } else {
     v4u w;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = bf16_bits(v[2 * i]) | bf16_bits(v[2 * i + 1]) << 16;
+    for (int i = 0; i < 4; ++i) w[i] = bf16_pair(v[2 * i], v[2 * i + 1]);
     __builtin_nontemporal_store(w, reinterpret_cast<v4u_unaligned*>(p));
   }
 }

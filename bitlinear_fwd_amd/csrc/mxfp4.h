@@ -42,6 +42,17 @@ __device__ __forceinline__ v4f mx_mfma(v4i a, v4i b, v4f acc, int sa, int sb) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wa, wb, acc, 4, 4, TA, sa, TB, sb);
 }
 
+// The same of 32 rows x 64 columns by 32 rows: lane l holds row l % 32 (of two tiles: rows 0 .. 15
+// of the first, then of the second), block l / 32 of the two in this half of the tiles' columns.
+// acc[i] of lane l is the sum for A's row 8 (i / 4) + 4 (l / 32) + i % 4 and B's row l % 32.
+typedef float v16f __attribute__((ext_vector_type(16)));
+template <int TA, int TB>
+__device__ __forceinline__ v16f mx_mfma32(v4i a, v4i b, v16f acc, int sa, int sb) {
+  const v8i wa = __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1);
+  const v8i wb = __builtin_shufflevector(b, b, 0, 1, 2, 3, -1, -1, -1, -1);
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wa, wb, acc, 4, 4, TA, sa, TB, sb);
+}
+
 // Scale byte of a block whose largest magnitude has the fp32 bits `bits` (sign cleared): the
 // power of two of that magnitude over 4, the grid's largest power (2^-127 at least); 255 where
 // the block holds a NaN or an infinity.
@@ -80,12 +91,14 @@ __device__ __forceinline__ void load8(const uint16_t* p, int64_t n, float (&v)[8
   }
 }
 
-// fp32 to bf16 bits, to nearest with ties to even (NaN stays NaN: a quiet bit is set).
-__device__ __forceinline__ uint32_t bf16_bits(float f) {
-  const uint32_t u = __float_as_uint(f);
-  if ((u & 0x7fffffffu) > 0x7f800000u) return (u >> 16) | 0x40u;
-  return (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
+// Two fp32 values to bf16 bits, to nearest with ties to even (one instruction; NaN stays NaN).
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  const v2f f = {lo, hi};
+  const v2bf b = __builtin_convertvector(f, v2bf);
+  return __builtin_bit_cast(uint32_t, b);
 }
+__device__ __forceinline__ uint16_t bf16_bits(float f) { return (uint16_t)bf16_pair(f, 0.0f); }
 
 // Eight fp32 values to a row; only the first n are written.
 __device__ __forceinline__ void store8(float* p, int64_t n, const float (&v)[8]) {
@@ -101,12 +114,12 @@ __device__ __forceinline__ void store8(uint16_t* p, int64_t n, const float (&v)[
   if (n >= 8) {
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = bf16_bits(v[2 * i]) | bf16_bits(v[2 * i + 1]) << 16;
+    for (int i = 0; i < 4; ++i) w[i] = bf16_pair(v[2 * i], v[2 * i + 1]);
     __builtin_memcpy(p, w, 16);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = (uint16_t)bf16_bits(v[i]);
+      if (i < n) p[i] = bf16_bits(v[i]);
   }
 }
 

@@ -9,6 +9,8 @@
 //   * The tile layout is the operand layout, so a 1 KiB tile goes from global memory straight into
 //     LDS (direct loads, no registers) and a fragment is one conflict-free 16-byte LDS read per
 //     lane.  Words of scales take the same way, once per four steps.
+//   * The reads of a step's fragments are spread over the matrix instructions of the step before:
+//     issued in one go they fill the LDS queue, and the four waves wait for one another.
 //   * Ring of four 128-column stages.  Step s: wait until stage s + 1 has landed (everybody's, by a
 //     barrier), issue the loads of stage s + 4 into the slot of stage s (its fragments were read in
 //     step s - 1 and the barrier waits for them), read the fragments of step s + 1, and run the
@@ -72,30 +74,6 @@ __device__ __forceinline__ T* uniform_ptr(T* p) {
               (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
 }
 
-template <typename TY>
-__device__ __forceinline__ void store4(TY* y, int64_t left, v4f v, bool vec) {
-  if constexpr (sizeof(TY) == 4) {
-    if (vec && left >= 4) {
-      *reinterpret_cast<v4f*>(y) = v;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < left) y[i] = v[i];
-    }
-  } else {
-    if (vec && left >= 4) {
-      uint2 w;
-      w.x = bf16_bits(v[0]) | bf16_bits(v[1]) << 16;
-      w.y = bf16_bits(v[2]) | bf16_bits(v[3]) << 16;
-      *reinterpret_cast<uint2*>(y) = w;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < left) y[i] = (TY)bf16_bits(v[i]);
-    }
-  }
-}
-
 // Four waves in 2 x 2, each with kB x kB tiles of 16 x 16: output tiles of 32 kB x 32 kB.
 template <int kB, typename TY>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kB == 8 ? 1 : 2, kB == 8 ? 1 : 2))) void k_mx_gemm(
@@ -150,27 +128,37 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kB == 8 ? 1
     }
   };
 
-  v4f acc[kB][kB];
+  // fragments of 32 rows x 64 columns: two tiles' rows, half h of their columns
+  constexpr int kT = kB / 2;
+  v16f acc[kT][kT];
 #pragma unroll
-  for (int i = 0; i < kB; ++i)
+  for (int i = 0; i < kT; ++i)
 #pragma unroll
-    for (int j = 0; j < kB; ++j) acc[i][j] = v4f{0, 0, 0, 0};
-  v4i fa[2][kB], fb[2][kB];
-  int sa[2][kB], sb[2][kB];
-  auto read = [&](int slot, v4i (&a)[kB], v4i (&b)[kB]) {
-    const uint8_t* p = lds + slot * kStage + 16 * lane;
+    for (int j = 0; j < kT; ++j)
 #pragma unroll
-    for (int i = 0; i < kB; ++i) {
-      a[i] = *reinterpret_cast<const v4i*>(p + (kB * wn + i) * 1024);
-      b[i] = *reinterpret_cast<const v4i*>(p + (kSide + kB * wm + i) * 1024);
-    }
-  };
-  auto read_scales = [&](int (&a)[kB], int (&b)[kB]) {
-    const uint8_t* p = lds + 4 * kStage + 4 * lane;
-#pragma unroll
-    for (int i = 0; i < kB; ++i) {
-      a[i] = *reinterpret_cast<const int*>(p + (kB * wn + i) * 256);
-      b[i] = *reinterpret_cast<const int*>(p + (kSide + kB * wm + i) * 256);
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+  v4i fa[2][2][kT], fb[2][2][kT];
+  int sa[2][2][kT], sb[2][2][kT];
+  const int tile = (lane >> 4) & 1, slot = 16 * (lane >> 5) + (lane & 15);  // of a fragment, this lane's
+  // The reads of a step, one at a time so that they can be spread over its matrix instructions:
+  // 4 kT fragments, then (with scales) as many words of scales; both matrices in turn, first half
+  // first.
+  auto read_one = [&](auto rr, int ring, v4i (&a)[2][kT], v4i (&b)[2][kT], int (&wa)[2][kT], int (&wb)[2][kT]) {
+    constexpr int r = rr, f = r % (4 * kT), h = f / (2 * kT), i = f % (2 * kT) / 2;
+    constexpr int rb = 2 * i;
+    const int base = f % 2 ? kSide + kB * wm : kB * wn;
+    if constexpr (r < 4 * kT) {
+      const v4i v = *reinterpret_cast<const v4i*>(lds + ring * kStage + (base + rb + tile) * 1024 + 16 * slot + 512 * h);
+      if constexpr (f % 2)
+        b[h][i] = v;
+      else
+        a[h][i] = v;
+    } else {
+      const int v = *reinterpret_cast<const int*>(lds + 4 * kStage + (base + rb + tile) * 256 + 4 * slot + 128 * h);
+      if constexpr (f % 2)
+        wb[h][i] = v;
+      else
+        wa[h][i] = v;
     }
   };
 
@@ -186,8 +174,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kB == 8 ? 1
   } else {
     ring_wait<0>();
   }
-  read(0, fa[0], fb[0]);
-  read_scales(sa[0], sb[0]);
+  static_for<8 * kT>([&](auto r) { read_one(r, 0, fa[0], fb[0], sa[0], sb[0]); });
 
   for (int c0 = 0; c0 < tiles; c0 += 8) {
     bool done = false;
@@ -203,29 +190,75 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kB == 8 ? 1
         ring_wait<2 * L + ((t == 1 || t == 2) ? S : 0)>();
       else
         ring_wait<0>();
-      if (c + 4 <= last) issue(c + 4, t, t == 0);
-      if (c + 1 <= last) {
-        read((t + 1) % 4, fa[1 - cur], fb[1 - cur]);
-        if constexpr (t == 3) read_scales(sa[1 - g], sb[1 - g]);
-      }
+      // 2 kT batches of kT matrix instructions; the reads of the next step go in front of all but the
+      // last two, whose time covers the latency of the last read, and the direct loads after the
+      // first.  (The reads of the step after the last fetch what is in LDS, for nothing.)
+      constexpr int kReads = t == 3 ? 8 * kT : 4 * kT, kBatch = (kReads + 2 * kT - 3) / (2 * kT - 2);
+      static_for<2 * kT>([&](auto bb) {
+        constexpr int h = bb / kT, i = bb % kT;
+        static_for<kBatch>([&](auto rr) {
+          if constexpr (bb * kBatch + rr < kReads)
+            read_one(std::integral_constant<int, bb * kBatch + rr>{}, (t + 1) % 4, fa[1 - cur], fb[1 - cur], sa[1 - g],
+                     sb[1 - g]);
+        });
 #pragma unroll
-      for (int i = 0; i < kB; ++i)
-#pragma unroll
-        for (int j = 0; j < kB; ++j) acc[i][j] = mx_mfma<t, t>(fa[cur][i], fb[cur][j], acc[i][j], sa[g][i], sb[g][j]);
+        for (int j = 0; j < kT; ++j)
+          acc[i][j] = mx_mfma32<t, t>(fa[cur][h][i], fb[cur][h][j], acc[i][j], sa[g][h][i], sb[g][h][j]);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (bb == 0) {
+          if (c + 4 <= last) issue(c + 4, t, t == 0);
+        }
+      });
     });
   }
 
-  // lane l of a tile: token l % 16, four consecutive outputs from 4 (l / 16)
-  const bool vec = N % 4 == 0 && ((uintptr_t)Y & (4 * sizeof(TY) - 1)) == 0;
+  // Each wave turns its accumulators (lane l of a 32 x 32 tile: token l % 32, four times four
+  // consecutive outputs) into whole rows through its quarter of the ring, 32 tokens at a time.  The
+  // row stride puts the 32 tokens of a write on different banks.
+  constexpr int kRow = 16 * kB * sizeof(TY) + (sizeof(TY) == 4 ? 16 : 8);  // bytes
+  constexpr int kPer = 16 / sizeof(TY);                                    // outputs of a 16-byte piece
+  constexpr int kPieces = 16 * kB / kPer;                                  // pieces of a row
+  static_assert(32 * kRow <= kStage, "a slab fits the wave's quarter");
+  ring_wait<0>();  // the other waves have read their last fragments
+  uint8_t* slab = lds + wave * kStage;
 #pragma unroll
-  for (int j = 0; j < kB; ++j) {
-    const int64_t m = ((int64_t)tm * kSide + kB * wm + j) * 16 + (lane & 15);
-    if (m >= M) continue;
+  for (int j = 0; j < kT; ++j) {
 #pragma unroll
-    for (int i = 0; i < kB; ++i) {
-      const int64_t n = ((int64_t)tn * kSide + kB * wn + i) * 16 + 4 * (lane >> 4);
-      store4(Y + m * N + n, N - n, acc[i][j], vec);
+    for (int i = 0; i < kT; ++i) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint8_t* at = slab + (lane & 31) * kRow + (32 * i + 8 * q + 4 * (lane >> 5)) * sizeof(TY);
+        const v4f v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        if constexpr (sizeof(TY) == 4) {
+          *reinterpret_cast<v4f*>(at) = v;
+        } else {
+          uint2 w;
+          w.x = bf16_pair(v[0], v[1]);
+          w.y = bf16_pair(v[2], v[3]);
+          *reinterpret_cast<uint2*>(at) = w;
+        }
+      }
     }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // a wave's own writes, read by its other lanes
+    const int64_t m0 = ((int64_t)tm * kSide + kB * wm + 2 * j) * 16;
+    const int64_t n0 = ((int64_t)tn * kSide + kB * wn) * 16;
+#pragma unroll 8
+    for (int t = 0; t < 32 * kPieces / 64; ++t) {
+      const int piece = 64 * t + lane, r = piece / kPieces, c = piece % kPieces;
+      const int64_t m = m0 + r, n = n0 + kPer * c, left = m < M ? N - n : 0;
+      TY* y = Y + m * N + n;
+      TY v[kPer];
+      __builtin_memcpy(v, slab + r * kRow + 16 * c, 8);
+      __builtin_memcpy(v + kPer / 2, slab + r * kRow + 16 * c + 8, 8);
+      if (left >= kPer) {
+        __builtin_memcpy(y, v, 16);
+      } else {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e)
+          if (e < left) y[e] = v[e];
+      }
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read before the next slab is written
   }
 }
 
