@@ -30,12 +30,14 @@ bool rows_ok(int64_t R, int64_t K) { return R >= 1 && K >= 1 && R < kMaxDim && K
 // eps of the sub-layer normalisation: finite and >= 0 (NaN fails both comparisons)
 bool eps_ok(float eps) { return eps >= 0.0f && eps <= 3.4028234663852886e38f; }
 
-constexpr int kMxDecodeMaxM = 64;  // tokens of an MXFP4 product that the decode kernel takes
+int mx_src(int dt) { return dt == BL_BF16 ? 1 : 2; }  // plan_mx_few's source of an un-quantised x
 hipError_t mx_forward(const uint8_t* codes, const uint8_t* scales, const uint8_t* xcodes, const uint8_t* xscales,
                       int64_t M, int64_t N, int64_t K, void* Y, int ydt, hipStream_t s) {
-  return M <= kMxDecodeMaxM
-             ? bl::launch_mx_decode(codes, scales, xcodes, xscales, M, N, K, Y, ydt == BL_BF16, s)
-             : bl::launch_mx_gemm(codes, scales, xcodes, xscales, M, N, K, Y, ydt == BL_BF16, s);
+  const int bf16 = ydt == BL_BF16;
+  if (bl::plan_mx_few(M, N, K, 0).ok)
+    return bl::launch_mx_few(codes, scales, xcodes, xscales, 0, M, N, K, Y, bf16, s);
+  return bl::mx_decode_wins(M, N, K) ? bl::launch_mx_decode(codes, scales, xcodes, xscales, M, N, K, Y, bf16, s)
+                                     : bl::launch_mx_gemm(codes, scales, xcodes, xscales, M, N, K, Y, bf16, s);
 }
 
 // Sizes of an MXFP4 product: both matrices addressable, and a launchable number of tiles.
@@ -174,6 +176,7 @@ int bitlinear_forward_mxfp4(const uint8_t* codes, const uint8_t* scales, const u
 
 int64_t bitlinear_forward_mxfp4_fused_ws_bytes(int64_t M, int64_t N, int64_t K, int dt) {
   if (!rows_ok(M, K) || !rows_ok(N, K) || !dtype_ok(dt)) return -1;
+  if (bl::plan_mx_few(M, N, K, mx_src(dt)).ok) return 0;
   return bl::mx_codes_bytes(M, K) + bl::mx_scales_bytes(M, K);
 }
 
@@ -187,6 +190,8 @@ int bitlinear_forward_mxfp4_fused(const uint8_t* codes, const uint8_t* scales, c
   const int64_t need = bitlinear_forward_mxfp4_fused_ws_bytes(M, N, K, dt);
   if (need > 0 && (!workspace || !aligned(workspace, 16) || ws_bytes < need)) return BL_ERR_INVALID_ARG;
   hipStream_t s = static_cast<hipStream_t>(stream);
+  if (need == 0)
+    return hip_status(bl::launch_mx_few(codes, scales, X, nullptr, mx_src(dt), M, N, K, Y, ydt == BL_BF16, s));
   uint8_t* xcodes = static_cast<uint8_t*>(workspace);
   uint8_t* xscales = xcodes + bl::mx_codes_bytes(M, K);
   const hipError_t e = bl::launch_mx_quant(X, dt == BL_BF16, M, K, xcodes, xscales, nullptr, s);

@@ -54,41 +54,6 @@ __device__ __forceinline__ void row_sum(F (&v)[kN], F* red, int i0 = threadIdx.x
   }
 }
 
-// Eight elements as they are in memory, so that the next row's loads can be in flight while this
-// one is worked on: widen8 makes fp32 of them.
-template <typename T>
-struct Raw8 {
-  uint32_t w[2 * sizeof(T)];
-};
-template <typename T>
-__device__ __forceinline__ Raw8<T> load_raw8(const T* p, int64_t n) {
-  Raw8<T> r;
-  if (n >= 8) {
-    __builtin_memcpy(r.w, p, 8 * sizeof(T));
-  } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r.w[i] = i < n ? __float_as_uint(p[i]) : 0u;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      r.w[i] = (2 * i < n ? (uint32_t)p[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)p[2 * i + 1] << 16 : 0u);
-  }
-  return r;
-}
-template <typename T>
-__device__ __forceinline__ void widen8(const Raw8<T>& r, float (&v)[8]) {
-  if constexpr (sizeof(T) == 4) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r.w[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(r.w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(r.w[i] & 0xffff0000u);
-    }
-  }
-}
-
 // store8 past the caches: for outputs larger than they hold.
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef v4u v4u_unaligned __attribute__((aligned(2)));

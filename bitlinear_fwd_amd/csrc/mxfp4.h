@@ -31,6 +31,7 @@ inline int64_t mx_scales_bytes(int64_t r, int64_t k) { return mx_row_blocks(r) *
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float v2f __attribute__((ext_vector_type(2)));
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 
 // acc += A B of one tile pair: A's 16 rows x 128 columns (lane l: row l % 16, block l / 16) by
 // B's, the scales in bytes TA and TB of sa and sb.  acc[i] of lane l is the sum for A's row
@@ -65,34 +66,82 @@ __device__ __forceinline__ uint32_t mx_scale_byte(uint32_t bits) {
 // The fp32 number 2^(e - 127), e < 255 (e = 0: the subnormal 2^-127).
 __device__ __forceinline__ float mx_scale(uint32_t e) { return __uint_as_float(e ? e << 23 : 0x00400000u); }
 
-// Eight consecutive elements of a row as fp32; elements past n are 0.  Whole groups are read 16
-// bytes at a time at any alignment (the target's global loads need none).
-__device__ __forceinline__ void load8(const float* p, int64_t n, float (&v)[8]) {
+// Eight consecutive elements of a row as they are in memory (fp32, or bf16 as uint16_t); elements
+// past n are 0.  Whole groups are read 16 bytes at a time at any alignment (the target's global loads
+// need none).  widen8 makes fp32 of them, load8 does both.
+template <typename T>
+struct Raw8 {
+  uint32_t w[2 * sizeof(T)];
+};
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_raw8(const T* p, int64_t n) {
+  Raw8<T> r;
   if (n >= 8) {
-    __builtin_memcpy(v, p, 32);
-  } else {
+    __builtin_memcpy(r.w, p, 8 * sizeof(T));
+  } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : 0.0f;
-  }
-}
-__device__ __forceinline__ void load8(const uint16_t* p, int64_t n, float (&v)[8]) {
-  uint32_t w[4];
-  if (n >= 8) {
-    __builtin_memcpy(w, p, 16);
+    for (int i = 0; i < 8; ++i) r.w[i] = i < n ? __float_as_uint(p[i]) : 0u;
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      w[i] = (2 * i < n ? (uint32_t)p[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)p[2 * i + 1] << 16 : 0u);
+      r.w[i] = (2 * i < n ? (uint32_t)p[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)p[2 * i + 1] << 16 : 0u);
   }
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void widen8(const Raw8<T>& r, float (&v)[8]) {
+  if constexpr (sizeof(T) == 4) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r.w[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(r.w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(r.w[i] & 0xffff0000u);
+    }
   }
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int64_t n, float (&v)[8]) {
+  widen8(load_raw8(p, n), v);
+}
+
+// Codes of eight values of a block that a quad of lanes shares (32 columns, lane p of it columns
+// 8 p ..), one 4-bit code after the other, and the block's scale byte e.
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xf, 0xf, true));
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xf, 0xf, true));
+}
+__device__ __forceinline__ uint32_t mx_quantize8(const Raw8<float>& r, uint32_t& e) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, r.w[i] & 0x7fffffffu);
+  e = mx_scale_byte(quad_max(top));
+  const float s = mx_scale(e == 255 ? 127 : e);
+  uint32_t q = 0;
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, __uint_as_float(r.w[0]), __uint_as_float(r.w[1]), s, 0);
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, __uint_as_float(r.w[2]), __uint_as_float(r.w[3]), s, 1);
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, __uint_as_float(r.w[4]), __uint_as_float(r.w[5]), s, 2);
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, __uint_as_float(r.w[6]), __uint_as_float(r.w[7]), s, 3);
+  return e == 255 ? 0 : q;
+}
+// bf16: the largest magnitude as 16-bit integers, two at a time, and the conversion from bf16 pairs.
+__device__ __forceinline__ uint32_t mx_quantize8(const Raw8<uint16_t>& r, uint32_t& e) {
+  typedef unsigned short v2u __attribute__((ext_vector_type(2)));
+  v2u m = __builtin_bit_cast(v2u, r.w[0] & 0x7fff7fffu);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(v2u, r.w[i] & 0x7fff7fffu));
+  e = mx_scale_byte(quad_max((uint32_t)max(m.x, m.y) << 16));
+  const float s = mx_scale(e == 255 ? 127 : e);
+  uint32_t q = 0;
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(v2bf, r.w[0]), s, 0);
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(v2bf, r.w[1]), s, 1);
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(v2bf, r.w[2]), s, 2);
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(v2bf, r.w[3]), s, 3);
+  return e == 255 ? 0 : q;
 }
 
 // Two fp32 values to bf16 bits, to nearest with ties to even (one instruction; NaN stays NaN).
-typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   const v2f f = {lo, hi};
   const v2bf b = __builtin_convertvector(f, v2bf);
@@ -130,6 +179,18 @@ hipError_t launch_mx_decode(const uint8_t* codes, const uint8_t* scales, const u
                             const uint8_t* xscales, int64_t M, int64_t N, int64_t K, void* Y, int ybf16,
                             hipStream_t s);
 
+// Few tokens (M <= 16) whose codes fit LDS, in one launch: src 0: x as codes and scales, 1: bf16, 2:
+// fp32 x[M][K], quantised by every workgroup.
+struct MxFewPlan {
+  bool ok = false;
+  int waves = 0;
+  int64_t groups = 0;  // workgroups
+  int64_t lds = 0;     // bytes
+};
+MxFewPlan plan_mx_few(int64_t M, int64_t N, int64_t K, int src);
+hipError_t launch_mx_few(const uint8_t* codes, const uint8_t* scales, const void* x, const uint8_t* xscales, int src,
+                         int64_t M, int64_t N, int64_t K, void* Y, int ybf16, hipStream_t s);
+
 // Launch plan of the decode kernel.
 struct MxDecodePlan {
   int waves = 4;       // waves per workgroup; they split the column groups
@@ -137,10 +198,12 @@ struct MxDecodePlan {
   int64_t gx = 0, gy = 0;
 };
 MxDecodePlan plan_mx_decode(int64_t M, int64_t N, int64_t K);
+// Whether the decode kernel is estimated to be faster than the GEMM.
+bool mx_decode_wins(int64_t M, int64_t N, int64_t K);
 
-// Launch plan of the GEMM: square output tiles.
+// Launch plan of the GEMM: output tiles of tile_m tokens x tile_n outputs.
 struct MxGemmPlan {
-  int64_t side = 256;  // 256 or 128
+  int64_t tile_m = 256, tile_n = 256;
   int64_t tiles_m = 0, tiles_n = 0;
 };
 MxGemmPlan plan_mx_gemm(int64_t M, int64_t N, int64_t K);

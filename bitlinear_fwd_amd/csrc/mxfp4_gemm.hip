@@ -1,21 +1,23 @@
 // MXFP4 product for many tokens: Y[M][N] = sum_k Xv[m][k] Wv[n][k], both matrices as codes and
 // scales in the layout of mxfp4.h, on the scaled matrix instructions (16x16x128, 4-bit operands).
 //
-// At 4 bits the matrix cores outrun the operands: a 16x16x128 step takes a wave 16 cycles and eats
-// 2 KiB, so what decides is how often a loaded byte is used.  Hence output tiles of 256 x 256 by
-// four waves of 128 x 128 each (64 matrix instructions per 16 KiB of fragments; 256 accumulator
-// registers, one wave per SIMD), or 128 x 128 by four waves of 64 x 64 where the large tiles would
-// leave compute units idle.
+// At 4 bits the matrix cores outrun the operands: a 32x32x64 step takes 32 cycles and eats 2 KiB, so
+// what decides is how often a loaded byte is used and what else runs meanwhile.  Output tiles of 128
+// tokens x 256 outputs by four waves of 64 x 128 (or 64 x 64, for 128 x 128, where the large tiles
+// would leave compute units idle), sized so that two workgroups share a compute unit: one's first
+// loads and output stores run under the other's matrix instructions.  Measured: tiles of 256 x 256
+// with one workgroup to a unit use each byte more often, but load, compute and store in turn (2048 x
+// 28672 x 8192 to bf16 with the quantiser 273 us, against 250; 8192^3 283 us against 276).
+//   * 32x32x64 instructions: with the 16x16x128 form the waves cannot issue fast enough (5.4 against
+//     9.6 PFLOP/s from registers, one wave per SIMD).  On random data power holds both back.
 //   * The tile layout is the operand layout, so a 1 KiB tile goes from global memory straight into
 //     LDS (direct loads, no registers) and a fragment is one conflict-free 16-byte LDS read per
 //     lane.  Words of scales take the same way, once per four steps.
-//   * The reads of a step's fragments are spread over the matrix instructions of the step before:
-//     issued in one go they fill the LDS queue, and the four waves wait for one another.
-//   * Ring of four 128-column stages.  Step s: wait until stage s + 1 has landed (everybody's, by a
-//     barrier), issue the loads of stage s + 4 into the slot of stage s (its fragments were read in
-//     step s - 1 and the barrier waits for them), read the fragments of step s + 1, and run the
-//     matrix instructions of step s on fragments that are already there: with one wave per SIMD
-//     nothing else hides the LDS latency.
+//   * Ring of three or four 128-column stages, worked on by halves of 64 columns: a half's matrix
+//     instructions run on fragments already in registers, with the reads of the next half's spread
+//     between them (in one go they fill the LDS queue, and the waves wait for one another).  In the
+//     middle of a step the workgroup waits until the next stage has landed; by then every wave has
+//     read the whole of this one, and the loads of the stage after the ring go into its slot.
 //   * The direct loads are written in inline assembly (they have no output registers): for the
 //     builtin the compiler would wait for every load in flight before any LDS read, as it cannot
 //     tell which slot a load writes.  All ordering of loads against reads is by ring_wait below,
@@ -36,24 +38,18 @@ __device__ __forceinline__ void ring_wait() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(n) : "memory");
 }
 
-// Direct loads of 1 KiB each from base[0 .. 3] (16 bytes per lane at `off`) to consecutive KiB of
-// LDS from byte address `lds`.  The wait states: M0 and the bases may have been written just before.
-__device__ __forceinline__ void load4_lds(const uint8_t* const (&base)[4], uint32_t off, uint32_t lds) {
+// Two direct loads of 1 KiB (16 bytes per lane at `off`) from a and b to consecutive KiB of LDS from
+// byte address `lds`.  The wait states: M0 and the bases may have been written just before.
+__device__ __forceinline__ void load2_lds(const uint8_t* a, const uint8_t* b, uint32_t off, uint32_t lds) {
   asm volatile(
       "s_nop 4\n\t"
-      "s_mov_b32 m0, %5\n\t"
+      "s_mov_b32 m0, %3\n\t"
       "s_nop 0\n\t"
-      "global_load_lds_dwordx4 %4, %0\n\t"
+      "global_load_lds_dwordx4 %2, %0\n\t"
       "s_add_u32 m0, m0, 0x400\n\t"
       "s_nop 0\n\t"
-      "global_load_lds_dwordx4 %4, %1\n\t"
-      "s_add_u32 m0, m0, 0x400\n\t"
-      "s_nop 0\n\t"
-      "global_load_lds_dwordx4 %4, %2\n\t"
-      "s_add_u32 m0, m0, 0x400\n\t"
-      "s_nop 0\n\t"
-      "global_load_lds_dwordx4 %4, %3"
-      ::"s"(base[0]), "s"(base[1]), "s"(base[2]), "s"(base[3]), "v"(off), "s"(lds)
+      "global_load_lds_dwordx4 %2, %1"
+      ::"s"(a), "s"(b), "v"(off), "s"(lds)
       : "memory", "scc");
 }
 // One direct load of 1 KiB, each lane's 16 bytes from its own address.
@@ -74,18 +70,20 @@ __device__ __forceinline__ T* uniform_ptr(T* p) {
               (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
 }
 
-// Four waves in 2 x 2, each with kB x kB tiles of 16 x 16: output tiles of 32 kB x 32 kB.
-template <int kB, typename TY>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kB == 8 ? 1 : 2, kB == 8 ? 1 : 2))) void k_mx_gemm(
-    const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, const uint8_t* __restrict__ xcodes,
-    const uint8_t* __restrict__ xscales, int64_t M, int64_t N, int tiles, int groups, int nblocks, int xblocks,
-    int tiles_m, int total, TY* __restrict__ Y) {
-  constexpr int kSide = 2 * kB;                  // row blocks of each matrix in a stage
-  constexpr int kStage = 2 * kSide * 1024;       // bytes: weights, then tokens
-  constexpr int kLoads = kSide / 2;              // direct loads per wave and stage
-  constexpr int kScaleLoads = kSide * 512 / 4096;  // and per wave and four stages, of scales
-  static_assert(kLoads % 4 == 0 && kScaleLoads >= 1, "whole batches of direct loads");
-  extern __shared__ uint8_t lds[];               // four stages, then 2 kSide x 256 bytes of scales
+// Four waves in 2 x 2, each with kN x kM blocks of 16 weight rows and 16 tokens: output tiles of
+// 32 kM tokens x 32 kN outputs.  kR stages of 128 columns in the ring.
+template <int kN, int kM, int kR, typename TY>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void
+k_mx_gemm(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, const uint8_t* __restrict__ xcodes,
+          const uint8_t* __restrict__ xscales, int64_t M, int64_t N, int tiles, int groups, int nblocks, int xblocks,
+          int tiles_m, int total, TY* __restrict__ Y) {
+  constexpr int kBlocks = 2 * (kN + kM);          // row blocks of a stage: weights, then tokens
+  constexpr int kStage = kBlocks * 1024;          // bytes
+  constexpr int L = kBlocks / 4;                  // direct loads per wave and stage
+  constexpr int S = (kBlocks / 4 + 3) / 4;        // and per wave and four stages, of scales
+  constexpr int TN = kN / 2, TM = kM / 2;         // 32-row tiles of a wave
+  static_assert(L % 2 == 0, "direct loads come in pairs");
+  extern __shared__ uint8_t lds[];                // the ring, then kBlocks x 256 bytes of scales
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wn = wave & 1, wm = wave >> 1;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)lds;
@@ -98,133 +96,133 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kB == 8 ? 1
   }
   const int tm = id % tiles_m, tn = id / tiles_m;
 
-  // this wave's direct loads: row blocks kLoads * wave .. of the stage (weights, then tokens)
-  const uint8_t* src[kLoads];
+  // row block t of a stage (past the last: the last again, not stored)
+  auto block = [&](int t, const uint8_t* w, const uint8_t* x, int64_t bytes) {
+    return t < 2 * kN ? w + min(tn * 2 * kN + t, nblocks - 1) * bytes
+                      : x + min(tm * 2 * kM + t - 2 * kN, xblocks - 1) * bytes;
+  };
+  // this wave's direct loads: blocks L wave .. of the stage, and of the scales KiB S wave .. (four
+  // blocks each; waves past the last repeat it, so that all have the same number in flight)
+  const uint8_t* src[L];
 #pragma unroll
-  for (int j = 0; j < kLoads; ++j) {
-    const int t = kLoads * wave + j;
-    const int64_t rb = t < kSide ? min(tn * kSide + t, nblocks - 1) : min(tm * kSide + t - kSide, xblocks - 1);
-    src[j] = uniform_ptr((t < kSide ? codes : xcodes) + rb * tiles * kMxTileBytes);
-  }
-  const uint8_t* ssrc[kScaleLoads];
+  for (int j = 0; j < L; ++j) src[j] = uniform_ptr(block(L * wave + j, codes, xcodes, (int64_t)tiles * kMxTileBytes));
+  const uint8_t* ssrc[S];
+  int sdst[S];
 #pragma unroll
-  for (int j = 0; j < kScaleLoads; ++j) {
-    const int t = 4 * (kScaleLoads * wave + j) + (lane >> 4);  // four row blocks to a load
-    const int64_t rb = t < kSide ? min(tn * kSide + t, nblocks - 1) : min(tm * kSide + t - kSide, xblocks - 1);
-    ssrc[j] = (t < kSide ? scales : xscales) + rb * groups * 256 + 16 * (lane & 15);
+  for (int j = 0; j < S; ++j) {
+    sdst[j] = min(S * wave + j, kBlocks / 4 - 1);
+    ssrc[j] = block(4 * sdst[j] + (lane >> 4), scales, xscales, (int64_t)groups * 256) + 16 * (lane & 15);
   }
   auto issue = [&](int c, int slot, bool with_scales) {
 #pragma unroll
-    for (int j = 0; j < kLoads; j += 4) {
-      const uint8_t* b[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) b[i] = src[j + i] + (int64_t)c * kMxTileBytes;
-      load4_lds(b, 16 * lane, lds0 + slot * kStage + (kLoads * wave + j) * 1024);
-    }
+    for (int j = 0; j < L; j += 2)
+      load2_lds(src[j] + (int64_t)c * kMxTileBytes, src[j + 1] + (int64_t)c * kMxTileBytes, 16 * lane,
+                lds0 + slot * kStage + (L * wave + j) * 1024);
     if (with_scales) {
 #pragma unroll
-      for (int j = 0; j < kScaleLoads; ++j)
-        load1_lds(ssrc[j] + (int64_t)(c >> 2) * 256, lds0 + 4 * kStage + (kScaleLoads * wave + j) * 1024);
+      for (int j = 0; j < S; ++j)
+        load1_lds(ssrc[j] + (int64_t)(c >> 2) * 256, lds0 + kR * kStage + sdst[j] * 1024);
     }
   };
 
-  // fragments of 32 rows x 64 columns: two tiles' rows, half h of their columns
-  constexpr int kT = kB / 2;
-  v16f acc[kT][kT];
+  v16f acc[TN][TM];
 #pragma unroll
-  for (int i = 0; i < kT; ++i)
+  for (int i = 0; i < TN; ++i)
 #pragma unroll
-    for (int j = 0; j < kT; ++j)
+    for (int j = 0; j < TM; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-  v4i fa[2][2][kT], fb[2][2][kT];
-  int sa[2][2][kT], sb[2][2][kT];
-  const int tile = (lane >> 4) & 1, slot = 16 * (lane >> 5) + (lane & 15);  // of a fragment, this lane's
-  // The reads of a step, one at a time so that they can be spread over its matrix instructions:
-  // 4 kT fragments, then (with scales) as many words of scales; both matrices in turn, first half
-  // first.
-  auto read_one = [&](auto rr, int ring, v4i (&a)[2][kT], v4i (&b)[2][kT], int (&wa)[2][kT], int (&wb)[2][kT]) {
-    constexpr int r = rr, f = r % (4 * kT), h = f / (2 * kT), i = f % (2 * kT) / 2;
-    constexpr int rb = 2 * i;
-    const int base = f % 2 ? kSide + kB * wm : kB * wn;
-    if constexpr (r < 4 * kT) {
-      const v4i v = *reinterpret_cast<const v4i*>(lds + ring * kStage + (base + rb + tile) * 1024 + 16 * slot + 512 * h);
-      if constexpr (f % 2)
-        b[h][i] = v;
-      else
-        a[h][i] = v;
-    } else {
-      const int v = *reinterpret_cast<const int*>(lds + 4 * kStage + (base + rb + tile) * 256 + 4 * slot + 128 * h);
-      if constexpr (f % 2)
-        wb[h][i] = v;
-      else
-        wa[h][i] = v;
-    }
+  // fragments of 32 rows x 64 columns (two blocks' rows, half h of their columns) of this half step
+  // and of the next, and the words of scales of this group of four steps and of the next
+  v4i fa[2][TN], fb[2][TM];
+  int sa[2][2][TN], sb[2][2][TM];
+  const uint8_t* lane_codes = lds + ((lane >> 4) & 1) * 1024 + 16 * (16 * (lane >> 5) + (lane & 15));
+  const uint8_t* lane_scales = lds + kR * kStage + ((lane >> 4) & 1) * 256 + 4 * (16 * (lane >> 5) + (lane & 15));
+  // the reads of a half step, one at a time so that they can be spread over its matrix
+  // instructions: TN + TM fragments of half h, and with scales the words of both halves
+  auto read_one = [&](auto rr, int slot, auto hh, v4i (&a)[TN], v4i (&b)[TM], int (&wa)[2][TN], int (&wb)[2][TM]) {
+    constexpr int r = rr, h = hh;
+    if constexpr (r < TN)
+      a[r] = *reinterpret_cast<const v4i*>(lane_codes + slot * kStage + (kN * wn + 2 * r) * 1024 + 512 * h);
+    else if constexpr (r < TN + TM)
+      b[r - TN] =
+          *reinterpret_cast<const v4i*>(lane_codes + slot * kStage + (2 * kN + kM * wm + 2 * (r - TN)) * 1024 + 512 * h);
+    else if constexpr (r < 3 * TN + TM)
+      wa[(r - TN - TM) / TN][(r - TN - TM) % TN] = *reinterpret_cast<const int*>(
+          lane_scales + (kN * wn + 2 * ((r - TN - TM) % TN)) * 256 + 128 * ((r - TN - TM) / TN));
+    else
+      wb[(r - 3 * TN - TM) / TM][(r - 3 * TN - TM) % TM] = *reinterpret_cast<const int*>(
+          lane_scales + (2 * kN + kM * wm + 2 * ((r - 3 * TN - TM) % TM)) * 256 + 128 * ((r - 3 * TN - TM) / TM));
   };
+  constexpr int kFrags = TN + TM, kAll = 3 * kFrags;
+  const std::integral_constant<int, 0> half0;
+  const std::integral_constant<int, 1> half1;
 
-  // loads per stage: kLoads, and the scales' with every fourth (stage 0, 4, ...)
-  constexpr int L = kLoads, S = kScaleLoads;
   const int last = tiles - 1;
-  issue(0, 0, true);
-  if (last >= 1) issue(1, 1, false);
-  if (last >= 2) issue(2, 2, false);
-  if (last >= 3) {
-    issue(3, 3, false);
-    ring_wait<3 * L>();
-  } else {
+#pragma unroll
+  for (int c = 0; c < kR; ++c)
+    if (c <= last) issue(c, c, c == 0);
+  if (last >= kR - 1)
+    ring_wait<(kR - 1) * L>();
+  else
     ring_wait<0>();
-  }
-  static_for<8 * kT>([&](auto r) { read_one(r, 0, fa[0], fb[0], sa[0], sb[0]); });
+  static_for<kAll>([&](auto r) { read_one(r, 0, half0, fa[0], fb[0], sa[0], sb[0]); });
 
+  int slot = 0;
   for (int c0 = 0; c0 < tiles; c0 += 8) {
     bool done = false;
     static_for<8>([&](auto tt) {
-      constexpr int u = tt, t = u % 4, cur = u % 2, g = u / 4;  // step, its byte of the scales, buffers
+      constexpr int u = tt, t = u % 4, g = u / 4;  // step, its byte of the scales, buffer of their words
       const int c = c0 + u;
       if (done || c >= tiles) {
         done = true;
         return;
       }
-      // stage c + 1 has landed where at most the loads of c + 2 and c + 3 are in flight
-      if (c + 3 <= last)
-        ring_wait<2 * L + ((t == 1 || t == 2) ? S : 0)>();
+      // Half a step: TN batches of TM matrix instructions, with the reads of the next half in front
+      // of all but the last, whose time (and the barrier's) covers the last read's latency.
+      auto half = [&](auto hh, auto reads, int rslot) {
+        constexpr int h = hh, kReads = decltype(reads)::value, kBatch = (kReads + TN - 2) / (TN - 1);
+        static_for<TN>([&](auto bb) {
+          constexpr int i = bb;
+          static_for<kBatch>([&](auto rr) {
+            if constexpr (i * kBatch + rr < kReads)
+              read_one(std::integral_constant<int, i * kBatch + rr>{}, rslot, std::integral_constant<int, 1 - h>{},
+                       fa[1 - h], fb[1 - h], sa[1 - g], sb[1 - g]);
+          });
+#pragma unroll
+          for (int j = 0; j < TM; ++j)
+            acc[i][j] = mx_mfma32<t, t>(fa[h][i], fb[h][j], acc[i][j], sa[g][h][i], sb[g][h][j]);
+          __builtin_amdgcn_sched_barrier(0);
+        });
+      };
+      half(half0, std::integral_constant<int, kFrags>{}, slot);
+      // stage c + 1 has landed where at most the loads of c + 2 .. c + kR - 1 are in flight, and stage
+      // c has been read by every wave: its slot takes stage c + kR
+      if (c + kR - 1 <= last)
+        ring_wait<(kR - 2) * L + ((t == 2 || (kR == 4 && t == 1)) ? S : 0)>();
       else
         ring_wait<0>();
-      // 2 kT batches of kT matrix instructions; the reads of the next step go in front of all but the
-      // last two, whose time covers the latency of the last read, and the direct loads after the
-      // first.  (The reads of the step after the last fetch what is in LDS, for nothing.)
-      constexpr int kReads = t == 3 ? 8 * kT : 4 * kT, kBatch = (kReads + 2 * kT - 3) / (2 * kT - 2);
-      static_for<2 * kT>([&](auto bb) {
-        constexpr int h = bb / kT, i = bb % kT;
-        static_for<kBatch>([&](auto rr) {
-          if constexpr (bb * kBatch + rr < kReads)
-            read_one(std::integral_constant<int, bb * kBatch + rr>{}, (t + 1) % 4, fa[1 - cur], fb[1 - cur], sa[1 - g],
-                     sb[1 - g]);
-        });
-#pragma unroll
-        for (int j = 0; j < kT; ++j)
-          acc[i][j] = mx_mfma32<t, t>(fa[cur][h][i], fb[cur][h][j], acc[i][j], sa[g][h][i], sb[g][h][j]);
-        __builtin_amdgcn_sched_barrier(0);
-        if constexpr (bb == 0) {
-          if (c + 4 <= last) issue(c + 4, t, t == 0);
-        }
-      });
+      const int next = slot + 1 == kR ? 0 : slot + 1;
+      if (c + kR <= last) issue(c + kR, slot, (t + kR) % 4 == 0);
+      // (the reads of the step after the last fetch what is in LDS, for nothing)
+      half(half1, std::integral_constant<int, t == 3 ? kAll : kFrags>{}, next);
+      slot = next;
     });
   }
 
   // Each wave turns its accumulators (lane l of a 32 x 32 tile: token l % 32, four times four
   // consecutive outputs) into whole rows through its quarter of the ring, 32 tokens at a time.  The
   // row stride puts the 32 tokens of a write on different banks.
-  constexpr int kRow = 16 * kB * sizeof(TY) + (sizeof(TY) == 4 ? 16 : 8);  // bytes
+  constexpr int kRow = 16 * kN * sizeof(TY) + (sizeof(TY) == 4 ? 16 : 8);  // bytes
   constexpr int kPer = 16 / sizeof(TY);                                    // outputs of a 16-byte piece
-  constexpr int kPieces = 16 * kB / kPer;                                  // pieces of a row
-  static_assert(32 * kRow <= kStage, "a slab fits the wave's quarter");
+  constexpr int kPieces = 16 * kN / kPer;                                  // pieces of a row
+  static_assert(32 * kRow <= kR * kStage / 4, "a slab fits the wave's quarter");
   ring_wait<0>();  // the other waves have read their last fragments
-  uint8_t* slab = lds + wave * kStage;
+  uint8_t* slab = lds + wave * (kR * kStage / 4);
 #pragma unroll
-  for (int j = 0; j < kT; ++j) {
+  for (int j = 0; j < TM; ++j) {
 #pragma unroll
-    for (int i = 0; i < kT; ++i) {
+    for (int i = 0; i < TN; ++i) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         uint8_t* at = slab + (lane & 31) * kRow + (32 * i + 8 * q + 4 * (lane >> 5)) * sizeof(TY);
@@ -240,8 +238,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kB == 8 ? 1
       }
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // a wave's own writes, read by its other lanes
-    const int64_t m0 = ((int64_t)tm * kSide + kB * wm + 2 * j) * 16;
-    const int64_t n0 = ((int64_t)tn * kSide + kB * wn) * 16;
+    const int64_t m0 = ((int64_t)tm * 2 * kM + kM * wm + 2 * j) * 16;
+    const int64_t n0 = ((int64_t)tn * 2 * kN + kN * wn) * 16;
 #pragma unroll 8
     for (int t = 0; t < 32 * kPieces / 64; ++t) {
       const int piece = 64 * t + lane, r = piece / kPieces, c = piece % kPieces;
@@ -262,17 +260,16 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(kB == 8 ? 1
   }
 }
 
-template <int kB, typename TY>
-hipError_t launch(const uint8_t* codes, const uint8_t* scales, const uint8_t* xcodes, const uint8_t* xscales,
-                  int64_t M, int64_t N, int64_t K, void* Y, hipStream_t s) {
-  const MxGemmPlan p = plan_mx_gemm(M, N, K);
-  constexpr int lds = 4 * 4 * kB * 1024 + 4 * kB * 256;
-  const void* fn = reinterpret_cast<const void*>(&k_mx_gemm<kB, TY>);
+template <int kN, int kM, int kR, typename TY>
+hipError_t launch(const MxGemmPlan& p, const uint8_t* codes, const uint8_t* scales, const uint8_t* xcodes,
+                  const uint8_t* xscales, int64_t M, int64_t N, int64_t K, void* Y, hipStream_t s) {
+  constexpr int lds = 2 * (kN + kM) * (kR * 1024 + 256);
+  const void* fn = reinterpret_cast<const void*>(&k_mx_gemm<kN, kM, kR, TY>);
   if (lds > 65536) {
     const hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
   }
-  k_mx_gemm<kB, TY><<<dim3((unsigned)(p.tiles_m * p.tiles_n)), 256, lds, s>>>(
+  k_mx_gemm<kN, kM, kR, TY><<<dim3((unsigned)(p.tiles_m * p.tiles_n)), 256, lds, s>>>(
       codes, scales, xcodes, xscales, M, N, (int)mx_tiles(K), (int)mx_groups(K), (int)mx_row_blocks(N),
       (int)mx_row_blocks(M), (int)p.tiles_m, (int)(p.tiles_m * p.tiles_n), static_cast<TY*>(Y));
   return hipGetLastError();
@@ -282,22 +279,26 @@ hipError_t launch(const uint8_t* codes, const uint8_t* scales, const uint8_t* xc
 
 MxGemmPlan plan_mx_gemm(int64_t M, int64_t N, int64_t K) {
   MxGemmPlan p;
-  auto tiles = [&](int64_t side) { return ((M + side - 1) / side) * ((N + side - 1) / side); };
-  p.side = tiles(256) >= 128 ? 256 : 128;
-  p.tiles_m = (M + p.side - 1) / p.side;
-  p.tiles_n = (N + p.side - 1) / p.side;
+  auto tiles = [&](int64_t tm, int64_t tn) { return ((M + tm - 1) / tm) * ((N + tn - 1) / tn); };
+  // 2048 x 6912 x 2560: 30.1 us with 256 x 128 tiles, 34.4 with 128 x 128; 512 x 8192 x 8192, where the
+  // large tiles are 128 on 256 compute units: 37.7 and 27.8
+  p.tile_m = 128;
+  p.tile_n = tiles(128, 256) >= 256 ? 256 : 128;
+  p.tiles_m = (M + p.tile_m - 1) / p.tile_m;
+  p.tiles_n = (N + p.tile_n - 1) / p.tile_n;
   return p;
 }
 
 hipError_t launch_mx_gemm(const uint8_t* codes, const uint8_t* scales, const uint8_t* xcodes,
                           const uint8_t* xscales, int64_t M, int64_t N, int64_t K, void* Y, int ybf16,
                           hipStream_t s) {
-  const bool big = plan_mx_gemm(M, N, K).side == 256;
-  if (ybf16)
-    return big ? launch<8, uint16_t>(codes, scales, xcodes, xscales, M, N, K, Y, s)
-               : launch<4, uint16_t>(codes, scales, xcodes, xscales, M, N, K, Y, s);
-  return big ? launch<8, float>(codes, scales, xcodes, xscales, M, N, K, Y, s)
-             : launch<4, float>(codes, scales, xcodes, xscales, M, N, K, Y, s);
+  const MxGemmPlan p = plan_mx_gemm(M, N, K);
+  auto go = [&](auto yt) {
+    using TY = decltype(yt);
+    if (p.tile_n == 256) return launch<8, 4, 3, TY>(p, codes, scales, xcodes, xscales, M, N, K, Y, s);
+    return launch<4, 4, 4, TY>(p, codes, scales, xcodes, xscales, M, N, K, Y, s);
+  };
+  return ybf16 ? go(uint16_t{}) : go(float{});
 }
 
 }  // namespace bl

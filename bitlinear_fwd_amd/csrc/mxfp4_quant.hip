@@ -19,12 +19,6 @@
 namespace bl {
 namespace {
 
-// max over the four lanes of a quad
-__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xf, 0xf, true));
-  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xf, 0xf, true));
-}
-
 template <typename T, bool kValues>
 __global__ __launch_bounds__(256) void k_mx_quant(const T* __restrict__ X, int64_t R, int64_t K, int64_t tiles,
                                                   int64_t groups, int64_t units, uint8_t* __restrict__ codes,
@@ -35,31 +29,23 @@ __global__ __launch_bounds__(256) void k_mx_quant(const T* __restrict__ X, int64
     const int64_t rb = u / groups, c4 = u % groups;
     const int64_t row = rb * kMxRows + r;
     const int64_t col = c4 * kMxGroupCols + 32 * b + 8 * p;
-    float v[4][8];
+    Raw8<T> v[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const int64_t left = row < R ? K - (col + kMxCols * t) : 0;
-      load8(X + row * K + col + kMxCols * t, left, v[t]);
+      v[t] = load_raw8(X + row * K + col + kMxCols * t, left);
     }
     uint32_t word = 0;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      uint32_t top = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[t][i]) & 0x7fffffffu);
-      const uint32_t e = mx_scale_byte(quad_max(top));
+      uint32_t e;
+      const uint32_t q = mx_quantize8(v[t], e);
       word |= e << (8 * t);
-      const float s = mx_scale(e == 255 ? 127 : e);
-      uint32_t q = 0;
-      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[t][0], v[t][1], s, 0);
-      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[t][2], v[t][3], s, 1);
-      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[t][4], v[t][5], s, 2);
-      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[t][6], v[t][7], s, 3);
-      if (e == 255) q = 0;
       const int64_t c = 4 * c4 + t;
       if (c < tiles)
         *reinterpret_cast<uint32_t*>(codes + (rb * tiles + c) * kMxTileBytes + 16 * (16 * b + r) + 4 * p) = q;
       if constexpr (kValues) {
+        const float s = mx_scale(e == 255 ? 127 : e);
         const v2f f0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 0);
         const v2f f1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 1);
         const v2f f2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 2);
