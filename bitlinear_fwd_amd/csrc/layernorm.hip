@@ -54,29 +54,6 @@ __device__ __forceinline__ void row_sum(F (&v)[kN], F* red, int i0 = threadIdx.x
   }
 }
 
-// store8 past the caches: for outputs larger than they hold.
-typedef uint32_t v4u __attribute__((ext_vector_type(4)));
-typedef v4u v4u_unaligned __attribute__((aligned(2)));
-template <typename T>
-__device__ __forceinline__ void stream8(T* p, int64_t n, const float (&v)[8]) {
-  if (n < 8) {
-    store8(p, n, v);
-  } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      v4u w;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(v[4 * h + i]);
-      __builtin_nontemporal_store(w, reinterpret_cast<v4u_unaligned*>(p + 4 * h));
-    }
-  } else {
-    v4u w;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = bf16_pair(v[2 * i], v[2 * i + 1]);
-    __builtin_nontemporal_store(w, reinterpret_cast<v4u_unaligned*>(p));
-  }
-}
-
 // One row per wave (kWave) or per workgroup, kG groups of 8 elements per thread (thread i of the T
 // that share the row takes groups i, i + T, ...).  A workgroup walks over rows with the next row's
 // loads in flight and (kHold) weight and bias in registers: read for every row they are four
@@ -150,7 +127,7 @@ __global__ __launch_bounds__(kWave ? 256 : 1024) void k_layernorm(const T* __res
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[g][i] = v[g][i] * rstd * w[g][i] + b[g][i];
       if constexpr (kWave || kG > 1)
-        stream8(Y + row * K + col, K - col, v[g]);
+        stream8(Y + row * K + col, K - col, v[g], whole_pieces(K));
       else
         store8(Y + row * K + col, K - col, v[g]);
     }
@@ -280,7 +257,7 @@ __global__ __launch_bounds__(kG == 1 ? 1024 : 768) void k_layernorm_bwd(
         const int64_t col = 8 * (int64_t)(i0 + g * threads);
 #pragma unroll
         for (int i = 0; i < 8; ++i) d[g][i] = rstd * (d[g][i] - c[0] - x[g][i] * c[1]);
-        store8(dX + row * K + col, row < M ? K - col : 0, d[g]);
+        stream8(dX + row * K + col, row < M ? K - col : 0, d[g], whole_pieces(K));
       }
     }
   }

@@ -56,7 +56,7 @@ __global__ __launch_bounds__(256) void k_mx_quant(const T* __restrict__ X, int64
           for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(0x7fc00000u);
         }
         const int64_t left = row < R ? K - (col + kMxCols * t) : 0;
-        store8(values + row * K + col + kMxCols * t, left, f);
+        stream8(values + row * K + col + kMxCols * t, left, f, whole_pieces(K));
       }
     }
     if (p == 0) *reinterpret_cast<uint32_t*>(scales + ((rb * groups + c4) * 64 + 16 * b + r) * 4) = word;
