@@ -7,7 +7,12 @@
 // would leave compute units idle), sized so that two workgroups share a compute unit: one's first
 // loads and output stores run under the other's matrix instructions.  Measured: tiles of 256 x 256
 // with one workgroup to a unit use each byte more often, but load, compute and store in turn (2048 x
-// 28672 x 8192 to bf16 with the quantiser 273 us, against 250; 8192^3 283 us against 276).
+// 28672 x 8192 to bf16 with the quantiser 273 us, against 250; 8192^3 to bf16 283 us against 270,
+// 4.08 PFLOP/s).  What bounds the large shapes now: with all-zero operands a 256 x 256 x 128 step of a
+// compute unit took 0.71 us, with random ones 0.92 - 1.0 (0.43 at the nominal clock): power, then LDS
+// (1150 of its cycles to 1024 of the matrix cores').  2048 x 6912 x 2560 to fp32, 27.2 us: 216 tiles of
+// 256 x 256 worth of work on 256 compute units, and 57 MB of output.  Output rows are stored past the
+// caches: 26.4 us against 30.3 there.
 //   * 32x32x64 instructions: with the 16x16x128 form the waves cannot issue fast enough (5.4 against
 //     9.6 PFLOP/s from registers, one wave per SIMD).  On random data power holds both back.
 //   * The tile layout is the operand layout, so a 1 KiB tile goes from global memory straight into
@@ -70,22 +75,25 @@ __device__ __forceinline__ T* uniform_ptr(T* p) {
               (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
 }
 
-// Four waves in 2 x 2, each with kN x kM blocks of 16 weight rows and 16 tokens: output tiles of
-// 32 kM tokens x 32 kN outputs.  kR stages of 128 columns in the ring.
+constexpr int kWN = 2, kWM = 2;  // waves of a workgroup along the outputs and along the tokens
+
+// Each wave has kN x kM blocks of 16 weight rows and 16 tokens: output tiles of 16 kWM kM tokens x 16
+// kWN kN outputs.  kR stages of 128 columns in the ring.
 template <int kN, int kM, int kR, typename TY>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void
-k_mx_gemm(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, const uint8_t* __restrict__ xcodes,
+__global__ __launch_bounds__(64 * kWN * kWM) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_mx_gemm(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, const uint8_t* __restrict__ xcodes,
           const uint8_t* __restrict__ xscales, int64_t M, int64_t N, int tiles, int groups, int nblocks, int xblocks,
           int tiles_m, int total, TY* __restrict__ Y) {
-  constexpr int kBlocks = 2 * (kN + kM);          // row blocks of a stage: weights, then tokens
+  constexpr int W = kWN * kWM;
+  constexpr int BN = kWN * kN, BM = kWM * kM;     // row blocks of a stage: weights, then tokens
+  constexpr int kBlocks = BN + BM;
   constexpr int kStage = kBlocks * 1024;          // bytes
-  constexpr int L = kBlocks / 4;                  // direct loads per wave and stage
-  constexpr int S = (kBlocks / 4 + 3) / 4;        // and per wave and four stages, of scales
+  constexpr int L = kBlocks / W;                  // direct loads per wave and stage
+  constexpr int S = (kBlocks / 4 + W - 1) / W;    // and per wave and four stages, of scales
   constexpr int TN = kN / 2, TM = kM / 2;         // 32-row tiles of a wave
   static_assert(L % 2 == 0, "direct loads come in pairs");
   extern __shared__ uint8_t lds[];                // the ring, then kBlocks x 256 bytes of scales
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wn = wave & 1, wm = wave >> 1;
+  const int wn = wave % kWN, wm = wave / kWN;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)lds;
 
   // tile of this workgroup: contiguous runs per XCD
@@ -98,8 +106,7 @@ k_mx_gemm(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
 
   // row block t of a stage (past the last: the last again, not stored)
   auto block = [&](int t, const uint8_t* w, const uint8_t* x, int64_t bytes) {
-    return t < 2 * kN ? w + min(tn * 2 * kN + t, nblocks - 1) * bytes
-                      : x + min(tm * 2 * kM + t - 2 * kN, xblocks - 1) * bytes;
+    return t < BN ? w + min(tn * BN + t, nblocks - 1) * bytes : x + min(tm * BM + t - BN, xblocks - 1) * bytes;
   };
   // this wave's direct loads: blocks L wave .. of the stage, and of the scales KiB S wave .. (four
   // blocks each; waves past the last repeat it, so that all have the same number in flight)
@@ -146,13 +153,13 @@ k_mx_gemm(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
       a[r] = *reinterpret_cast<const v4i*>(lane_codes + slot * kStage + (kN * wn + 2 * r) * 1024 + 512 * h);
     else if constexpr (r < TN + TM)
       b[r - TN] =
-          *reinterpret_cast<const v4i*>(lane_codes + slot * kStage + (2 * kN + kM * wm + 2 * (r - TN)) * 1024 + 512 * h);
+          *reinterpret_cast<const v4i*>(lane_codes + slot * kStage + (BN + kM * wm + 2 * (r - TN)) * 1024 + 512 * h);
     else if constexpr (r < 3 * TN + TM)
       wa[(r - TN - TM) / TN][(r - TN - TM) % TN] = *reinterpret_cast<const int*>(
           lane_scales + (kN * wn + 2 * ((r - TN - TM) % TN)) * 256 + 128 * ((r - TN - TM) / TN));
     else
       wb[(r - 3 * TN - TM) / TM][(r - 3 * TN - TM) % TM] = *reinterpret_cast<const int*>(
-          lane_scales + (2 * kN + kM * wm + 2 * ((r - 3 * TN - TM) % TM)) * 256 + 128 * ((r - 3 * TN - TM) / TM));
+          lane_scales + (BN + kM * wm + 2 * ((r - 3 * TN - TM) % TM)) * 256 + 128 * ((r - 3 * TN - TM) / TM));
   };
   constexpr int kFrags = TN + TM, kAll = 3 * kFrags;
   const std::integral_constant<int, 0> half0;
@@ -211,14 +218,15 @@ k_mx_gemm(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
   }
 
   // Each wave turns its accumulators (lane l of a 32 x 32 tile: token l % 32, four times four
-  // consecutive outputs) into whole rows through its quarter of the ring, 32 tokens at a time.  The
+  // consecutive outputs) into whole rows through its share of the ring, 32 tokens at a time.  The
   // row stride puts the 32 tokens of a write on different banks.
   constexpr int kRow = 16 * kN * sizeof(TY) + (sizeof(TY) == 4 ? 16 : 8);  // bytes
   constexpr int kPer = 16 / sizeof(TY);                                    // outputs of a 16-byte piece
   constexpr int kPieces = 16 * kN / kPer;                                  // pieces of a row
-  static_assert(32 * kRow <= kR * kStage / 4, "a slab fits the wave's quarter");
+  static_assert(32 * kRow <= kR * kStage / W, "a slab fits the wave's share of the ring");
+  const bool stream = whole_pieces(N);
   ring_wait<0>();  // the other waves have read their last fragments
-  uint8_t* slab = lds + wave * (kR * kStage / 4);
+  uint8_t* slab = lds + wave * (kR * kStage / W);
 #pragma unroll
   for (int j = 0; j < TM; ++j) {
 #pragma unroll
@@ -238,22 +246,33 @@ k_mx_gemm(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
       }
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // a wave's own writes, read by its other lanes
-    const int64_t m0 = ((int64_t)tm * 2 * kM + kM * wm + 2 * j) * 16;
-    const int64_t n0 = ((int64_t)tn * 2 * kN + kN * wn) * 16;
+    const int64_t m0 = ((int64_t)tm * BM + kM * wm + 2 * j) * 16;
+    const int64_t n0 = ((int64_t)tn * BN + kN * wn) * 16;
+    if (stream && m0 + 32 <= M && n0 + 16 * kN <= N) {  // a whole slab, past the caches
 #pragma unroll 8
-    for (int t = 0; t < 32 * kPieces / 64; ++t) {
-      const int piece = 64 * t + lane, r = piece / kPieces, c = piece % kPieces;
-      const int64_t m = m0 + r, n = n0 + kPer * c, left = m < M ? N - n : 0;
-      TY* y = Y + m * N + n;
-      TY v[kPer];
-      __builtin_memcpy(v, slab + r * kRow + 16 * c, 8);
-      __builtin_memcpy(v + kPer / 2, slab + r * kRow + 16 * c + 8, 8);
-      if (left >= kPer) {
-        __builtin_memcpy(y, v, 16);
-      } else {
+      for (int t = 0; t < 32 * kPieces / 64; ++t) {
+        const int piece = 64 * t + lane, r = piece / kPieces, c = piece % kPieces;
+        v4u v;
+        __builtin_memcpy(&v, slab + r * kRow + 16 * c, 8);
+        __builtin_memcpy(reinterpret_cast<char*>(&v) + 8, slab + r * kRow + 16 * c + 8, 8);
+        __builtin_nontemporal_store(v, reinterpret_cast<v4u_unaligned*>(Y + (m0 + r) * N + n0 + kPer * c));
+      }
+    } else {
+#pragma unroll 8
+      for (int t = 0; t < 32 * kPieces / 64; ++t) {
+        const int piece = 64 * t + lane, r = piece / kPieces, c = piece % kPieces;
+        const int64_t m = m0 + r, n = n0 + kPer * c, left = m < M ? N - n : 0;
+        TY* y = Y + m * N + n;
+        TY v[kPer];
+        __builtin_memcpy(v, slab + r * kRow + 16 * c, 8);
+        __builtin_memcpy(v + kPer / 2, slab + r * kRow + 16 * c + 8, 8);
+        if (left >= kPer) {
+          __builtin_memcpy(y, v, 16);
+        } else {
 #pragma unroll
-        for (int e = 0; e < kPer; ++e)
-          if (e < left) y[e] = v[e];
+          for (int e = 0; e < kPer; ++e)
+            if (e < left) y[e] = v[e];
+        }
       }
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read before the next slab is written
@@ -263,13 +282,14 @@ k_mx_gemm(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
 template <int kN, int kM, int kR, typename TY>
 hipError_t launch(const MxGemmPlan& p, const uint8_t* codes, const uint8_t* scales, const uint8_t* xcodes,
                   const uint8_t* xscales, int64_t M, int64_t N, int64_t K, void* Y, hipStream_t s) {
-  constexpr int lds = 2 * (kN + kM) * (kR * 1024 + 256);
-  const void* fn = reinterpret_cast<const void*>(&k_mx_gemm<kN, kM, kR, TY>);
+  constexpr int lds = (kWN * kN + kWM * kM) * (kR * 1024 + 256);
+  const auto fn = &k_mx_gemm<kN, kM, kR, TY>;
   if (lds > 65536) {
-    const hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
   }
-  k_mx_gemm<kN, kM, kR, TY><<<dim3((unsigned)(p.tiles_m * p.tiles_n)), 256, lds, s>>>(
+  fn<<<dim3((unsigned)(p.tiles_m * p.tiles_n)), 64 * kWN * kWM, lds, s>>>(
       codes, scales, xcodes, xscales, M, N, (int)mx_tiles(K), (int)mx_groups(K), (int)mx_row_blocks(N),
       (int)mx_row_blocks(M), (int)p.tiles_m, (int)(p.tiles_m * p.tiles_n), static_cast<TY*>(Y));
   return hipGetLastError();
