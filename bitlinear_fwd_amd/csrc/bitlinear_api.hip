@@ -40,9 +40,9 @@ hipError_t mx_forward(const uint8_t* codes, const uint8_t* scales, const uint8_t
                                      : bl::launch_mx_gemm(codes, scales, xcodes, xscales, M, N, K, Y, bf16, s);
 }
 
-// Sizes of an MXFP4 product: both matrices addressable, and a launchable number of tiles.
+// Sizes of an MXFP4 product: both matrices addressable, and a launchable number of output tiles.
 bool mx_product_ok(int64_t M, int64_t N, int64_t K) {
-  return M <= kMaxCount / K && N <= kMaxCount / K && bl::mx_row_blocks(M) <= (int64_t(1) << 30) / bl::mx_row_blocks(N);
+  return M <= kMaxCount / K && N <= kMaxCount / K && (M + 127) / 128 <= (int64_t(1) << 23) / ((N + 127) / 128);
 }
 
 int grouped_impl(const bl_matrix* mats, int count, const void* X, int dt, int64_t M, int64_t K, const float* gain,

@@ -54,17 +54,22 @@ __device__ __forceinline__ v16f mx_mfma32(v4i a, v4i b, v16f acc, int sa, int sb
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wa, wb, acc, 4, 4, TA, sa, TB, sb);
 }
 
-// Scale byte of a block whose largest magnitude has the fp32 bits `bits` (sign cleared): the
-// power of two of that magnitude over 4, the grid's largest power (2^-127 at least); 255 where
-// the block holds a NaN or an infinity.
-__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t bits) {
-  const uint32_t field = bits >> 23;
-  if (field == 255) return 255;
-  return field < 2 ? 0 : field - 2;
+// Scale of a block from the fp32 bits of its largest magnitude: e = max(exponent field - 2, 0), the
+// power of two of that magnitude over 4, the grid's largest power; the number 2^(e - 127) (e = 0: a
+// subnormal).  bad: the block holds a NaN or an infinity (e is 255 then, the scale any number).
+struct MxScale {
+  uint32_t e;
+  float scale;
+  bool bad;
+};
+__device__ __forceinline__ MxScale mx_scale(uint32_t top) {
+  const uint32_t field = top >> 23, e = max(field, 2u) - 2;
+  MxScale s;
+  s.bad = field == 255;
+  s.e = s.bad ? 255 : e;
+  s.scale = __uint_as_float(max(e << 23, 0x00400000u));
+  return s;
 }
-
-// The fp32 number 2^(e - 127), e < 255 (e = 0: the subnormal 2^-127).
-__device__ __forceinline__ float mx_scale(uint32_t e) { return __uint_as_float(e ? e << 23 : 0x00400000u); }
 
 // Eight consecutive elements of a row as they are in memory (fp32, or bf16 as uint16_t); elements
 // past n are 0.  Whole groups are read 16 bytes at a time at any alignment (the target's global loads
@@ -106,39 +111,44 @@ __device__ __forceinline__ void load8(const T* p, int64_t n, float (&v)[8]) {
   widen8(load_raw8(p, n), v);
 }
 
-// Codes of eight values of a block that a quad of lanes shares (32 columns, lane p of it columns
-// 8 p ..), one 4-bit code after the other, and the block's scale byte e.
-__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xf, 0xf, true));
-  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xf, 0xf, true));
-}
-__device__ __forceinline__ uint32_t mx_quantize8(const Raw8<float>& r, uint32_t& e) {
+// The fp32 bits of the largest magnitude of eight elements (bf16: as 16-bit integers, two at a time).
+__device__ __forceinline__ uint32_t top_bits(const Raw8<float>& r) {
   uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) top = max(top, r.w[i] & 0x7fffffffu);
-  e = mx_scale_byte(quad_max(top));
-  const float s = mx_scale(e == 255 ? 127 : e);
-  uint32_t q = 0;
-  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, __uint_as_float(r.w[0]), __uint_as_float(r.w[1]), s, 0);
-  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, __uint_as_float(r.w[2]), __uint_as_float(r.w[3]), s, 1);
-  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, __uint_as_float(r.w[4]), __uint_as_float(r.w[5]), s, 2);
-  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, __uint_as_float(r.w[6]), __uint_as_float(r.w[7]), s, 3);
-  return e == 255 ? 0 : q;
+  return top;
 }
-// bf16: the largest magnitude as 16-bit integers, two at a time, and the conversion from bf16 pairs.
-__device__ __forceinline__ uint32_t mx_quantize8(const Raw8<uint16_t>& r, uint32_t& e) {
+__device__ __forceinline__ uint32_t top_bits(const Raw8<uint16_t>& r) {
   typedef unsigned short v2u __attribute__((ext_vector_type(2)));
   v2u m = __builtin_bit_cast(v2u, r.w[0] & 0x7fff7fffu);
 #pragma unroll
   for (int i = 1; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(v2u, r.w[i] & 0x7fff7fffu));
-  e = mx_scale_byte(quad_max((uint32_t)max(m.x, m.y) << 16));
-  const float s = mx_scale(e == 255 ? 127 : e);
+  return (uint32_t)max(m.x, m.y) << 16;
+}
+// The larger of two neighbouring lanes' values, and of the four lanes of a quad.
+__device__ __forceinline__ uint32_t pair_max(uint32_t v) {
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xf, 0xf, true));
+}
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+  v = pair_max(v);
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xf, 0xf, true));
+}
+// The codes of eight elements, low nibble first (zeros where the block is bad).
+__device__ __forceinline__ uint32_t codes8(const Raw8<float>& r, const MxScale& s) {
   uint32_t q = 0;
-  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(v2bf, r.w[0]), s, 0);
-  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(v2bf, r.w[1]), s, 1);
-  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(v2bf, r.w[2]), s, 2);
-  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(v2bf, r.w[3]), s, 3);
-  return e == 255 ? 0 : q;
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, __uint_as_float(r.w[0]), __uint_as_float(r.w[1]), s.scale, 0);
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, __uint_as_float(r.w[2]), __uint_as_float(r.w[3]), s.scale, 1);
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, __uint_as_float(r.w[4]), __uint_as_float(r.w[5]), s.scale, 2);
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, __uint_as_float(r.w[6]), __uint_as_float(r.w[7]), s.scale, 3);
+  return s.bad ? 0 : q;
+}
+__device__ __forceinline__ uint32_t codes8(const Raw8<uint16_t>& r, const MxScale& s) {
+  uint32_t q = 0;
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(v2bf, r.w[0]), s.scale, 0);
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(v2bf, r.w[1]), s.scale, 1);
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(v2bf, r.w[2]), s.scale, 2);
+  q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(v2bf, r.w[3]), s.scale, 3);
+  return s.bad ? 0 : q;
 }
 
 // Two fp32 values to bf16 bits, to nearest with ties to even (one instruction; NaN stays NaN).

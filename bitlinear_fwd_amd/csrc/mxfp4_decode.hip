@@ -1,10 +1,17 @@
 // MXFP4 product for few tokens: Y[M][N] = sum_k Xv[m][k] Wv[n][k] with both matrices as codes
 // and scales in the layout of mxfp4.h, fp32 accumulation in the matrix cores.
 //
-// A workgroup takes one 16-row block of the weights and TG groups of 16 tokens; its waves split
-// the columns in groups of four tiles and add their sums in LDS at the end, in wave order.  Each
-// weight tile is loaded once (one coalesced 1 KiB wave load straight into operand registers) and
-// serves TG matrix instructions.
+// Bound by the weights' bytes (17/32 byte each).  Up to 16 tokens (k_mx_few) the tokens' codes live in
+// LDS and weights stream past: 1 x 28672 x 8192 21.9 us (5.7 TB/s of weights; a large copy moves 5.2),
+// 1 x 8192 x 28672 from fp32 22.9, 1 x 6912 x 2560 4.1.  What took it there from 24 and 29 us: one
+// launch instead of two, and workgroups that stay (16 waves to a unit) and keep the next group's
+// loads in flight over the sums of this row block.  Loads past the caches, as the weights are read
+// once.
+// More tokens (k_mx_decode): a workgroup takes one 16-row block of the weights and TG groups of 16
+// tokens; its waves split the columns in groups of four tiles and add their sums in LDS at the end, in
+// wave order.  Each weight tile is loaded once (one coalesced 1 KiB wave load straight into operand
+// registers) and serves TG matrix instructions; the tokens' tiles come from L2, which is what bounds
+// it (0.1 us for a thousand products of a weight tile with 16 tokens).
 #include "mxfp4.h"
 
 #include <algorithm>
@@ -78,10 +85,10 @@ enum { kFromCodes, kFromBf16, kFromF32 };
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 // Up to 16 tokens whose codes fit LDS.  The workgroup first fills LDS with the tokens' codes and
-// scales (kFromCodes: copied; else quantised there from X[M][K], four lanes to a block as in the
-// quantiser), then walks over row blocks of the weights: its waves split the columns in groups of
-// four tiles, the next group's loads in flight, and add their sums through LDS in wave order.
-// LDS: codes [4 groups tiles][4 blocks][M] x 16 bytes, scales [groups][4 blocks][M] words, sums.
+// scales (kFromCodes: copied; else quantised there from X[M][K], two lanes to a block), then walks
+// over row blocks of the weights: its waves split the columns in groups of four tiles, the next
+// group's loads in flight, and add their sums through LDS in wave order.
+// LDS: sums, codes [4 groups tiles][4 blocks][M] x 16 bytes, scale bytes [4 groups tiles][4 blocks][M].
 // magic: ceil(2^32 / M) (M > 1); i / M is the high word of i magic for the few thousand blocks that
 // fit LDS.
 template <int kSrc, typename TY>
@@ -94,7 +101,7 @@ __global__ __launch_bounds__(1024) void k_mx_few(const uint8_t* __restrict__ cod
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = blockDim.x >> 6, workers = min(waves, groups);  // workers: waves with weights to read
   uint8_t* xc = reinterpret_cast<uint8_t*>(part + 2 * workers * 64);
-  uint32_t* xs = reinterpret_cast<uint32_t*>(xc + groups * 256 * M);
+  uint8_t* xs = xc + groups * 256 * M;
 
   v4i w[2][4];
   int sw[2];
@@ -117,44 +124,46 @@ __global__ __launch_bounds__(1024) void k_mx_few(const uint8_t* __restrict__ cod
       if (cb < 4 * tiles) v = *reinterpret_cast<const v4i*>(xcodes + (int64_t)cb * 256 + 16 * r);
       *reinterpret_cast<v4i*>(xc + 16 * i) = v;
     }
-    for (int i = threadIdx.x; i < groups * 4 * M; i += blockDim.x) {
-      const int gb = i / M, r = i - gb * M;
-      xs[i] = *reinterpret_cast<const uint32_t*>(xscales + (gb * 16 + r) * 4);
+    for (int i = threadIdx.x; i < groups * 16 * M; i += blockDim.x) {
+      const int cb = i / M, r = i - cb * M, c = cb >> 2, b = cb & 3;
+      xs[i] = xscales[((c >> 2) * 64 + 16 * b + r) * 4 + (c & 3)];
     }
   } else {
     using T = std::conditional_t<kSrc == kFromBf16, uint16_t, float>;
     const T* x = static_cast<const T*>(X);
-    uint8_t* xsb = reinterpret_cast<uint8_t*>(xs);
-    const int p = threadIdx.x & 3, quads = 16 * waves, items = M * 16 * groups;
-    // item i: block i / M of token i % M, in the order of LDS (token by token, a wave's quads would
-    // write one bank); kBatch of a quad's items are loaded before the first is used
+    const int p = threadIdx.x & 1, pairs = 32 * waves, items = M * 16 * groups;
+    // item i: block i / M of token i % M, in the order of LDS, for two lanes; kBatch of a pair's items
+    // are loaded before the first is used
     auto quantize = [&](auto batch) {
       constexpr int kBatch = decltype(batch)::value;
-      for (int i0 = threadIdx.x >> 2; i0 < items; i0 += kBatch * quads) {
-        Raw8<T> v[kBatch];
-        int rr[kBatch], cc[kBatch];
+      for (int i0 = threadIdx.x >> 1; i0 < items; i0 += kBatch * pairs) {
+        Raw8<T> v[kBatch][2];
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-          const int i = i0 + j * quads;
-          cc[j] = M == 1 ? i : (int)__umulhi((uint32_t)i, magic);
-          rr[j] = i - cc[j] * M;
-          const int col = 32 * cc[j] + 8 * p;
-          v[j] = load_raw8(x + (rr[j] * (int)K + col), i < items ? (int)K - col : 0);
+          const int i = i0 + j * pairs, cb = M == 1 ? i : (int)__umulhi((uint32_t)i, magic), r = i - cb * M;
+          const int col = 32 * cb + 16 * p, left = i < items ? (int)K - col : 0;
+          const T* at = x + (r * (int)K + col);
+          v[j][0] = load_raw8(at, left);
+          v[j][1] = load_raw8(at + 8, left - 8);
         }
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-          uint32_t e;
-          const uint32_t q = mx_quantize8(v[j], e);
-          if (i0 + j * quads < items) {
-            const int c = cc[j] >> 2, b = cc[j] & 3;
-            *reinterpret_cast<uint32_t*>(xc + 16 * (cc[j] * M + rr[j]) + 4 * p) = q;
-            if (p == 0) xsb[4 * (((c >> 2) * 4 + b) * M + rr[j]) + (c & 3)] = (uint8_t)e;
+          const MxScale s = mx_scale(pair_max(max(top_bits(v[j][0]), top_bits(v[j][1]))));
+          uint2 q;
+          q.x = codes8(v[j][0], s);
+          q.y = codes8(v[j][1], s);
+          const int i = i0 + j * pairs;
+          if (i < items) {
+            *reinterpret_cast<uint2*>(xc + 16 * i + 8 * p) = q;
+            if (p == 0) xs[i] = (uint8_t)s.e;
           }
         }
       }
     };
-    if (items <= quads)
+    if (items <= pairs)
       quantize(std::integral_constant<int, 1>{});
+    else if (items <= 2 * pairs)
+      quantize(std::integral_constant<int, 2>{});
     else
       quantize(std::integral_constant<int, 4>{});
   }
@@ -168,7 +177,7 @@ __global__ __launch_bounds__(1024) void k_mx_few(const uint8_t* __restrict__ cod
 
   const int tok = min(lane & 15, M - 1);  // lanes of tokens past the last repeat it; not stored
   const uint8_t* xl = xc + 16 * ((lane >> 4) * M + tok);
-  const uint32_t* sl = xs + (lane >> 4) * M + tok;
+  const uint8_t* sl = xs + (lane >> 4) * M + tok;
   v4f acc = {0, 0, 0, 0};
   int g = wave, turn = 0;
   while (nb < nblocks) {
@@ -179,10 +188,9 @@ __global__ __launch_bounds__(1024) void k_mx_few(const uint8_t* __restrict__ cod
       const int64_t nnb = more ? nb : nb + gridDim.x;
       const int ng = more ? g + workers : wave;
       fetch(nnb, ng, w[1 - cur], sw[1 - cur]);
-      const int sx = (int)sl[g * 4 * M];
       static_for<4>([&](auto t) {
         const v4i xv = *reinterpret_cast<const v4i*>(xl + (4 * g + t) * 64 * M);
-        acc = mx_mfma<t, t>(w[cur][t], xv, acc, sw[cur], sx);
+        acc = mx_mfma<t, 0>(w[cur][t], xv, acc, sw[cur], sl[(4 * g + t) * 4 * M]);
       });
       if (!more) {
         v4f* mine = part + (turn & 1) * workers * 64;
@@ -218,15 +226,15 @@ void launch(const MxDecodePlan& p, const uint8_t* codes, const uint8_t* scales, 
 
 }  // namespace
 
-// Blocks that a workgroup quantises by itself at most; beyond, the quantiser runs first.  Measured
-// (graph replays; the issue of an eager call takes 9.3 and 14 us): 16 x 2560 x 2560 6.6 and 7.4 us,
-// 16 x 2560 x 6912 (3584 blocks) 11.5 and 9.3, 4 x 8192 x 28672 (3584) 27.2 and 26.3.
+// Blocks that a workgroup quantises by itself at most; beyond, the quantiser runs first.  Measured, one
+// launch against two (graph replays; the issue of an eager call takes 9.3 and 14 us): 16 x 2560 x 2560
+// 5.6 and 7.4 us, 16 x 2560 x 6912 (3584 blocks) 9.5 and 9.3, 4 x 8192 x 28672 (3584) 25.4 and 26.3.
 constexpr int64_t kFewItems = 4096;
 
 MxFewPlan plan_mx_few(int64_t M, int64_t N, int64_t K, int src) {
   MxFewPlan p;
   if (M > 16) return p;
-  // Waves: one per group of four tiles, and enough that no quad of lanes quantises more than four
+  // Waves: one per group of four tiles, and enough that no pair of lanes quantises more than two
   // blocks; 16 at most.  Workgroups: what fits a compute unit with 16 waves, so that each fills its
   // LDS once and then streams weights.
   const int64_t groups = mx_groups(K), items = 16 * groups * M;

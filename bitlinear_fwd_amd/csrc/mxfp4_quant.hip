@@ -38,20 +38,19 @@ __global__ __launch_bounds__(256) void k_mx_quant(const T* __restrict__ X, int64
     uint32_t word = 0;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      uint32_t e;
-      const uint32_t q = mx_quantize8(v[t], e);
-      word |= e << (8 * t);
+      const MxScale s = mx_scale(quad_max(top_bits(v[t])));
+      const uint32_t q = codes8(v[t], s);
+      word |= s.e << (8 * t);
       const int64_t c = 4 * c4 + t;
       if (c < tiles)
         *reinterpret_cast<uint32_t*>(codes + (rb * tiles + c) * kMxTileBytes + 16 * (16 * b + r) + 4 * p) = q;
       if constexpr (kValues) {
-        const float s = mx_scale(e == 255 ? 127 : e);
-        const v2f f0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 0);
-        const v2f f1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 1);
-        const v2f f2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 2);
-        const v2f f3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 3);
+        const v2f f0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s.scale, 0);
+        const v2f f1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s.scale, 1);
+        const v2f f2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s.scale, 2);
+        const v2f f3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s.scale, 3);
         float f[8] = {f0.x, f0.y, f1.x, f1.y, f2.x, f2.y, f3.x, f3.y};
-        if (e == 255) {
+        if (s.bad) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(0x7fc00000u);
         }

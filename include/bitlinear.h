@@ -379,8 +379,8 @@ int bitlinear_forward_binary_plan(int64_t M, int64_t N, int64_t K, int32_t out[6
  *           not matter and nothing carries over.  Calls that share a workspace must not
  *           overlap.
  * Limits: 1 <= R, M, N < 2^31, 1 <= K <= 2^24 (else BL_ERR_INVALID_ARG); BL_ERR_UNSUPPORTED
- * for other types, for R * K > 2^40 and for products of more than 2^30 output tiles of 16
- * x 16.  Buffers of one call must not overlap.
+ * for other types, for R * K (M * K, N * K) > 2^40 and for products of more than 2^23 output
+ * tiles of 128 x 128.  Buffers of one call must not overlap.
  */
 int64_t bitlinear_mxfp4_codes_bytes(int64_t R, int64_t K);  /* -1 for arguments < 1 */
 int64_t bitlinear_mxfp4_scales_bytes(int64_t R, int64_t K); /* -1 for arguments < 1 */

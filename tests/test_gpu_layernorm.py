@@ -168,3 +168,88 @@ def test_layernorm_argument_errors():
             bad()
     with pytest.raises(bl.BitLinearError):
         bl.layernorm(x, w, b, eps=0.0)
+
+
+def test_layernorm_offsets_past_32_bits():
+    """More than 2^32 elements (8.6 GB each way): the last rows against the same rows alone."""
+    m, k = 262145, 16400
+    x = torch.zeros((m, k), dtype=torch.bfloat16, device=DEV)
+    tail, w, b, dy = data(5, k, "bf16", seed=2)
+    x[m - 5:] = tail
+    y, mean, rstd = bl.layernorm(x, w, b)
+    ty, tm, tr = bl.layernorm(tail, w, b)
+    assert torch.equal(y[m - 5:], ty) and torch.equal(mean[m - 5:], tm) and torch.equal(rstd[m - 5:], tr)
+    assert torch.equal(y[0], b.to(torch.bfloat16)) and float(mean[7]) == 0.0
+    y.zero_()
+    y[m - 5:] = dy  # as the gradient: zeros but for the last rows
+    dx, dw, db = bl.layernorm_backward(y, x, w, mean, rstd)
+    tx, tw, tb = bl.layernorm_backward(dy, tail, w, tm, tr)
+    assert torch.equal(dx[m - 5:], tx) and not dx[:7].any()
+    torch.testing.assert_close(dw, tw, rtol=0, atol=8 * U * float((dy.float().abs() * 5).sum(0).max()))
+    torch.testing.assert_close(db, tb, rtol=0, atol=8 * U * float(dy.float().abs().sum(0).max()))
+
+
+def test_layernorm_graph_replays_and_streams():
+    """Forward and backward captured into a graph on a side stream, replayed with new inputs and eager
+    work between; then on two streams at once."""
+    sizes = [(5, 100, "f32"), (300, 2560, "bf16"), (40, 9000, "f32"), (3, 40000, "bf16")]
+    ins = [data(m, k, dt, seed=i) for i, (m, k, dt) in enumerate(sizes)]
+
+    def run():
+        out = []
+        for x, w, b, dy in ins:
+            y, mean, rstd = bl.layernorm(x, w, b)
+            out += [y, mean, rstd, *bl.layernorm_backward(dy, x, w, mean, rstd)]
+        return out
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        got = run()
+    for turn in range(3):
+        for i, (m, k, dt) in enumerate(sizes):
+            for t, new in zip(ins[i], data(m, k, dt, seed=10 * turn + i + 50)):
+                t.copy_(new)
+        g.replay()
+        want = run()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), turn
+    streams, both = [torch.cuda.Stream() for _ in range(2)], []
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            both.append([run() for _ in range(3)])
+    torch.cuda.synchronize()
+    for runs in both:
+        for out in runs:
+            for a, b in zip(out, want):
+                assert torch.equal(a, b)
+
+
+def test_layernorm_gradients_against_differences():
+    """dx, dweight and dbias along random directions against central differences of the kernel's own
+    forward pass.  With |r|, |v| <= 1 and rows of 64 values of unit spread the loss is a few tens, its
+    fp32 error about 64 * 6 * 64 * U ~ 1.5e-3 in the worst case; at a step of 0.05 that is 0.03 in the
+    difference, and the third derivative adds 0.05^2 / 6 of a few tens ~ 0.02."""
+    m, k, step = 6, 64, 0.05
+    x, w, b, _ = data(m, k, "f32", seed=3)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(1)
+    r = torch.rand((m, k), generator=g, device=DEV) * 2 - 1
+
+    def loss(x, w, b):
+        return float((bl.layernorm(x, w, b)[0].double() * r.double()).sum())
+
+    _, mean, rstd = bl.layernorm(x, w, b)
+    for i, grad in enumerate(bl.layernorm_backward(r, x, w, mean, rstd)):
+        args = [x, w, b]
+        v = torch.rand(args[i].shape, generator=g, device=DEV) * 2 - 1
+        up, down = list(args), list(args)
+        up[i], down[i] = args[i] + step * v, args[i] - step * v
+        slope = (loss(*up) - loss(*down)) / (2 * step)
+        assert abs(slope - float((grad.double() * v.double()).sum())) <= 0.06, i

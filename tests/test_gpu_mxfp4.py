@@ -236,3 +236,117 @@ def test_forward_argument_errors():
     with pytest.raises(ValueError):  # a workspace that is too small
         bl.forward_mxfp4_fused(wc, ws, torch.randn(700, 256, device=DEV), 32, 256,
                                workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+
+
+def test_forward_offsets_past_32_bits():
+    """An output of more than 2^32 elements (8.6 GB) and an input of as many: rows at both ends
+    against the same rows computed alone."""
+    m, n, k = 65600, 65552, 64
+    x, w = grid_matrix(m, k, 1), grid_matrix(n, k, 2)
+    wc, ws = bl.quantize_mxfp4(w)
+    y = bl.forward_mxfp4_fused(wc, ws, x, n, k, out_dtype=torch.bfloat16)
+    for lo in (0, 32768, m - 40):
+        want = bl.forward_mxfp4_fused(wc, ws, x[lo:lo + 40].contiguous(), n, k, out_dtype=torch.bfloat16)
+        assert torch.equal(y[lo:lo + 40], want)
+    del y, want
+    r, k = 262200, 16400
+    x = torch.zeros((r, k), dtype=torch.bfloat16, device=DEV)
+    tail = outliers(37, k, seed=8, dtype=torch.bfloat16)
+    x[r - 37:] = tail
+    codes, scales, values = bl.quantize_mxfp4(x, want_values=True)
+    q, s, v = ref.quantize(acts_host_f32(tail))
+    check_equal(acts_host_f32(values[r - 37:]).astype(np.float64), v, "values")
+    # the last 8 rows start a row block: r = 16 * 16387 + 8
+    want, wsc = ref.pack(q[-8:], s[-8:], k)
+    check_equal(host(codes[-want.size:]), want, "codes")
+    check_equal(host(scales[-wsc.size:]), wsc, "scales")
+
+
+def test_largest_k():
+    """The longest rows the calls take, one token (the quantiser, then the decode kernel)."""
+    n, k = 3, 1 << 24
+    w, x = torch.full((n, k), 2.0 ** -12, device=DEV), torch.full((1, k), 0.5, device=DEV)
+    x[0, 1::2] = 1.0
+    y = bl.forward_mxfp4_fused(*bl.quantize_mxfp4(w), x, n, k)
+    assert (y == k * 0.75 * 2.0 ** -12).all()
+
+
+def test_graph_replays_and_streams():
+    """The products and the quantiser captured into a graph on a side stream, replayed with new
+    inputs and eager work between, and two streams at once, against eager results."""
+    shapes = [(1, 300, 2560), (16, 128, 6912), (16, 64, 8704), (40, 500, 1000), (300, 600, 1500)]
+    w = [grid_matrix(n, k, i, shift=-3) for i, (m, n, k) in enumerate(shapes)]
+    wq = [bl.quantize_mxfp4(t) for t in w]
+    xs = [outliers(m, k, seed=i, dtype=torch.bfloat16) for i, (m, n, k) in enumerate(shapes)]
+
+    def run():
+        out = []
+        for (m, n, k), (c, s), x in zip(shapes, wq, xs):
+            out.append(bl.forward_mxfp4_fused(c, s, x, n, k))
+            out.append(bl.forward_mxfp4(c, s, *bl.quantize_mxfp4(x), m, n, k, out_dtype=torch.bfloat16))
+        return out
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        got = run()
+    for turn in range(3):
+        for i, x in enumerate(xs):
+            x.copy_(outliers(*x.shape, seed=100 * turn + i, dtype=torch.bfloat16))
+        g.replay()
+        want = run()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), turn
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    both = []
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            both.append([run() for _ in range(3)])
+    torch.cuda.synchronize()
+    for runs in both:
+        for out in runs:
+            for a, b in zip(out, want):
+                assert torch.equal(a, b)
+
+
+def test_workspace_of_the_caller():
+    """A given workspace is used whatever it holds, and one serves calls of several shapes."""
+    shapes = [(20, 48, 640), (16, 40, 28672), (130, 200, 513)]
+    need = max(bl.forward_mxfp4_fused_ws_bytes(m, n, k, "f32") for m, n, k in shapes)
+    assert need > 0 and bl.forward_mxfp4_fused_ws_bytes(1, 64, 2560) == 0
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device=DEV)
+    for m, n, k in shapes:
+        w, x = bl.quantize_mxfp4(grid_matrix(n, k, 3)), outliers(m, k, seed=m)
+        assert torch.equal(bl.forward_mxfp4_fused(*w, x, n, k, workspace=ws), bl.forward_mxfp4_fused(*w, x, n, k))
+
+
+@pytest.mark.parametrize("tokens", [1, 5, 16, 50, 300])
+def test_norm_quantise_product_together(tokens):
+    """A layer as it would be used: layer norm, its output quantised once for two projections, squared
+    ReLU gating, and the down projection from the un-quantised hidden rows; against 64 bits on the
+    values that each quantiser saw."""
+    d, h = 640, 1111
+    g = torch.Generator(device=DEV)
+    g.manual_seed(tokens)
+    x = torch.randn((tokens, d), generator=g, device=DEV).to(torch.bfloat16)
+    gain, bias = 1 + 0.1 * torch.randn(d, generator=g, device=DEV), 0.1 * torch.randn(d, generator=g, device=DEV)
+    wg, wu, wd = (torch.randn(s, generator=g, device=DEV) * 0.05 for s in ((h, d), (h, d), (d, h)))
+    (gc, gs), (uc, us), (dc, ds) = (bl.quantize_mxfp4(w) for w in (wg, wu, wd))
+    y, mean, rstd = bl.layernorm(x, gain, bias)
+    yc, ys = bl.quantize_mxfp4(y)
+    gate = bl.forward_mxfp4(gc, gs, yc, ys, tokens, h, d)
+    up = bl.forward_mxfp4(uc, us, yc, ys, tokens, h, d)
+    hidden = torch.relu(gate) ** 2 * up
+    out = bl.forward_mxfp4_fused(dc, ds, hidden, d, h)
+    wy = ref.layernorm(acts_host_f32(x), host(gain), host(bias), 1e-5)[0]
+    assert np.abs(acts_host_f32(y) - wy).max() <= 2.0 ** -8 * np.abs(wy).max() + 1e-4
+    yv = ref.quantize(acts_host_f32(y))[2]
+    check_product(gate, yv, ref.quantize(host(wg))[2], d)
+    check_product(up, yv, ref.quantize(host(wu))[2], d)
+    check_product(out, ref.quantize(host(hidden))[2], ref.quantize(host(wd))[2], h)
