@@ -11,9 +11,13 @@
 // stay in registers until it ends and writes one partial row of dw and of db; a second launch
 // adds the partial rows in order.  No atomics: results do not depend on timing.
 //
-// Both are bound by memory: x (and dy) in, y (dx) out.  Rows are held by 64, 256 or 1024 threads
-// with up to four groups of 8 elements each; longer rows are read again for each sum, with the
-// sums in fp64.
+// Both are bound by memory: x (and dy) in, y (dx) out.  A row is shared by a wave (up to 1024
+// elements, forward) or by as many waves as hold it with one or two groups of 8 elements a thread;
+// rows longer than 32768 (backward 12288) elements are read again for each sum, with the sums in
+// fp64.  Measured (a large copy moves 5.2 TB/s): forward 8192 x 8192 bf16 53 us, 5.1 TB/s; 2048 x 8192
+// fp32 27.4 us, 4.9 TB/s; 16 x 2560 bf16 3.5 us, a launch and one round trip to memory.  Backward 2048
+// x 2560 bf16 18.1 us, of which the second launch takes 4 and the first about 7 before and after its
+// rows (2.7 us for every 768 of them, 4.4 TB/s); 1003 x 7001 fp32 28.8 us.
 #include "layernorm.h"
 
 #include <algorithm>
@@ -25,6 +29,9 @@ namespace {
 
 constexpr int64_t kMaxGrid = 1 << 20;    // workgroups of a launch; rows beyond are walked over
 constexpr int64_t kCUs = 256;
+// Rows per compute unit up to which a row is spread over as many threads as possible: the latency of
+// one row counts (16 x 2560 bf16: 3.5 us, 4.9 with two groups a thread), beyond it the bytes in flight
+// (8192 x 8192 bf16: 82 us with one group, 65 with two).
 constexpr int kFewRows = 4;
 
 // Sum of each v[] over the threads that share a row; every thread gets it.  kTh 64: a wave.  Else
@@ -54,6 +61,68 @@ __device__ __forceinline__ void row_sum(F (&v)[kN], F* red, int i0 = threadIdx.x
   }
 }
 
+// The eight columns of group g of a thread, as two runs of four.  A wave's 16-byte loads have to be
+// consecutive: the runs are neighbours in a bf16 row and 4 `threads` columns apart in an fp32 one
+// (2048 x 8192 fp32: 27.4 us, 32.0 with runs that are neighbours; backward 47.6 and 51.4).
+struct Cols {
+  int64_t a, b;
+  __device__ __forceinline__ int64_t at(int i) const { return i < 4 ? a + i : b + i - 4; }
+};
+template <typename T>
+__device__ __forceinline__ Cols cols(int i0, int g, int threads) {
+  if constexpr (sizeof(T) == 4) return {4 * (int64_t)(i0 + 2 * g * threads), 4 * (int64_t)(i0 + (2 * g + 1) * threads)};
+  const int64_t c = 8 * (int64_t)(i0 + g * threads);
+  return {c, c + 4};
+}
+__device__ __forceinline__ void load4(const float* p, int64_t n, uint32_t* v) {
+  if (n >= 4) {
+    __builtin_memcpy(v, p, 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = i < n ? __float_as_uint(p[i]) : 0u;
+  }
+}
+// A group of a row of K elements (0: none, all zeros).
+__device__ __forceinline__ Raw8<uint16_t> load_group(const uint16_t* row, Cols c, int64_t K) {
+  return load_raw8(row + c.a, K - c.a);
+}
+__device__ __forceinline__ Raw8<float> load_group(const float* row, Cols c, int64_t K) {
+  Raw8<float> r;
+  load4(row + c.a, K - c.a, r.w);
+  load4(row + c.b, K - c.b, r.w + 4);
+  return r;
+}
+__device__ __forceinline__ void load_params(const float* p, Cols c, int64_t K, float (&v)[8]) {
+  Raw8<float> r;
+  load4(p + c.a, K - c.a, r.w);
+  load4(p + c.b, K - c.b, r.w + 4);
+  widen8(r, v);
+}
+// stream: past the caches.
+__device__ __forceinline__ void store_group(uint16_t* row, Cols c, int64_t K, const float (&v)[8], bool stream) {
+  stream8(row + c.a, K - c.a, v, stream);
+}
+__device__ __forceinline__ void store_group(float* row, Cols c, int64_t K, const float (&v)[8], bool stream) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t col = h ? c.b : c.a;
+    float* p = row + col;
+    if (K - col >= 4) {
+      v4u w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(v[4 * h + i]);
+      if (stream)
+        __builtin_nontemporal_store(w, reinterpret_cast<v4u_unaligned*>(p));
+      else
+        *reinterpret_cast<v4u_unaligned*>(p) = w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (col + i < K) p[i] = v[4 * h + i];
+    }
+  }
+}
+
 // One row per wave (kWave) or per workgroup, kG groups of 8 elements per thread (thread i of the T
 // that share the row takes groups i, i + T, ...).  A workgroup walks over rows with the next row's
 // loads in flight and (kHold) weight and bias in registers: read for every row they are four
@@ -74,21 +143,21 @@ __global__ __launch_bounds__(kWave ? 256 : 1024) void k_layernorm(const T* __res
   auto fetch = [&](int64_t r) {
 #pragma unroll
     for (int g = 0; g < kG; ++g) {
-      const int64_t col = 8 * (int64_t)(i0 + g * threads);
-      raw[g] = load_raw8(X + r * K + col, r < M ? K - col : 0);
+      const Cols c8 = cols<T>(i0, g, threads);
+      raw[g] = load_group(X + r * K, c8, r < M ? K : 0);
     }
   };
   fetch(row);
   float w[kG][8], b[kG][8];
   auto params = [&](int g) {
-    const int64_t col = 8 * (int64_t)(i0 + g * threads);
+    const Cols c8 = cols<T>(i0, g, threads);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       w[g][i] = 1.0f;
       b[g][i] = 0.0f;
     }
-    if (weight) load8(weight + col, K - col, w[g]);
-    if (bias) load8(bias + col, K - col, b[g]);
+    if (weight) load_params(weight, c8, K, w[g]);
+    if (bias) load_params(bias, c8, K, b[g]);
   };
   if constexpr (kHold) {
 #pragma unroll
@@ -107,10 +176,10 @@ __global__ __launch_bounds__(kWave ? 256 : 1024) void k_layernorm(const T* __res
     const float mean = sum[0] / (float)K;
 #pragma unroll
     for (int g = 0; g < kG; ++g) {
-      const int64_t col = 8 * (int64_t)(i0 + g * threads);
+      const Cols c8 = cols<T>(i0, g, threads);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        v[g][i] = col + i < K ? v[g][i] - mean : 0.0f;
+        v[g][i] = c8.at(i) < K ? v[g][i] - mean : 0.0f;
         sq[0] += v[g][i] * v[g][i];
       }
     }
@@ -122,14 +191,11 @@ __global__ __launch_bounds__(kWave ? 256 : 1024) void k_layernorm(const T* __res
     }
 #pragma unroll
     for (int g = 0; g < kG; ++g) {
-      const int64_t col = 8 * (int64_t)(i0 + g * threads);
+      const Cols c8 = cols<T>(i0, g, threads);
       if constexpr (!kHold) params(g);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[g][i] = v[g][i] * rstd * w[g][i] + b[g][i];
-      if constexpr (kWave || kG > 1)
-        stream8(Y + row * K + col, K - col, v[g], whole_pieces(K));
-      else
-        store8(Y + row * K + col, K - col, v[g]);
+      store_group(Y + row * K, c8, K, v[g], (kWave || kG > 1) && whole_pieces(K));
     }
   }
 }
@@ -199,14 +265,14 @@ __global__ __launch_bounds__(kG == 1 ? 1024 : 768) void k_layernorm_bwd(
   float dw[kG][8], db[kG][8], w[kG][8];
 #pragma unroll
   for (int g = 0; g < kG; ++g) {
-    const int64_t col = 8 * (int64_t)(i0 + g * threads);
+    const Cols c8 = cols<T>(i0, g, threads);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       dw[g][i] = 0.0f;
       db[g][i] = 0.0f;
       w[g][i] = 1.0f;
     }
-    if (weight) load8(weight + col, K - col, w[g]);
+    if (weight) load_params(weight, c8, K, w[g]);
   }
   Raw8<T> rx[kG], rd[kG];
   float rmean = 0.0f, rrstd = 0.0f;
@@ -214,9 +280,9 @@ __global__ __launch_bounds__(kG == 1 ? 1024 : 768) void k_layernorm_bwd(
     const bool in = row < M;
 #pragma unroll
     for (int g = 0; g < kG; ++g) {
-      const int64_t col = 8 * (int64_t)(i0 + g * threads), left = in ? K - col : 0;
-      rx[g] = load_raw8(X + row * K + col, left);
-      rd[g] = load_raw8(dY + row * K + col, left);
+      const Cols c8 = cols<T>(i0, g, threads);
+      rx[g] = load_group(X + row * K, c8, in ? K : 0);
+      rd[g] = load_group(dY + row * K, c8, in ? K : 0);
     }
     rmean = in ? mean_in[row] : 0.0f;
     rrstd = in ? rstd_in[row] : 0.0f;
@@ -254,10 +320,10 @@ __global__ __launch_bounds__(kG == 1 ? 1024 : 768) void k_layernorm_bwd(
       const int64_t row = r0 + sub;
 #pragma unroll
       for (int g = 0; g < kG; ++g) {
-        const int64_t col = 8 * (int64_t)(i0 + g * threads);
+        const Cols c8 = cols<T>(i0, g, threads);
 #pragma unroll
         for (int i = 0; i < 8; ++i) d[g][i] = rstd * (d[g][i] - c[0] - x[g][i] * c[1]);
-        stream8(dX + row * K + col, row < M ? K - col : 0, d[g], whole_pieces(K));
+        store_group(dX + row * K, c8, row < M ? K : 0, d[g], whole_pieces(K));
       }
     }
   }
@@ -286,9 +352,9 @@ __global__ __launch_bounds__(kG == 1 ? 1024 : 768) void k_layernorm_bwd(
     if (sub < rows - 1) return;
 #pragma unroll
     for (int g = 0; g < kG; ++g) {
-      const int64_t col = 8 * (int64_t)(i0 + g * threads);
-      store8(part + 2 * (int64_t)blockIdx.x * K + col, K - col, dw[g]);
-      store8(part + (2 * (int64_t)blockIdx.x + 1) * K + col, K - col, db[g]);
+      const Cols c8 = cols<T>(i0, g, threads);
+      store_group(part + 2 * (int64_t)blockIdx.x * K, c8, K, dw[g], false);
+      store_group(part + (2 * (int64_t)blockIdx.x + 1) * K, c8, K, db[g], false);
     }
   }
 }
@@ -457,7 +523,8 @@ hipError_t launch_layernorm(const void* X, int bf16, int64_t M, int64_t K, const
 LnBwdPlan plan_layernorm_backward(int64_t M, int64_t K) {
   LnBwdPlan p;
   // one group of 8 elements per thread up to 16 waves a row, and as many rows as 16 waves hold (one
-  // workgroup to a compute unit, so one partial row each); two groups and one row up to 12 waves
+  // workgroup to a compute unit, so one partial row each); two groups and one row up to 12 waves.
+  // 512 workgroups with half the rows write twice the partial rows: 2048 x 2560 bf16 21.1 us, 18.1 so.
   if (K <= 12288) {
     p.groups = K <= 8192 ? 1 : 2;
     const int waves = (int)((K + 512 * p.groups - 1) / (512 * p.groups));
