@@ -232,6 +232,7 @@ hipError_t launch_mx_few(const uint8_t* codes, const uint8_t* scales, const void
 struct MxDecodePlan {
   int waves = 4;       // waves per workgroup; they split the column groups
   int tg = 1;          // token groups of 16 per workgroup
+  int rb = 1;          // row blocks per workgroup
   int64_t gx = 0, gy = 0;
 };
 MxDecodePlan plan_mx_decode(int64_t M, int64_t N, int64_t K);

@@ -7,11 +7,13 @@
 // launch instead of two, and workgroups that stay (16 waves to a unit) and keep the next group's
 // loads in flight over the sums of this row block.  Loads past the caches, as the weights are read
 // once.
-// More tokens (k_mx_decode): a workgroup takes one 16-row block of the weights and TG groups of 16
-// tokens; its waves split the columns in groups of four tiles and add their sums in LDS at the end, in
-// wave order.  Each weight tile is loaded once (one coalesced 1 KiB wave load straight into operand
-// registers) and serves TG matrix instructions; the tokens' tiles come from L2, which is what bounds
-// it (0.1 us for a thousand products of a weight tile with 16 tokens).
+// More tokens, or longer rows of up to 16 (k_mx_decode): a workgroup takes one or two 16-row blocks of
+// the weights and TG groups of 16 tokens; its waves split the columns in groups of four tiles, the
+// next group's weights in flight, and add their sums in LDS at the end, in wave order.  Each weight
+// tile is one coalesced 1 KiB wave load straight into operand registers and serves TG matrix
+// instructions; the tokens' tiles come from L2, which is what bounds it from some 32 tokens on (65 ns
+// for a thousand products of a weight tile with 16 tokens).  16 x 8192 x 28672: 22.6 us, 5.5 TB/s of
+// weights.
 #include "mxfp4.h"
 
 #include <algorithm>
@@ -19,70 +21,130 @@
 namespace bl {
 namespace {
 
+// Four consecutive outputs of a token, those before column N.
 template <typename TY>
-__device__ __forceinline__ void store_y(TY* y, float v) {
-  if constexpr (sizeof(TY) == 4)
-    *y = v;
-  else
-    *y = (TY)bf16_bits(v);
+__device__ __forceinline__ void store_y(TY* y, int64_t left, v4f v) {
+  if constexpr (sizeof(TY) == 4) {
+    if (left >= 4) {
+      __builtin_memcpy(y, &v, 16);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (q < left) y[q] = v[q];
+    }
+  } else {
+    if (left >= 4) {
+      const uint32_t w[2] = {bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+      __builtin_memcpy(y, w, 8);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (q < left) y[q] = bf16_bits(v[q]);
+    }
+  }
 }
 
-template <int TG, typename TY>
+// Barrier between LDS writes and reads that leaves global loads in flight.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// Four tiles of a row block's codes from p (16 bytes per lane; those past `left` are zeros).  kOnce:
+// past the caches.
+template <bool kOnce>
+__device__ __forceinline__ void load_group(const uint8_t* p, int left, v4i (&v)[4]) {
+  if (left >= 4) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const v4i* at = reinterpret_cast<const v4i*>(p + t * kMxTileBytes);
+      v[t] = kOnce ? __builtin_nontemporal_load(at) : *at;
+    }
+  } else {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      v[t] = v4i{0, 0, 0, 0};
+      if (t < left) v[t] = *reinterpret_cast<const v4i*>(p + t * kMxTileBytes);
+    }
+  }
+}
+
+// RB row blocks of the weights by TG groups of 16 tokens.
+template <int TG, int RB, bool kOnce, typename TY>
 __global__ __launch_bounds__(512) void k_mx_decode(const uint8_t* __restrict__ codes,
                                                    const uint8_t* __restrict__ scales,
                                                    const uint8_t* __restrict__ xcodes,
                                                    const uint8_t* __restrict__ xscales, int64_t M, int64_t N,
-                                                   int64_t tiles, int64_t groups, int64_t nblocks, int64_t xblocks,
+                                                   int tiles, int groups, int64_t nblocks, int64_t xblocks,
                                                    TY* __restrict__ Y) {
-  extern __shared__ v4f part[];  // [waves][TG][64]
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  extern __shared__ v4f part[];  // [waves][RB][TG][64]
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int waves = blockDim.x >> 6;
   const int64_t xb0 = (int64_t)blockIdx.y * TG;
-  for (int64_t nb = blockIdx.x; nb < nblocks; nb += gridDim.x) {
-    v4f acc[TG];
+  for (int64_t nb0 = (int64_t)blockIdx.x * RB; nb0 < nblocks; nb0 += (int64_t)gridDim.x * RB) {
+    const uint8_t *wp[RB], *xp[TG];
+    const int *sp[RB], *xsp[TG];
 #pragma unroll
-    for (int j = 0; j < TG; ++j) acc[j] = v4f{0, 0, 0, 0};
-    for (int64_t g = wave; g < groups; g += waves) {
-      const int sw = *reinterpret_cast<const int*>(scales + ((nb * groups + g) * 64 + lane) * 4);
-      v4i w[4];
-      static_for<4>([&](auto t) {
-        w[t] = v4i{0, 0, 0, 0};
-        if (4 * g + t < tiles)
-          w[t] = *reinterpret_cast<const v4i*>(codes + (nb * tiles + 4 * g + t) * kMxTileBytes + 16 * lane);
+    for (int i = 0; i < RB; ++i) {  // row blocks and token groups past the last repeat it; not stored
+      const int64_t nb = min(nb0 + i, nblocks - 1);
+      wp[i] = codes + nb * tiles * kMxTileBytes + 16 * lane;
+      sp[i] = reinterpret_cast<const int*>(scales) + nb * groups * 64 + lane;
+    }
+#pragma unroll
+    for (int j = 0; j < TG; ++j) {
+      const int64_t xb = min(xb0 + j, xblocks - 1);
+      xp[j] = xcodes + xb * tiles * kMxTileBytes + 16 * lane;
+      xsp[j] = reinterpret_cast<const int*>(xscales) + xb * groups * 64 + lane;
+    }
+    v4f acc[RB][TG];
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+      for (int j = 0; j < TG; ++j) acc[i][j] = v4f{0, 0, 0, 0};
+    v4i w[2][RB][4];
+    int sw[2][RB];
+    auto fetch = [&](int g, v4i (&v)[RB][4], int (&sc)[RB]) {
+      const int left = g < groups ? tiles - 4 * g : 0;
+#pragma unroll
+      for (int i = 0; i < RB; ++i) {
+        sc[i] = left > 0 ? sp[i][g * 64] : 0;
+        load_group<kOnce>(wp[i] + (int64_t)g * 4096, left, v[i]);
+      }
+    };
+    fetch(wave, w[0], sw[0]);
+    for (int g0 = wave; g0 < groups; g0 += 2 * waves) {
+      static_for<2>([&](auto u) {
+        constexpr int cur = u;
+        const int g = g0 + cur * waves;
+        if (g >= groups) return;
+        fetch(g + waves, w[1 - cur], sw[1 - cur]);
+#pragma unroll
+        for (int j = 0; j < TG; ++j) {
+          v4i x[4];
+          const int sx = xsp[j][g * 64];
+          load_group<false>(xp[j] + (int64_t)g * 4096, tiles - 4 * g, x);
+          static_for<4>([&](auto t) {
+#pragma unroll
+            for (int i = 0; i < RB; ++i) acc[i][j] = mx_mfma<t, t>(w[cur][i][t], x[t], acc[i][j], sw[cur][i], sx);
+          });
+        }
       });
-#pragma unroll
-      for (int j = 0; j < TG; ++j) {
-        const int64_t xb = min(xb0 + j, xblocks - 1);  // a group past the last repeats it; not stored
-        const int sx = *reinterpret_cast<const int*>(xscales + ((xb * groups + g) * 64 + lane) * 4);
-        static_for<4>([&](auto t) {
-          v4i x = {0, 0, 0, 0};
-          if (4 * g + t < tiles)
-            x = *reinterpret_cast<const v4i*>(xcodes + (xb * tiles + 4 * g + t) * kMxTileBytes + 16 * lane);
-          acc[j] = mx_mfma<t, t>(w[t], x, acc[j], sw, sx);
-        });
-      }
     }
 #pragma unroll
-    for (int j = 0; j < TG; ++j) part[(wave * TG + j) * 64 + lane] = acc[j];
-    __syncthreads();
-    for (int i = threadIdx.x; i < TG * 64; i += blockDim.x) {
-      v4f s = part[i];
-      for (int w = 1; w < waves; ++w) s += part[w * TG * 64 + i];
-      const int64_t m = (xb0 + i / 64) * 16 + (i & 15), n = nb * 16 + 4 * ((i & 63) >> 4);
-      if (m < M) {
+    for (int i = 0; i < RB; ++i)
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (n + q < N) store_y(Y + m * N + n + q, s[q]);
-      }
+      for (int j = 0; j < TG; ++j) part[((wave * RB + i) * TG + j) * 64 + lane] = acc[i][j];
+    lds_barrier();
+    for (int o = threadIdx.x; o < RB * TG * 64; o += blockDim.x) {
+      v4f s = part[o];
+      for (int v = 1; v < waves; ++v) s += part[v * RB * TG * 64 + o];
+      const int i = o / (64 * TG), j = o / 64 % TG, l = o % 64;
+      const int64_t m = (xb0 + j) * 16 + (l & 15), n = (nb0 + i) * 16 + 4 * (l >> 4);
+      if (m < M) store_y(Y + m * N + n, N - n, s);
     }
-    __syncthreads();
+    lds_barrier();
   }
 }
 
 // Where k_mx_few takes the activations from.
 enum { kFromCodes, kFromBf16, kFromF32 };
-
-// Barrier between LDS writes and reads that leaves global loads in flight.
-__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 // Up to 16 tokens whose codes fit LDS.  The workgroup first fills LDS with the tokens' codes and
 // scales (kFromCodes: copied; else quantised there from X[M][K], two lanes to a block), then walks
@@ -202,11 +264,7 @@ __global__ __launch_bounds__(1024) void k_mx_few(const uint8_t* __restrict__ cod
           for (int v = 1; v < workers; ++v) s += mine[v * 64 + lane];
           const int64_t n = nb * 16 + 4 * (lane >> 4);
           const int m = lane & 15;
-          if (m < M) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              if (n + q < N) store_y(Y + m * N + n + q, s[q]);
-          }
+          if (m < M) store_y(Y + m * N + n, N - n, s);
         }
         ++turn;
       }
@@ -216,11 +274,12 @@ __global__ __launch_bounds__(1024) void k_mx_few(const uint8_t* __restrict__ cod
   }
 }
 
-template <int TG, typename TY>
+template <int TG, int RB, typename TY>
 void launch(const MxDecodePlan& p, const uint8_t* codes, const uint8_t* scales, const uint8_t* xcodes,
             const uint8_t* xscales, int64_t M, int64_t N, int64_t K, void* Y, hipStream_t s) {
-  k_mx_decode<TG, TY><<<dim3((unsigned)p.gx, (unsigned)p.gy), 64 * p.waves, p.waves * TG * 1024, s>>>(
-      codes, scales, xcodes, xscales, M, N, mx_tiles(K), mx_groups(K), mx_row_blocks(N), mx_row_blocks(M),
+  const auto fn = p.gy == 1 ? &k_mx_decode<TG, RB, true, TY> : &k_mx_decode<TG, RB, false, TY>;
+  fn<<<dim3((unsigned)p.gx, (unsigned)p.gy), 64 * p.waves, p.waves * RB * TG * 1024, s>>>(
+      codes, scales, xcodes, xscales, M, N, (int)mx_tiles(K), (int)mx_groups(K), mx_row_blocks(N), mx_row_blocks(M),
       static_cast<TY*>(Y));
 }
 
@@ -272,27 +331,33 @@ hipError_t launch_mx_few(const uint8_t* codes, const uint8_t* scales, const void
   }
 }
 
-// Estimates in microseconds that fit both sides: the decode kernel by its products of a weight tile
-// with 16 tokens (64 x 8192 x 8192: 131072 of them, 17.1 us; 128 x 2560 x 6912: 69120, 10.4; 256 x 6912
-// x 2560: 138240, 14.7), the GEMM, while its 128 x 128 tiles fit the chip at once, by its steps of 128
-// columns (20, 54, 64 and 224 steps: 11.8, 20.6, 25.2 and 73.6).  17 to 64 tokens of 8192 x 8192
-// decode, 128 of them go through the GEMM (28.4 against 25.3), 128 of 2560 x 6912 decode (10.4
-// against 20.6).
+// Estimates in microseconds, fitted to 22 shapes of 20 to 512 tokens measured both ways: the decode
+// kernel by its products of a weight tile with 16 tokens, the GEMM, while its 128 x 128 tiles fit the
+// chip at once, by its steps of 128 columns, both by the weights' bytes.  The rule takes the faster
+// path of all but one (128 x 6912 x 2560: 10.4 against 9.7 us).  Decode and GEMM in us: 64 x 8192 x
+// 8192 12.5 and 24.9, 128 x 8192 x 8192 22.9 and 24.1, 256 x 8192 x 8192 42.6 and 25.5, 256 x 2560 x
+// 6912 14.6 and 19.6, 40 x 28672 x 8192 39.7 and 31.3, 500 x 1000 x 8000 9.5 and 23.7.
 bool mx_decode_wins(int64_t M, int64_t N, int64_t K) {
   if (M <= 16) return true;
   if (M > 512) return false;
+  const MxDecodePlan p = plan_mx_decode(M, N, K);
+  const double tiles = (double)mx_row_blocks(N) * (double)mx_tiles(K), stream = tiles * 1088.0 / 5e6;
   const int64_t rounds = (((M + 127) / 128) * ((N + 127) / 128) + 511) / 512;
-  const double decode = 3.0 + 1e-4 * (double)(mx_row_blocks(N) * mx_tiles(K)) * (double)mx_row_blocks(M);
-  const double gemm = 5.0 + 0.31 * (double)(mx_tiles(K) * rounds);
+  const double stores = 1e-6 * (double)M * (double)N;  // the decode kernel's go out in pieces of 64 bytes
+  const double decode = std::max(3.5 + 6.5e-5 * tiles * (double)(p.gy * p.tg), 5.0 + stream) + stores;
+  const double gemm = std::max(5.0 + 0.3 * (double)(mx_tiles(K) * rounds), 6.0 + stream);
   return decode <= gemm;
 }
 
 MxDecodePlan plan_mx_decode(int64_t M, int64_t N, int64_t K) {
   MxDecodePlan p;
   p.tg = M <= 16 ? 1 : M <= 32 ? 2 : 4;
-  p.waves = (int)std::min<int64_t>(8, std::max<int64_t>(1, mx_groups(K) / 2));
-  p.gx = std::min<int64_t>(mx_row_blocks(N), 1 << 22);
   p.gy = (mx_row_blocks(M) + p.tg - 1) / p.tg;
+  // two row blocks share the tokens' tiles where the workgroups left fill the chip (64 x 8192 x 8192:
+  // 12.5 us, 15.8 with one; 64 x 2560 x 6912, 160 row blocks: 9.3, 7.3 with one)
+  p.rb = mx_row_blocks(N) * p.gy >= 256 ? 2 : 1;
+  p.waves = (int)std::min<int64_t>(8, mx_groups(K));
+  p.gx = std::min<int64_t>((mx_row_blocks(N) + p.rb - 1) / p.rb, 1 << 22);
   return p;
 }
 
@@ -300,19 +365,25 @@ hipError_t launch_mx_decode(const uint8_t* codes, const uint8_t* scales, const u
                             const uint8_t* xscales, int64_t M, int64_t N, int64_t K, void* Y, int ybf16,
                             hipStream_t s) {
   const MxDecodePlan p = plan_mx_decode(M, N, K);
-  auto go = [&](auto tg) {
-    constexpr int TG = decltype(tg)::value;
+  auto go = [&](auto tg, auto rb) {
+    constexpr int TG = decltype(tg)::value, RB = decltype(rb)::value;
     if (ybf16)
-      launch<TG, uint16_t>(p, codes, scales, xcodes, xscales, M, N, K, Y, s);
+      launch<TG, RB, uint16_t>(p, codes, scales, xcodes, xscales, M, N, K, Y, s);
     else
-      launch<TG, float>(p, codes, scales, xcodes, xscales, M, N, K, Y, s);
+      launch<TG, RB, float>(p, codes, scales, xcodes, xscales, M, N, K, Y, s);
+  };
+  auto by_rb = [&](auto tg) {
+    if (p.rb == 2)
+      go(tg, std::integral_constant<int, 2>{});
+    else
+      go(tg, std::integral_constant<int, 1>{});
   };
   if (p.tg == 1)
-    go(std::integral_constant<int, 1>{});
+    by_rb(std::integral_constant<int, 1>{});
   else if (p.tg == 2)
-    go(std::integral_constant<int, 2>{});
+    by_rb(std::integral_constant<int, 2>{});
   else
-    go(std::integral_constant<int, 4>{});
+    by_rb(std::integral_constant<int, 4>{});
   return hipGetLastError();
 }
 
