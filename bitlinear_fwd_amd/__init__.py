@@ -124,6 +124,8 @@ def lib() -> ctypes.CDLL:
         L.bitlinear_forward_mxfp4_fused_ws_bytes.argtypes = [i64, i64, i64, c_int]
         L.bitlinear_forward_mxfp4_fused.restype = c_int
         L.bitlinear_forward_mxfp4_fused.argtypes = [p, p, p, c_int, i64, i64, i64, p, c_int, p, i64, p]
+        L.bitlinear_forward_mxfp4_plan.restype = c_int
+        L.bitlinear_forward_mxfp4_plan.argtypes = [i64, i64, i64, c_int, p]
         L.bitlinear_layernorm.restype = c_int
         L.bitlinear_layernorm.argtypes = [p, c_int, i64, i64, p, p, f32, p, p, p, p]
         L.bitlinear_layernorm_backward.restype = c_int
@@ -147,7 +149,7 @@ EXPORTED_SYMBOLS = (
     "bitlinear_forward_ws_plan", "bitlinear_probe_prefill_occupancy", "bitlinear_mxfp4_codes_bytes",
     "bitlinear_mxfp4_scales_bytes", "bitlinear_quantize_mxfp4", "bitlinear_forward_mxfp4",
     "bitlinear_forward_mxfp4_fused_ws_bytes", "bitlinear_forward_mxfp4_fused", "bitlinear_layernorm",
-    "bitlinear_layernorm_backward_ws_bytes", "bitlinear_layernorm_backward",
+    "bitlinear_layernorm_backward_ws_bytes", "bitlinear_layernorm_backward", "bitlinear_forward_mxfp4_plan",
 )
 
 MAX_GROUP = 8
@@ -1033,6 +1035,16 @@ def forward_mxfp4(codes, scales, xcodes, xscales, m: int, n: int, k: int, y=None
     y, ydt = _product_output(y, out_dtype, m, n, codes)
     _call("bitlinear_forward_mxfp4", dev, *ptrs, m, n, k, y.data_ptr(), ydt)
     return y
+
+
+def forward_mxfp4_plan(m: int, n: int, k: int, x=None) -> dict:
+    """The launches of forward_mxfp4 (``x`` None) or of forward_mxfp4_fused (``x`` "bf16" or "f32")
+    for (M, N, K), computed on the host."""
+    out = (ctypes.c_int32 * 6)()
+    xdt = -1 if x is None else BL_BF16 if x == "bf16" else BL_F32
+    _check("bitlinear_forward_mxfp4_plan", lib().bitlinear_forward_mxfp4_plan(m, n, k, xdt, out))
+    return {"kernel": {7: "lds", 8: "decode", 9: "gemm"}[out[0]], "workgroups": out[1], "threads": out[2],
+            "tokens": out[3], "outputs": out[4], "launches": out[5]}
 
 
 def forward_mxfp4_fused_ws_bytes(m: int, n: int, k: int, dtype: str = "bf16") -> int:

@@ -174,6 +174,26 @@ int bitlinear_forward_mxfp4(const uint8_t* codes, const uint8_t* scales, const u
       mx_forward(codes, scales, xcodes, xscales, M, N, K, Y, ydt, static_cast<hipStream_t>(stream)));
 }
 
+int bitlinear_forward_mxfp4_plan(int64_t M, int64_t N, int64_t K, int xdt, int32_t out[6]) {
+  if (!out || !rows_ok(M, K) || !rows_ok(N, K)) return BL_ERR_INVALID_ARG;
+  if (!mx_product_ok(M, N, K) || (xdt != -1 && !dtype_ok(xdt))) return BL_ERR_UNSUPPORTED;
+  bl::MxFewPlan f;
+  if (xdt != -1) f = bl::plan_mx_few(M, N, K, mx_src(xdt));
+  out[5] = xdt == -1 || f.ok ? 1 : 2;
+  if (!f.ok) f = bl::plan_mx_few(M, N, K, 0);
+  if (f.ok) {
+    out[0] = 7, out[1] = (int32_t)f.groups, out[2] = 64 * f.waves, out[3] = 16, out[4] = 16;
+  } else if (bl::mx_decode_wins(M, N, K)) {
+    const bl::MxDecodePlan p = bl::plan_mx_decode(M, N, K);
+    out[0] = 8, out[1] = (int32_t)(p.gx * p.gy), out[2] = 64 * p.waves, out[3] = 16 * p.tg, out[4] = 16 * p.rb;
+  } else {
+    const bl::MxGemmPlan p = bl::plan_mx_gemm(M, N, K);
+    out[0] = 9, out[1] = (int32_t)(p.tiles_m * p.tiles_n), out[2] = 256;
+    out[3] = (int32_t)p.tile_m, out[4] = (int32_t)p.tile_n;
+  }
+  return BL_OK;
+}
+
 int64_t bitlinear_forward_mxfp4_fused_ws_bytes(int64_t M, int64_t N, int64_t K, int dt) {
   if (!rows_ok(M, K) || !rows_ok(N, K) || !dtype_ok(dt)) return -1;
   if (bl::plan_mx_few(M, N, K, mx_src(dt)).ok) return 0;

@@ -389,6 +389,15 @@ int bitlinear_quantize_mxfp4(const void* X, int dt, int64_t R, int64_t K, uint8_
 int bitlinear_forward_mxfp4(const uint8_t* codes, const uint8_t* scales, const uint8_t* xcodes,
                             const uint8_t* xscales, int64_t M, int64_t N, int64_t K, void* Y, int ydt, void* stream);
 int64_t bitlinear_forward_mxfp4_fused_ws_bytes(int64_t M, int64_t N, int64_t K, int dt);
+/*
+ * Host-only: the launches of bitlinear_forward_mxfp4 (xdt = -1) or of
+ * bitlinear_forward_mxfp4_fused (xdt = the type of X) for (M, N, K).  out[0] = 7: one kernel
+ * with the tokens' codes in LDS (up to 16 tokens), 8: the decode kernel, 9: the GEMM; out[1] =
+ * its workgroups, out[2] = threads per workgroup, out[3] and out[4] = tokens and outputs of a
+ * workgroup at a time, out[5] = launches (2: the quantiser first).  Returns BL_OK,
+ * BL_ERR_INVALID_ARG or BL_ERR_UNSUPPORTED as the calls do.
+ */
+int bitlinear_forward_mxfp4_plan(int64_t M, int64_t N, int64_t K, int xdt, int32_t out[6]);
 int bitlinear_forward_mxfp4_fused(const uint8_t* codes, const uint8_t* scales, const void* X, int dt, int64_t M,
                                   int64_t N, int64_t K, void* Y, int ydt, void* workspace, int64_t ws_bytes,
                                   void* stream);

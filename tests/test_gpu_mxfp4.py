@@ -6,6 +6,7 @@ import torch
 
 import bitlinear_fwd_amd as bl
 import mxfp4_reference as ref
+from test_mxfp4_cpu import VARIANTS
 from gpu_helpers import acts_host_f32, check_equal, host
 
 pytestmark = pytest.mark.gpu
@@ -127,7 +128,7 @@ PRODUCTS = [(1, 16, 32), (1, 1, 1), (2, 17, 33), (1, 6912, 2560), (3, 100, 513),
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("m,n,k", PRODUCTS)
+@pytest.mark.parametrize("m,n,k", PRODUCTS + [(520, 300, 640), (2100, 4000, 390), (513, 130, 129), (1000, 257, 2000)])
 def test_forward(m, n, k, dtype):
     print(f"case: forward_mxfp4 M={m} N={n} K={k} {dtype}", flush=True)
     x, w = outliers(m, k, seed=m + 1, dtype=DT[dtype]), outliers(n, k, seed=n + 2) * 0.02
@@ -151,7 +152,8 @@ def grid_matrix(r, k, seed, shift=0):
     return torch.from_numpy((v * 2.0 ** shift).astype(np.float32)).to(DEV)
 
 
-@pytest.mark.parametrize("m,n,k", PRODUCTS + [(5, 40, 28672), (70, 90, 28672), (150, 70, 4100)])
+@pytest.mark.parametrize("m,n,k", PRODUCTS + [(5, 40, 28672), (70, 90, 28672), (150, 70, 4100)]
+                         + [v[0] for v in VARIANTS])
 def test_forward_exact_sums(m, n, k):
     """All scales equal and every partial sum a multiple of 1/4 below 2^22: the product is exact, so
     any wrong element, scale or index shows."""
@@ -166,7 +168,7 @@ def test_forward_exact_sums(m, n, k):
     check_equal(host(bl.forward_mxfp4_fused(wc, ws, xb, n, k)).astype(np.float64), want, "fused bf16 y")
 
 
-@pytest.mark.parametrize("m", [1, 7, 16, 20, 64, 130])
+@pytest.mark.parametrize("m", [1, 7, 16, 20, 64, 130, 520])
 def test_forward_block_scales(m):
     """One block per row pair at its own power of two: each output is one product of scales."""
     k, n = 640, 48
@@ -181,7 +183,7 @@ def test_forward_block_scales(m):
     check_equal(host(bl.forward_mxfp4_fused(wc, ws, x, n, k)).astype(np.float64), want, "y")
 
 
-@pytest.mark.parametrize("m", [1, 4, 16, 40, 100, 200])
+@pytest.mark.parametrize("m", [1, 4, 16, 40, 100, 200, 520])
 def test_forward_nonfinite(m):
     """A NaN or an infinity spoils its token's row of the output, or its weight's column, and
     nothing else."""
@@ -274,7 +276,7 @@ def test_largest_k():
 def test_graph_replays_and_streams():
     """The products and the quantiser captured into a graph on a side stream, replayed with new
     inputs and eager work between, and two streams at once, against eager results."""
-    shapes = [(1, 300, 2560), (16, 128, 6912), (16, 64, 8704), (40, 500, 1000), (300, 600, 1500)]
+    shapes = [(1, 300, 2560), (16, 128, 6912), (16, 64, 8704), (40, 500, 1000), (600, 600, 1500)]
     w = [grid_matrix(n, k, i, shift=-3) for i, (m, n, k) in enumerate(shapes)]
     wq = [bl.quantize_mxfp4(t) for t in w]
     xs = [outliers(m, k, seed=i, dtype=torch.bfloat16) for i, (m, n, k) in enumerate(shapes)]
@@ -317,7 +319,7 @@ def test_graph_replays_and_streams():
 
 def test_workspace_of_the_caller():
     """A given workspace is used whatever it holds, and one serves calls of several shapes."""
-    shapes = [(20, 48, 640), (16, 40, 28672), (130, 200, 513)]
+    shapes = [(20, 48, 640), (16, 40, 28672), (530, 200, 513)]
     need = max(bl.forward_mxfp4_fused_ws_bytes(m, n, k, "f32") for m, n, k in shapes)
     assert need > 0 and bl.forward_mxfp4_fused_ws_bytes(1, 64, 2560) == 0
     ws = torch.full((need,), 0xFF, dtype=torch.uint8, device=DEV)
@@ -326,7 +328,7 @@ def test_workspace_of_the_caller():
         assert torch.equal(bl.forward_mxfp4_fused(*w, x, n, k, workspace=ws), bl.forward_mxfp4_fused(*w, x, n, k))
 
 
-@pytest.mark.parametrize("tokens", [1, 5, 16, 50, 300])
+@pytest.mark.parametrize("tokens", [1, 5, 16, 50, 300, 700])
 def test_norm_quantise_product_together(tokens):
     """A layer as it would be used: layer norm, its output quantised once for two projections, squared
     ReLU gating, and the down projection from the un-quantised hidden rows; against 64 bits on the

@@ -1,5 +1,7 @@
 """MXFP4 and layer norm on the host: size helpers, refusals, and the tests' own plain forms
 checked against hand-derived values.  No call here reaches a GPU."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -199,3 +201,32 @@ def test_reference_layernorm_gradients_by_differences():
             down = loss(x, w, b)
             arr[i] = keep
             assert abs((up - down) / 2e-5 - grad[i]) < 1e-6, i
+
+
+# (M, N, K), the kernel of the product and, of the fused call on bf16, its launches: each shape below is
+# one that the GPU tests run, so that every kernel form is reached there
+VARIANTS = [((1, 6912, 2560), ("lds", 16, 16), 1), ((16, 64, 8704), ("lds", 16, 16), 2),
+            ((16, 40, 28672), ("decode", 16, 16), 2), ((16, 4100, 28672), ("decode", 16, 32), 2),
+            ((17, 64, 128), ("decode", 32, 16), 2), ((20, 4100, 1100), ("decode", 32, 32), 2),
+            ((64, 2560, 2560), ("decode", 64, 16), 2), ((100, 4100, 1100), ("decode", 64, 32), 2),
+            ((520, 300, 640), ("gemm", 128, 128), 2), ((2100, 4000, 390), ("gemm", 128, 256), 2),
+            ((2050, 4100, 120), ("gemm", 128, 256), 2), ((600, 515, 1029), ("gemm", 128, 128), 2)]
+
+
+@pytest.mark.parametrize("shape,want,launches", VARIANTS)
+def test_plan(shape, want, launches):
+    p = bl.forward_mxfp4_plan(*shape)
+    assert (p["kernel"], p["tokens"], p["outputs"]) == want and p["launches"] == 1
+    f = bl.forward_mxfp4_plan(*shape, x="bf16")
+    assert f["launches"] == launches and (launches == 2) == (bl.forward_mxfp4_fused_ws_bytes(*shape) > 0)
+    m, n, k = shape
+    if p["kernel"] != "lds":  # workgroups cover the output once
+        assert p["workgroups"] == -(-m // p["tokens"]) * -(-n // p["outputs"])
+    assert p["threads"] in range(64, 1025, 64)
+
+
+def test_plan_refusals():
+    out = (ctypes.c_int32 * 6)()
+    f = bl.lib().bitlinear_forward_mxfp4_plan
+    assert f(0, 1, 1, -1, out) == BAD and f(1, 1, 1 << 25, -1, out) == BAD and f(1, 1, 1, -1, None) == BAD
+    assert f(1, 1, 1, 5, out) == UNS and f(1 << 30, 1 << 30, 1, -1, out) == UNS
