@@ -34,30 +34,51 @@ constexpr int64_t kCUs = 256;
 // (8192 x 8192 bf16: 82 us with one group, 65 with two).
 constexpr int kFewRows = 4;
 
-// Sum of each v[] over the threads that share a row; every thread gets it.  kTh 64: a wave.  Else
-// through LDS (red: kN values per wave of the row), with all threads of the workgroup taking part:
-// kTh threads, or kTh -1: `threads` of them, this one the i0-th.
-template <int kTh, int kN, typename F>
-__device__ __forceinline__ void row_sum(F (&v)[kN], F* red, int i0 = threadIdx.x, int threads = kTh) {
+// Sum over each 16 lanes, by lane moves; every lane gets its own 16's.
+__device__ __forceinline__ float sum16(float v) {
+  auto moved = [&](auto ctrl) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value, 0xf, 0xf, true));
+  };
+  v += moved(std::integral_constant<int, 0xB1>{});   // quad_perm 1 0 3 2
+  v += moved(std::integral_constant<int, 0x4E>{});   // quad_perm 2 3 0 1
+  v += moved(std::integral_constant<int, 0x141>{});  // row_half_mirror
+  v += moved(std::integral_constant<int, 0x140>{});  // row_mirror
+  return v;
+}
+__device__ __forceinline__ double sum16(double v) {
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) {
+  for (int off = 8; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
+  return v;
+}
+// Sum over a wave; every lane gets it.
+__device__ __forceinline__ float wave_sum(float v) {
+  v = sum16(v);
+  auto row = [&](int lane) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane)); };
+  return (row(0) + row(16)) + (row(32) + row(48));
+}
+__device__ __forceinline__ double wave_sum(double v) {
+  v = sum16(v);
+  v += __shfl_xor(v, 16, 64);
+  return v + __shfl_xor(v, 32, 64);
+}
+
+// Sum of each v[] over the threads that share a row; every thread gets it.  kWave: a wave.  Else up to
+// 16 waves, through LDS, with one barrier for all threads of the workgroup: `red` has kN values per
+// wave of the row, this thread is in the row's wave-th of `waves`.  Two sums in a row take two
+// different buffers, so that no thread writes what another still reads.
+template <bool kWave, int kN, typename F>
+__device__ __forceinline__ void row_sum(F (&v)[kN], F* red, int wave, int waves) {
 #pragma unroll
-    for (int j = 0; j < kN; ++j) v[j] += __shfl_xor(v[j], off, 64);
-  }
-  if constexpr (kTh != 64) {
-    __syncthreads();  // the values of the sum before have been read
+  for (int j = 0; j < kN; ++j) v[j] = wave_sum(v[j]);
+  if constexpr (!kWave) {
     if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-      for (int j = 0; j < kN; ++j) red[(i0 >> 6) * kN + j] = v[j];
+      for (int j = 0; j < kN; ++j) red[wave * kN + j] = v[j];
     }
     __syncthreads();
+    const int l = threadIdx.x & 15;
 #pragma unroll
-    for (int j = 0; j < kN; ++j) v[j] = red[j];
-#pragma unroll 4
-    for (int w = 1; w < threads >> 6; ++w) {
-#pragma unroll
-      for (int j = 0; j < kN; ++j) v[j] += red[w * kN + j];
-    }
+    for (int j = 0; j < kN; ++j) v[j] = sum16(l < waves ? red[l * kN + j] : F(0));
   }
 }
 
@@ -133,8 +154,7 @@ __global__ __launch_bounds__(kWave ? 256 : 1024) void k_layernorm(const T* __res
                                                                   const float* __restrict__ bias, float eps,
                                                                   T* __restrict__ Y, float* __restrict__ mean_out,
                                                                   float* __restrict__ rstd_out) {
-  __shared__ float red[16];
-  constexpr int kTh = kWave ? 64 : -1;
+  __shared__ float red[2][16];
   const int threads = kWave ? 64 : blockDim.x;
   const int i0 = kWave ? threadIdx.x & 63 : threadIdx.x;
   const int64_t step = (int64_t)gridDim.x * (kWave ? 4 : 1);
@@ -172,7 +192,7 @@ __global__ __launch_bounds__(kWave ? 256 : 1024) void k_layernorm(const T* __res
       for (int i = 0; i < 8; ++i) sum[0] += v[g][i];
     }
     fetch(row + step);
-    row_sum<kTh, 1>(sum, red, i0, threads);
+    row_sum<kWave, 1>(sum, red[0], i0 >> 6, threads >> 6);
     const float mean = sum[0] / (float)K;
 #pragma unroll
     for (int g = 0; g < kG; ++g) {
@@ -183,7 +203,7 @@ __global__ __launch_bounds__(kWave ? 256 : 1024) void k_layernorm(const T* __res
         sq[0] += v[g][i] * v[g][i];
       }
     }
-    row_sum<kTh, 1>(sq, red, i0, threads);
+    row_sum<kWave, 1>(sq, red[1], i0 >> 6, threads >> 6);
     const float rstd = 1.0f / sqrtf(sq[0] / (float)K + eps);
     if (i0 == 0) {
       if (mean_out) mean_out[row] = mean;
@@ -207,7 +227,7 @@ __global__ __launch_bounds__(1024) void k_layernorm_long(const T* __restrict__ X
                                                          const float* __restrict__ bias, float eps,
                                                          T* __restrict__ Y, float* __restrict__ mean_out,
                                                          float* __restrict__ rstd_out) {
-  __shared__ double red[16];
+  __shared__ double red[2][16];
   for (int64_t row = blockIdx.x; row < M; row += gridDim.x) {
     const T* x = X + row * K;
     double s[1] = {0.0};
@@ -217,7 +237,7 @@ __global__ __launch_bounds__(1024) void k_layernorm_long(const T* __restrict__ X
 #pragma unroll
       for (int i = 0; i < 8; ++i) s[0] += (double)v[i];
     }
-    row_sum<1024, 1>(s, red);
+    row_sum<false, 1>(s, red[0], threadIdx.x >> 6, 16);
     const double mean = s[0] / (double)K;
     double q[1] = {0.0};
     for (int64_t col = 8 * (int64_t)threadIdx.x; col < K; col += 8 * 1024) {
@@ -229,7 +249,7 @@ __global__ __launch_bounds__(1024) void k_layernorm_long(const T* __restrict__ X
         q[0] += d * d;
       }
     }
-    row_sum<1024, 1>(q, red);
+    row_sum<false, 1>(q, red[1], threadIdx.x >> 6, 16);
     const float meanf = (float)mean, rstd = (float)(1.0 / sqrt(q[0] / (double)K + (double)eps));
     if (threadIdx.x == 0) {
       if (mean_out) mean_out[row] = meanf;
@@ -258,7 +278,7 @@ __global__ __launch_bounds__(kG == 1 ? 1024 : 768) void k_layernorm_bwd(
     const T* __restrict__ dY, const T* __restrict__ X, int64_t M, int64_t K, int rows, int threads,
     const float* __restrict__ weight, const float* __restrict__ mean_in, const float* __restrict__ rstd_in,
     T* __restrict__ dX, float* __restrict__ part) {
-  __shared__ float red[32];        // two values per wave
+  __shared__ float red[2][32];     // two values per wave, in turns
   extern __shared__ float sums[];  // [2][8 kG][threads] where rows > 1
   const int sub = kWave ? threadIdx.x >> 6 : threadIdx.x / threads;
   const int i0 = kWave ? threadIdx.x & 63 : threadIdx.x - sub * threads;
@@ -288,6 +308,7 @@ __global__ __launch_bounds__(kG == 1 ? 1024 : 768) void k_layernorm_bwd(
     rrstd = in ? rstd_in[row] : 0.0f;
   };
   const int64_t first = (int64_t)blockIdx.x * rows, step = (int64_t)gridDim.x * rows;
+  int turn = 0;
   fetch(first + sub);
   for (int64_t r0 = first; r0 < M; r0 += step) {  // the same trips for every thread: barriers inside
     float x[kG][8], d[kG][8];
@@ -314,7 +335,8 @@ __global__ __launch_bounds__(kG == 1 ? 1024 : 768) void k_layernorm_bwd(
       }
     }
     if (dX) {
-      row_sum<kWave ? 64 : -1, 2>(c, red + 2 * sub * (threads >> 6), i0, threads);
+      row_sum<kWave, 2>(c, red[turn] + 2 * sub * (threads >> 6), i0 >> 6, threads >> 6);
+      turn ^= 1;
       c[0] /= (float)K;
       c[1] /= (float)K;
       const int64_t row = r0 + sub;
@@ -365,7 +387,8 @@ __global__ __launch_bounds__(1024) void k_layernorm_bwd_long(const T* __restrict
                                                              int64_t M, int64_t K, const float* __restrict__ weight,
                                                              const float* __restrict__ mean_in,
                                                              const float* __restrict__ rstd_in, T* __restrict__ dX) {
-  __shared__ double red[32];
+  __shared__ double red[2][32];
+  int turn = 0;
   for (int64_t row = blockIdx.x; row < M; row += gridDim.x) {
     const float mean = mean_in[row], rstd = rstd_in[row];
     double c[2] = {0.0, 0.0};
@@ -381,7 +404,8 @@ __global__ __launch_bounds__(1024) void k_layernorm_bwd_long(const T* __restrict
         c[1] += (double)g * (double)((x[i] - mean) * rstd);
       }
     }
-    row_sum<1024, 2>(c, red);
+    row_sum<false, 2>(c, red[turn], threadIdx.x >> 6, 16);
+    turn ^= 1;
     const float c0 = (float)(c[0] / (double)K), c1 = (float)(c[1] / (double)K);
     for (int64_t col = 8 * (int64_t)threadIdx.x; col < K; col += 8 * 1024) {
       float x[8], d[8], w[8];
