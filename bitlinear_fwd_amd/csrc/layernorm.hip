@@ -14,10 +14,12 @@
 // Both are bound by memory: x (and dy) in, y (dx) out.  A row is shared by a wave (up to 1024
 // elements, forward) or by as many waves as hold it with one or two groups of 8 elements a thread;
 // rows longer than 32768 (backward 12288) elements are read again for each sum, with the sums in
-// fp64.  Measured (a large copy moves 5.2 TB/s): forward 8192 x 8192 bf16 53 us, 5.1 TB/s; 2048 x 8192
-// fp32 27.4 us, 4.9 TB/s; 16 x 2560 bf16 3.5 us, a launch and one round trip to memory.  Backward 2048
-// x 2560 bf16 18.1 us, of which the second launch takes 4 and the first about 7 before and after its
-// rows (2.7 us for every 768 of them, 4.4 TB/s); 1003 x 7001 fp32 28.8 us.
+// fp64.  Measured (a large copy moves 5.2 TB/s): forward 8192 x 8192 bf16 49.6 us, 5.4 TB/s; 2048 x
+// 8192 fp32 27.4 us, 4.9 TB/s; 16 x 2560 bf16 3.2 us, a launch and one round trip to memory.  Backward
+// 8192 x 8192 bf16 91 us, 4.4 TB/s; 2048 x 2560 bf16 16.6 us, of which the second launch takes 4 and the
+// first about 6 before and after its rows; 1003 x 7001 fp32 26.2 us.  The sums over a row cost most
+// after the bytes: with lane exchanges through LDS and two barriers each, 8192 x 8192 took 53 us
+// forward and 112 backward.
 #include "layernorm.h"
 
 #include <algorithm>
@@ -167,7 +169,10 @@ __global__ __launch_bounds__(kWave ? 256 : 1024) void k_layernorm(const T* __res
       raw[g] = load_group(X + r * K, c8, r < M ? K : 0);
     }
   };
-  fetch(row);
+  // four groups of fp32 leave no registers for a row ahead (2048 x 20000: 77 us, 125
+  // with one, which spills)
+  constexpr bool kAhead = kG < 4 || sizeof(T) == 2;
+  if constexpr (kAhead) fetch(row);
   float w[kG][8], b[kG][8];
   auto params = [&](int g) {
     const Cols c8 = cols<T>(i0, g, threads);
@@ -185,13 +190,14 @@ __global__ __launch_bounds__(kWave ? 256 : 1024) void k_layernorm(const T* __res
   }
   for (; row < M; row += step) {
     float v[kG][8], sum[1] = {0.0f}, sq[1] = {0.0f};
+    if constexpr (!kAhead) fetch(row);
 #pragma unroll
     for (int g = 0; g < kG; ++g) {
       widen8(raw[g], v[g]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum[0] += v[g][i];
     }
-    fetch(row + step);
+    if constexpr (kAhead) fetch(row + step);
     row_sum<kWave, 1>(sum, red[0], i0 >> 6, threads >> 6);
     const float mean = sum[0] / (float)K;
 #pragma unroll
@@ -309,16 +315,20 @@ __global__ __launch_bounds__(kG == 1 ? 1024 : 768) void k_layernorm_bwd(
   };
   const int64_t first = (int64_t)blockIdx.x * rows, step = (int64_t)gridDim.x * rows;
   int turn = 0;
-  fetch(first + sub);
+  // two groups of fp32 leave no registers for a row ahead (2048 x 11000: 63.5 us, 83.9
+  // with one, which spills)
+  constexpr bool kAhead = kG == 1 || sizeof(T) == 2;
+  if constexpr (kAhead) fetch(first + sub);
   for (int64_t r0 = first; r0 < M; r0 += step) {  // the same trips for every thread: barriers inside
     float x[kG][8], d[kG][8];
+    if constexpr (!kAhead) fetch(r0 + sub);
     const float mean = rmean, rstd = rrstd;
 #pragma unroll
     for (int g = 0; g < kG; ++g) {
       widen8(rx[g], x[g]);
       widen8(rd[g], d[g]);
     }
-    fetch(r0 + step + sub);
+    if constexpr (kAhead) fetch(r0 + step + sub);
     float c[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int g = 0; g < kG; ++g) {
@@ -548,7 +558,8 @@ LnBwdPlan plan_layernorm_backward(int64_t M, int64_t K) {
   LnBwdPlan p;
   // one group of 8 elements per thread up to 16 waves a row, and as many rows as 16 waves hold (one
   // workgroup to a compute unit, so one partial row each); two groups and one row up to 12 waves.
-  // 512 workgroups with half the rows write twice the partial rows: 2048 x 2560 bf16 21.1 us, 18.1 so.
+  // Fewer workgroups write fewer partial rows, and lose more than that: 2048 x 2560 bf16 18.2 us, 20.6
+  // with 192, 23.7 with 128.
   if (K <= 12288) {
     p.groups = K <= 8192 ? 1 : 2;
     const int waves = (int)((K + 512 * p.groups - 1) / (512 * p.groups));
