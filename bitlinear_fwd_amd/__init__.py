@@ -908,18 +908,68 @@ class BitLinear:
         return y
 
 
-# The calls below take a few microseconds of host time each, so their checks read every attribute
-# once and allocate nothing that the caller has given.
+# The calls below take a few microseconds of host time each, a launch included, so what they need of
+# torch and of the library is looked up once, their checks read every attribute once, and they
+# allocate nothing that the caller has given.
 
 
-def _dtype_code(t, name: str) -> int:
-    import torch
+class _Runtime:
+    """torch and the library, bound on the first call."""
 
-    if t == torch.bfloat16:
-        return BL_BF16
-    if t == torch.float32:
-        return BL_F32
-    raise ValueError(f"{name} must be float32 or bfloat16")
+    def __init__(self):
+        import torch
+
+        L = lib()
+        self.torch, self.empty, self.empty_like = torch, torch.empty, torch.empty_like
+        self.stream, self.current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        self.u8, self.f32 = torch.uint8, torch.float32
+        self.codes = {torch.float32: BL_F32, torch.bfloat16: BL_BF16}
+        self.quantize_mxfp4 = L.bitlinear_quantize_mxfp4
+        self.forward_mxfp4 = L.bitlinear_forward_mxfp4
+        self.forward_mxfp4_fused = L.bitlinear_forward_mxfp4_fused
+        self.fused_ws_bytes = L.bitlinear_forward_mxfp4_fused_ws_bytes
+        self.layernorm = L.bitlinear_layernorm
+        self.layernorm_backward = L.bitlinear_layernorm_backward
+        self.backward_ws_bytes = L.bitlinear_layernorm_backward_ws_bytes
+
+
+_RT = None
+
+
+def _runtime() -> _Runtime:
+    global _RT
+    if _RT is None:
+        _RT = _Runtime()
+    return _RT
+
+
+def _call(rt, f, index: int, args) -> None:
+    """The library call `f` on the device's current stream, with the device the current one."""
+    if rt.current() == index:
+        st = f(*args, rt.stream(index))
+    else:
+        with rt.torch.cuda.device(index):
+            st = f(*args, rt.stream(index))
+    if st != BL_OK:
+        _check(f.__name__, st)
+
+
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _dtype_code(rt, dtype, name: str) -> int:
+    code = rt.codes.get(dtype)
+    if code is None:
+        raise ValueError(f"{name} must be float32 or bfloat16")
+    return code
+
+
+def _require_rows(rt, t, name: str) -> int:
+    """A contiguous GPU matrix of fp32 or bf16 rows; returns its bl_dtype."""
+    if t.is_cuda and t.is_contiguous() and t.dim() == 2 and t.numel():
+        return _dtype_code(rt, t.dtype, name)
+    raise ValueError(f"{name} must be a non-empty contiguous 2-D GPU tensor")
 
 
 def _given(t, name: str, shape, dtype, index: int):
@@ -930,46 +980,12 @@ def _given(t, name: str, shape, dtype, index: int):
     return t
 
 
-def _bytes_at_least(t, name: str, nbytes: int, index: int) -> int:
+def _bytes_at_least(rt, t, name: str, nbytes: int, index: int) -> int:
     """The address of `t`, checked to be a contiguous uint8 tensor of at least nbytes on the
     device."""
-    import torch
-
-    if t.get_device() != index or t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() < nbytes:
+    if t.get_device() != index or t.dtype != rt.u8 or not t.is_contiguous() or t.numel() < nbytes:
         raise ValueError(f"{name} must be a contiguous uint8 tensor of at least {nbytes} bytes on cuda:{index}")
     return t.data_ptr()
-
-
-def _call(fn: str, index: int, *args) -> None:
-    """The library call on the device's current stream, with the device the current one."""
-    import torch
-
-    f = getattr(_lib or lib(), fn)
-    stream = torch._C._cuda_getCurrentRawStream(index)
-    if torch._C._cuda_getDevice() == index:
-        st = f(*args, stream)
-    else:
-        with torch.cuda.device(index):
-            st = f(*args, stream)
-    if st != BL_OK:
-        _check(fn, st)
-
-
-def _ptr(t):
-    return t.data_ptr() if t is not None else None
-
-
-def _require_rows(t, name: str) -> int:
-    """A contiguous GPU matrix of fp32 or bf16 rows; returns its bl_dtype."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D")
-    if t.numel() == 0:
-        raise ValueError(f"{name} must not be empty")
-    return _dtype_code(t.dtype, name)
 
 
 def mxfp4_codes_bytes(rows: int, k: int) -> int:
@@ -989,51 +1005,48 @@ def quantize_mxfp4(x, codes=None, scales=None, values=None, want_values: bool = 
     Returns ``(codes uint8, scales uint8)`` in the layout of bitlinear.h, plus ``values``
     ([R][K] of x's type, what the codes stand for) when ``want_values`` is set or ``values``
     is given."""
-    import torch
-
-    dt = _require_rows(x, "x")
+    rt = _RT or _runtime()
+    dt = _require_rows(rt, x, "x")
     r, k = x.shape
     dev = x.get_device()
     nc, ns = mxfp4_codes_bytes(r, k), mxfp4_scales_bytes(r, k)
     if codes is None:
-        codes = torch.empty(nc, dtype=torch.uint8, device=x.device)
+        codes = rt.empty(nc, dtype=rt.u8, device=x.device)
     if scales is None:
-        scales = torch.empty(ns, dtype=torch.uint8, device=x.device)
+        scales = rt.empty(ns, dtype=rt.u8, device=x.device)
     if values is not None:
         _given(values, "values", (r, k), x.dtype, dev)
     elif want_values:
-        values = torch.empty_like(x)
-    _call("bitlinear_quantize_mxfp4", dev, x.data_ptr(), dt, r, k, _bytes_at_least(codes, "codes", nc, dev),
-          _bytes_at_least(scales, "scales", ns, dev), _ptr(values))
+        values = rt.empty_like(x)
+    _call(rt, rt.quantize_mxfp4, dev, (x.data_ptr(), dt, r, k, _bytes_at_least(rt, codes, "codes", nc, dev),
+                                       _bytes_at_least(rt, scales, "scales", ns, dev), _ptr(values)))
     return (codes, scales, values) if values is not None else (codes, scales)
 
 
-def _product_output(y, out_dtype, m: int, n: int, like):
+def _product_output(rt, y, out_dtype, m: int, n: int, like):
     """(y, its bl_dtype) of a product: the caller's or a new one on like's device."""
-    import torch
-
     if y is not None:
         dtype = out_dtype or y.dtype
-        ydt = _dtype_code(dtype, "out_dtype")
-        return _given(y, "y", (m, n), dtype, like.get_device()), ydt
-    dtype = out_dtype or torch.float32
-    ydt = _dtype_code(dtype, "out_dtype")
-    return torch.empty((max(m, 0), max(n, 0)), dtype=dtype, device=like.device), ydt
+        return _given(y, "y", (m, n), dtype, like.get_device()), _dtype_code(rt, dtype, "out_dtype")
+    dtype = out_dtype or rt.f32
+    ydt = _dtype_code(rt, dtype, "out_dtype")
+    return rt.empty((max(m, 0), max(n, 0)), dtype=dtype, device=like.device), ydt
 
 
 def forward_mxfp4(codes, scales, xcodes, xscales, m: int, n: int, k: int, y=None, out_dtype=None):
     """y[M][N] = Xv Wv^T of MXFP4 activations (xcodes, xscales: M rows) and weights (codes,
     scales: N rows), both of K columns, accumulated in fp32; y in ``out_dtype`` (fp32, or
     bf16), or in that of the given ``y``."""
+    rt = _RT or _runtime()
     dev = codes.get_device()
     if dev < 0:
         raise ValueError("codes must be a GPU tensor")
-    ptrs = (_bytes_at_least(codes, "codes", mxfp4_codes_bytes(n, k), dev),
-            _bytes_at_least(scales, "scales", mxfp4_scales_bytes(n, k), dev),
-            _bytes_at_least(xcodes, "xcodes", mxfp4_codes_bytes(m, k), dev),
-            _bytes_at_least(xscales, "xscales", mxfp4_scales_bytes(m, k), dev))
-    y, ydt = _product_output(y, out_dtype, m, n, codes)
-    _call("bitlinear_forward_mxfp4", dev, *ptrs, m, n, k, y.data_ptr(), ydt)
+    wc = _bytes_at_least(rt, codes, "codes", mxfp4_codes_bytes(n, k), dev)
+    ws = _bytes_at_least(rt, scales, "scales", mxfp4_scales_bytes(n, k), dev)
+    xc = _bytes_at_least(rt, xcodes, "xcodes", mxfp4_codes_bytes(m, k), dev)
+    xs = _bytes_at_least(rt, xscales, "xscales", mxfp4_scales_bytes(m, k), dev)
+    y, ydt = _product_output(rt, y, out_dtype, m, n, codes)
+    _call(rt, rt.forward_mxfp4, dev, (wc, ws, xc, xs, m, n, k, y.data_ptr(), ydt))
     return y
 
 
@@ -1059,43 +1072,41 @@ def forward_mxfp4_fused(codes, scales, x, n: int, k: int, y=None, workspace=None
     """Quantise x[M][K] (fp32 or bf16) to MXFP4 and apply MXFP4 weights (codes, scales: N
     rows) in one call; y[M][N] as forward_mxfp4.  A workspace of at least
     forward_mxfp4_fused_ws_bytes is allocated unless one is given."""
-    import torch
-
-    dt = _require_rows(x, "x")
-    m = x.shape[0]
-    if x.shape[1] != k:
+    rt = _RT or _runtime()
+    dt = _require_rows(rt, x, "x")
+    m, cols = x.shape
+    if cols != k:
         raise ValueError("x must be [tokens, K]")
     dev = x.get_device()
-    wc = _bytes_at_least(codes, "codes", mxfp4_codes_bytes(n, k), dev)
-    ws = _bytes_at_least(scales, "scales", mxfp4_scales_bytes(n, k), dev)
-    y, ydt = _product_output(y, out_dtype, m, n, x)
-    need = (_lib or lib()).bitlinear_forward_mxfp4_fused_ws_bytes(m, n, k, dt)
+    wc = _bytes_at_least(rt, codes, "codes", mxfp4_codes_bytes(n, k), dev)
+    ws = _bytes_at_least(rt, scales, "scales", mxfp4_scales_bytes(n, k), dev)
+    y, ydt = _product_output(rt, y, out_dtype, m, n, x)
+    need = rt.fused_ws_bytes(m, n, k, dt)
     if workspace is not None:
-        _bytes_at_least(workspace, "workspace", need, dev)
+        _bytes_at_least(rt, workspace, "workspace", need, dev)
     elif need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    _call("bitlinear_forward_mxfp4_fused", dev, wc, ws, x.data_ptr(), dt, m, n, k, y.data_ptr(), ydt,
-          _ptr(workspace), workspace.numel() if workspace is not None else 0)
+        workspace = rt.empty(need, dtype=rt.u8, device=x.device)
+    _call(rt, rt.forward_mxfp4_fused, dev, (wc, ws, x.data_ptr(), dt, m, n, k, y.data_ptr(), ydt, _ptr(workspace),
+                                            workspace.numel() if workspace is not None else 0))
     return y
 
 
 def layernorm(x, weight=None, bias=None, eps: float = 1e-5, y=None, mean=None, rstd=None):
     """Layer normalisation of the rows of x[M][K] (fp32 or bf16) with fp32 weight and bias
     (None: ones, zeros).  Returns ``(y, mean fp32 [M], rstd fp32 [M])``; y has x's type."""
-    import torch
-
-    dt = _require_rows(x, "x")
+    rt = _RT or _runtime()
+    dt = _require_rows(rt, x, "x")
     m, k = x.shape
-    dev, f32 = x.get_device(), torch.float32
+    dev, f32, device = x.get_device(), rt.f32, x.device
     if weight is not None:
         _given(weight, "weight", (k,), f32, dev)
     if bias is not None:
         _given(bias, "bias", (k,), f32, dev)
-    y = torch.empty_like(x) if y is None else _given(y, "y", (m, k), x.dtype, dev)
-    mean = torch.empty(m, dtype=f32, device=x.device) if mean is None else _given(mean, "mean", (m,), f32, dev)
-    rstd = torch.empty(m, dtype=f32, device=x.device) if rstd is None else _given(rstd, "rstd", (m,), f32, dev)
-    _call("bitlinear_layernorm", dev, x.data_ptr(), dt, m, k, _ptr(weight), _ptr(bias), eps, y.data_ptr(),
-          mean.data_ptr(), rstd.data_ptr())
+    y = rt.empty_like(x) if y is None else _given(y, "y", (m, k), x.dtype, dev)
+    mean = rt.empty(m, dtype=f32, device=device) if mean is None else _given(mean, "mean", (m,), f32, dev)
+    rstd = rt.empty(m, dtype=f32, device=device) if rstd is None else _given(rstd, "rstd", (m,), f32, dev)
+    _call(rt, rt.layernorm, dev, (x.data_ptr(), dt, m, k, _ptr(weight), _ptr(bias), eps, y.data_ptr(),
+                                  mean.data_ptr(), rstd.data_ptr()))
     return y, mean, rstd
 
 
@@ -1113,11 +1124,10 @@ def layernorm_backward(dy, x, weight, mean, rstd, dx=None, dweight=None, dbias=N
     from the forward call.  Returns ``(dx, dweight, dbias)``, or ``dx`` alone with
     ``want_params=False``; dx has x's type, the others are fp32 and overwritten.  A workspace
     of at least layernorm_backward_ws_bytes is allocated unless one is given."""
-    import torch
-
-    dt = _require_rows(x, "x")
+    rt = _RT or _runtime()
+    dt = _require_rows(rt, x, "x")
     m, k = x.shape
-    dev, f32 = x.get_device(), torch.float32
+    dev, f32, device = x.get_device(), rt.f32, x.device
     if mean is None or rstd is None:
         raise ValueError("mean and rstd of the forward call are needed")
     _given(dy, "dy", (m, k), x.dtype, dev)
@@ -1125,20 +1135,20 @@ def layernorm_backward(dy, x, weight, mean, rstd, dx=None, dweight=None, dbias=N
     _given(rstd, "rstd", (m,), f32, dev)
     if weight is not None:
         _given(weight, "weight", (k,), f32, dev)
-    dx = torch.empty_like(x) if dx is None else _given(dx, "dx", (m, k), x.dtype, dev)
+    dx = rt.empty_like(x) if dx is None else _given(dx, "dx", (m, k), x.dtype, dev)
     if want_params:
-        dweight = (torch.empty(k, dtype=f32, device=x.device) if dweight is None
+        dweight = (rt.empty(k, dtype=f32, device=device) if dweight is None
                    else _given(dweight, "dweight", (k,), f32, dev))
-        dbias = (torch.empty(k, dtype=f32, device=x.device) if dbias is None
+        dbias = (rt.empty(k, dtype=f32, device=device) if dbias is None
                  else _given(dbias, "dbias", (k,), f32, dev))
-        need = (_lib or lib()).bitlinear_layernorm_backward_ws_bytes(m, k)
+        need = rt.backward_ws_bytes(m, k)
         if workspace is None:
-            workspace = torch.empty(max(need, 0), dtype=torch.uint8, device=x.device)
+            workspace = rt.empty(max(need, 0), dtype=rt.u8, device=device)
         else:
-            _bytes_at_least(workspace, "workspace", need, dev)
+            _bytes_at_least(rt, workspace, "workspace", need, dev)
     else:
         dweight = dbias = workspace = None
-    _call("bitlinear_layernorm_backward", dev, dy.data_ptr(), x.data_ptr(), dt, m, k, _ptr(weight), mean.data_ptr(),
-          rstd.data_ptr(), dx.data_ptr(), _ptr(dweight), _ptr(dbias), _ptr(workspace),
-          workspace.numel() if workspace is not None else 0)
+    _call(rt, rt.layernorm_backward, dev,
+          (dy.data_ptr(), x.data_ptr(), dt, m, k, _ptr(weight), mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(),
+           _ptr(dweight), _ptr(dbias), _ptr(workspace), workspace.numel() if workspace is not None else 0))
     return (dx, dweight, dbias) if want_params else dx
