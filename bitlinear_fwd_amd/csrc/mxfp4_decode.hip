@@ -169,7 +169,8 @@ __global__ __launch_bounds__(1024) void k_mx_few(const uint8_t* __restrict__ cod
   int sw[2];
   auto fetch = [&](int64_t nb, int g, v4i (&v)[4], int& sc) {
     const bool in = nb < nblocks;
-    sc = in ? __builtin_nontemporal_load(reinterpret_cast<const int*>(scales + ((nb * groups + g) * 64 + lane) * 4)) : 0;
+    const int* sp = reinterpret_cast<const int*>(scales + ((nb * groups + g) * 64 + lane) * 4);
+    sc = in ? __builtin_nontemporal_load(sp) : 0;
     static_for<4>([&](auto t) {
       v[t] = v4i{0, 0, 0, 0};
       if (in && 4 * g + t < tiles)

@@ -1,5 +1,5 @@
 // MXFP4 product for many tokens: Y[M][N] = sum_k Xv[m][k] Wv[n][k], both matrices as codes and
-// scales in the layout of mxfp4.h, on the scaled matrix instructions (16x16x128, 4-bit operands).
+// scales in the layout of mxfp4.h, on the scaled matrix instructions (32x32x64, 4-bit operands).
 //
 // At 4 bits the matrix cores outrun the operands: a 32x32x64 step takes 32 cycles and eats 2 KiB, so
 // what decides is how often a loaded byte is used and what else runs meanwhile.  Output tiles of 128
@@ -82,9 +82,10 @@ constexpr int kWN = 2, kWM = 2;  // waves of a workgroup along the outputs and a
 // Each wave has kN x kM blocks of 16 weight rows and 16 tokens: output tiles of 16 kWM kM tokens x 16
 // kWN kN outputs.  kR stages of 128 columns in the ring.
 template <int kN, int kM, int kR, typename TY>
-__global__ __launch_bounds__(64 * kWN * kWM) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_mx_gemm(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, const uint8_t* __restrict__ xcodes,
-          const uint8_t* __restrict__ xscales, int64_t M, int64_t N, int tiles, int groups, int nblocks, int xblocks,
-          int tiles_m, int tiles_n, int band, TY* __restrict__ Y) {
+__global__ __launch_bounds__(64 * kWN * kWM) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_mx_gemm(
+    const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, const uint8_t* __restrict__ xcodes,
+    const uint8_t* __restrict__ xscales, int64_t M, int64_t N, int tiles, int groups, int nblocks, int xblocks,
+    int tiles_m, int tiles_n, int band, TY* __restrict__ Y) {
   constexpr int W = kWN * kWM;
   constexpr int BN = kWN * kN, BM = kWM * kM;     // row blocks of a stage: weights, then tokens
   constexpr int kBlocks = BN + BM;

@@ -14,7 +14,10 @@ U = 2.0 ** -24
 
 # one element, rows shared by a wave, by 256 and by 1024 threads, longer rows; odd sizes around each
 SIZES = [(1, 1), (3, 7), (2, 8), (5, 64), (9, 513), (4, 2048), (3, 2049), (7, 2560), (6, 5000), (5, 8192), (2, 8193),
-         (3, 28672), (2, 32768), (2, 32775), (1, 100003), (700, 40), (1030, 257), (530, 2560)]
+         (3, 28672), (2, 32768), (2, 32775), (1, 100003), (700, 40), (1030, 257), (530, 2560),
+         # enough rows that a workgroup walks over several, in each form
+         (9000, 100), (5300, 600), (1100, 1500), (1700, 2560), (1050, 5001), (1030, 8192), (300, 8000), (600, 12288),
+         (300, 12289), (520, 20000)]
 
 
 def data(m, k, dtype, seed, offset=0.5):
@@ -120,6 +123,22 @@ def test_layernorm_backward_subsets(m, k):
                                                    mean.data_ptr(), rstd.data_ptr(), *ptr, ws.data_ptr(), ws.numel(), s)
         assert st == bl.BL_OK
         assert torch.equal(out, full[i])
+
+
+@pytest.mark.parametrize("m,k", [(5, 100), (7, 3000), (3, 40000)])
+def test_layernorm_without_statistics(m, k):
+    """mean and rstd may be null, each by itself or both, and so may weight and bias."""
+    x, w, b, _ = data(m, k, "bf16", seed=k)
+    y, mean, rstd = bl.layernorm(x, w, b, 1e-5)
+    s = torch.cuda.current_stream().cuda_stream
+    for give in ((True, False), (False, True), (False, False)):
+        out = torch.empty_like(x)
+        stats = [torch.full((m,), 7.0, device=DEV) for _ in range(2)]
+        st = bl.lib().bitlinear_layernorm(x.data_ptr(), bl.BL_BF16, m, k, w.data_ptr(), b.data_ptr(), 1e-5,
+                                          out.data_ptr(), *(t.data_ptr() if g else None for t, g in zip(stats, give)), s)
+        assert st == bl.BL_OK and torch.equal(out, y)
+        for t, g, want in zip(stats, give, (mean, rstd)):
+            assert torch.equal(t, want if g else torch.full_like(t, 7.0))
 
 
 def test_layernorm_nonfinite_rows_stay_apart():
