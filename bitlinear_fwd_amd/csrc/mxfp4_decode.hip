@@ -227,8 +227,10 @@ __global__ __launch_bounds__(1024) void k_mx_few(const uint8_t* __restrict__ cod
       quantize(std::integral_constant<int, 1>{});
     else if (items <= 2 * pairs)
       quantize(std::integral_constant<int, 2>{});
-    else
+    else if (sizeof(T) == 4 || items <= 4 * pairs)
       quantize(std::integral_constant<int, 4>{});
+    else
+      quantize(std::integral_constant<int, sizeof(T) == 4 ? 4 : 8>{});
   }
   if (wave >= workers) {  // more waves than groups of tiles: they have quantised, and keep the barriers
     lds_barrier();
@@ -288,7 +290,7 @@ void launch(const MxDecodePlan& p, const uint8_t* codes, const uint8_t* scales, 
 
 // Blocks that a workgroup quantises by itself at most; beyond, the quantiser runs first.  Measured, one
 // launch against two (graph replays; the issue of an eager call takes 9.3 and 14 us): 16 x 2560 x 2560
-// 5.6 and 7.4 us, 16 x 2560 x 6912 (3584 blocks) 9.5 and 9.3, 4 x 8192 x 28672 (3584) 25.4 and 26.3.
+// 5.6 and 7.4 us, 16 x 2560 x 6912 (3584 blocks) 9.1 and 9.3, 4 x 8192 x 28672 (3584) 25.4 and 26.3.
 constexpr int64_t kFewItems = 4096;
 
 MxFewPlan plan_mx_few(int64_t M, int64_t N, int64_t K, int src) {

@@ -46,7 +46,8 @@ __device__ __forceinline__ void ring_wait() {
 }
 
 // Two direct loads of 1 KiB (16 bytes per lane at `off`) from a and b to consecutive KiB of LDS from
-// byte address `lds`.  The wait states: M0 and the bases may have been written just before.
+// byte address `lds`.  The wait states: M0 and the bases may have been written just before.  Nothing else
+// in these kernels uses M0 (which cannot be named as clobbered).
 __device__ __forceinline__ void load2_lds(const uint8_t* a, const uint8_t* b, uint32_t off, uint32_t lds) {
   asm volatile(
       "s_nop 4\n\t"
