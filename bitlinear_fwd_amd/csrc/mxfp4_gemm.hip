@@ -81,9 +81,11 @@ __device__ __forceinline__ T* uniform_ptr(T* p) {
 constexpr int kWN = 2, kWM = 2;  // waves of a workgroup along the outputs and along the tokens
 
 // Each wave has kN x kM blocks of 16 weight rows and 16 tokens: output tiles of 16 kWM kM tokens x 16
-// kWN kN outputs.  kR stages of 128 columns in the ring.
-template <int kN, int kM, int kR, typename TY>
-__global__ __launch_bounds__(64 * kWN * kWM) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_mx_gemm(
+// kWN kN outputs.  kR stages of 128 columns in the ring.  kKS 2: two groups of such waves, each with a
+// ring of its own, take half of the columns each (in whole groups of four stages, the first group's no
+// fewer) and add their sums through LDS; both go through the same number of barriers.
+template <int kN, int kM, int kR, int kKS, typename TY>
+__global__ __launch_bounds__(64 * kWN * kWM * kKS) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_mx_gemm(
     const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, const uint8_t* __restrict__ xcodes,
     const uint8_t* __restrict__ xscales, int64_t M, int64_t N, int tiles, int groups, int nblocks, int xblocks,
     int tiles_m, int tiles_n, int band, TY* __restrict__ Y) {
@@ -94,11 +96,18 @@ __global__ __launch_bounds__(64 * kWN * kWM) __attribute__((amdgpu_waves_per_eu(
   constexpr int L = kBlocks / W;                  // direct loads per wave and stage
   constexpr int S = (kBlocks / 4 + W - 1) / W;    // and per wave and four stages, of scales
   constexpr int TN = kN / 2, TM = kM / 2;         // 32-row tiles of a wave
+  constexpr int kGroupLds = kR * kStage + kBlocks * 256;  // a ring and its scales
   static_assert(L % 2 == 0, "direct loads come in pairs");
-  extern __shared__ uint8_t lds[];                // the ring, then kBlocks x 256 bytes of scales
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  static_assert(kKS == 1 || (kKS == 2 && TM == 2), "the two groups keep one of two token tiles each");
+  extern __shared__ uint8_t lds_all[];            // per group a ring, then kBlocks x 256 bytes of scales
+  const int lane = threadIdx.x & 63, wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kg = wave_all / W, wave = wave_all % W;
   const int wn = wave % kWN, wm = wave / kWN;
+  uint8_t* lds = lds_all + kg * kGroupLds;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)lds;
+  // this group's stages: `count` from stage `first`; `steps` for both
+  const int steps = kKS == 1 ? tiles : min(tiles, (tiles + 7) / 8 * 4);
+  const int first = kg * steps, count = kg == 0 ? steps : tiles - first;
 
   // tile of this workgroup: contiguous runs per XCD
   int id = blockIdx.x;
@@ -119,13 +128,16 @@ __global__ __launch_bounds__(64 * kWN * kWM) __attribute__((amdgpu_waves_per_eu(
   // blocks each; waves past the last repeat it, so that all have the same number in flight)
   const uint8_t* src[L];
 #pragma unroll
-  for (int j = 0; j < L; ++j) src[j] = uniform_ptr(block(L * wave + j, codes, xcodes, (int64_t)tiles * kMxTileBytes));
+  for (int j = 0; j < L; ++j)
+    src[j] = uniform_ptr(block(L * wave + j, codes, xcodes, (int64_t)tiles * kMxTileBytes) +
+                         (int64_t)first * kMxTileBytes);
   const uint8_t* ssrc[S];
   int sdst[S];
 #pragma unroll
   for (int j = 0; j < S; ++j) {
     sdst[j] = min(S * wave + j, kBlocks / 4 - 1);
-    ssrc[j] = block(4 * sdst[j] + (lane >> 4), scales, xscales, (int64_t)groups * 256) + 16 * (lane & 15);
+    ssrc[j] = block(4 * sdst[j] + (lane >> 4), scales, xscales, (int64_t)groups * 256) + (int64_t)(first >> 2) * 256 +
+              16 * (lane & 15);
   }
   auto issue = [&](int c, int slot, bool with_scales) {
 #pragma unroll
@@ -172,7 +184,7 @@ __global__ __launch_bounds__(64 * kWN * kWM) __attribute__((amdgpu_waves_per_eu(
   const std::integral_constant<int, 0> half0;
   const std::integral_constant<int, 1> half1;
 
-  const int last = tiles - 1;
+  const int last = count - 1;
 #pragma unroll
   for (int c = 0; c < kR; ++c)
     if (c <= last) issue(c, c, c == 0);
@@ -183,15 +195,16 @@ __global__ __launch_bounds__(64 * kWN * kWM) __attribute__((amdgpu_waves_per_eu(
   static_for<kAll>([&](auto r) { read_one(r, 0, half0, fa[0], fb[0], sa[0], sb[0]); });
 
   int slot = 0;
-  for (int c0 = 0; c0 < tiles; c0 += 8) {
+  for (int c0 = 0; c0 < steps; c0 += 8) {
     bool done = false;
     static_for<8>([&](auto tt) {
       constexpr int u = tt, t = u % 4, g = u / 4;  // step, its byte of the scales, buffer of their words
       const int c = c0 + u;
-      if (done || c >= tiles) {
+      if (done || c >= steps) {
         done = true;
         return;
       }
+      const bool mine = kKS == 1 || c < count;
       // Half a step: TN batches of TM matrix instructions, with the reads of the next half in front
       // of all but the last, whose time (and the barrier's) covers the last read's latency.
       auto half = [&](auto hh, auto reads, int rslot) {
@@ -209,7 +222,7 @@ __global__ __launch_bounds__(64 * kWN * kWM) __attribute__((amdgpu_waves_per_eu(
           __builtin_amdgcn_sched_barrier(0);
         });
       };
-      half(half0, std::integral_constant<int, kFrags>{}, slot);
+      if (mine) half(half0, std::integral_constant<int, kFrags>{}, slot);
       // stage c + 1 has landed where at most the loads of c + 2 .. c + kR - 1 are in flight, and stage
       // c has been read by every wave: its slot takes stage c + kR
       if (c + kR - 1 <= last)
@@ -219,7 +232,7 @@ __global__ __launch_bounds__(64 * kWN * kWM) __attribute__((amdgpu_waves_per_eu(
       const int next = slot + 1 == kR ? 0 : slot + 1;
       if (c + kR <= last) issue(c + kR, slot, (t + kR) % 4 == 0);
       // (the reads of the step after the last fetch what is in LDS, for nothing)
-      half(half1, std::integral_constant<int, t == 3 ? kAll : kFrags>{}, next);
+      if (mine) half(half1, std::integral_constant<int, t == 3 ? kAll : kFrags>{}, next);
       slot = next;
     });
   }
@@ -230,12 +243,46 @@ __global__ __launch_bounds__(64 * kWN * kWM) __attribute__((amdgpu_waves_per_eu(
   constexpr int kRow = 16 * kN * sizeof(TY) + (sizeof(TY) == 4 ? 16 : 8);  // bytes
   constexpr int kPer = 16 / sizeof(TY);                                    // outputs of a 16-byte piece
   constexpr int kPieces = 16 * kN / kPer;                                  // pieces of a row
-  static_assert(32 * kRow <= kR * kStage / W, "a slab fits the wave's share of the ring");
+  constexpr int kXchg = kKS == 1 ? 0 : 2 * W * TN * 4096;  // the two groups' exchanged tiles
+  static_assert(kXchg + kKS * W * 32 * kRow <= kKS * kGroupLds, "exchange and slabs fit the rings");
   const bool stream = whole_pieces(N);
   ring_wait<0>();  // the other waves have read their last fragments
-  uint8_t* slab = lds + wave * (kR * kStage / W);
+  if constexpr (kKS == 2) {  // group kg keeps token tile kg of each wave and sends the other
+    auto send = [&](auto jj) {
+      constexpr int j = jj;
+#pragma unroll
+      for (int i = 0; i < TN; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<v4f*>(lds_all + ((wave_all * TN + i) * 4 + q) * 1024 + 16 * lane) =
+              v4f{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+    };
+    auto add = [&](auto jj) {
+      constexpr int j = jj;
+      const int from = (1 - kg) * W + wave;
+#pragma unroll
+      for (int i = 0; i < TN; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const v4f v = *reinterpret_cast<const v4f*>(lds_all + ((from * TN + i) * 4 + q) * 1024 + 16 * lane);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] += v[e];
+        }
+    };
+    if (kg == 0)
+      send(half1);
+    else
+      send(half0);
+    ring_wait<0>();
+    if (kg == 0)
+      add(half0);
+    else
+      add(half1);
+  }
+  uint8_t* slab = lds_all + kXchg + wave_all * (32 * kRow);
 #pragma unroll
   for (int j = 0; j < TM; ++j) {
+    if (kKS == 2 && j != kg) continue;
 #pragma unroll
     for (int i = 0; i < TN; ++i) {
 #pragma unroll
@@ -286,17 +333,17 @@ __global__ __launch_bounds__(64 * kWN * kWM) __attribute__((amdgpu_waves_per_eu(
   }
 }
 
-template <int kN, int kM, int kR, typename TY>
+template <int kN, int kM, int kR, int kKS, typename TY>
 hipError_t launch(const MxGemmPlan& p, const uint8_t* codes, const uint8_t* scales, const uint8_t* xcodes,
                   const uint8_t* xscales, int64_t M, int64_t N, int64_t K, void* Y, hipStream_t s) {
-  constexpr int lds = (kWN * kN + kWM * kM) * (kR * 1024 + 256);
-  const auto fn = &k_mx_gemm<kN, kM, kR, TY>;
+  constexpr int lds = kKS * (kWN * kN + kWM * kM) * (kR * 1024 + 256);
+  const auto fn = &k_mx_gemm<kN, kM, kR, kKS, TY>;
   if (lds > 65536) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
   }
-  fn<<<dim3((unsigned)(p.tiles_m * p.tiles_n)), 64 * kWN * kWM, lds, s>>>(
+  fn<<<dim3((unsigned)(p.tiles_m * p.tiles_n)), 64 * kWN * kWM * kKS, lds, s>>>(
       codes, scales, xcodes, xscales, M, N, (int)mx_tiles(K), (int)mx_groups(K), (int)mx_row_blocks(N),
       (int)mx_row_blocks(M), (int)p.tiles_m, (int)p.tiles_n, (int)p.band, static_cast<TY*>(Y));
   return hipGetLastError();
@@ -314,6 +361,13 @@ MxGemmPlan plan_mx_gemm(int64_t M, int64_t N, int64_t K) {
   p.tiles_m = (M + p.tile_m - 1) / p.tile_m;
   p.tiles_n = (N + p.tile_n - 1) / p.tile_n;
   p.band = p.tiles_m * p.tiles_n > 512 ? 8 : p.tiles_m;
+  // Few tiles leave one workgroup to a compute unit, whose four waves then wait for each step's reads
+  // and barrier with nothing else to run (0.3 us a step, 0.11 of it the matrix instructions): two groups
+  // of waves halve the steps.  One group and two, us: 600 x 128 x 8192 23.6 and 19.6, 600 x 2560 x 6912
+  // 22.1 and 19.0, 1024 x 4096 x 4096 (256 tiles, 32 steps) 16.2 and 15.8.  Of more tiles two share a
+  // unit (600 x 6912 x 2560, 270 tiles, 15.3 and 19.9), and short sums do not pay for the exchange
+  // (1024^3, 8 steps, 6.3 and 7.0).
+  p.ks = p.tile_n == 128 && p.tiles_m * p.tiles_n <= 256 && mx_tiles(K) >= 16 ? 2 : 1;
   return p;
 }
 
@@ -323,8 +377,9 @@ hipError_t launch_mx_gemm(const uint8_t* codes, const uint8_t* scales, const uin
   const MxGemmPlan p = plan_mx_gemm(M, N, K);
   auto go = [&](auto yt) {
     using TY = decltype(yt);
-    if (p.tile_n == 256) return launch<8, 4, 3, TY>(p, codes, scales, xcodes, xscales, M, N, K, Y, s);
-    return launch<4, 4, 4, TY>(p, codes, scales, xcodes, xscales, M, N, K, Y, s);
+    if (p.tile_n == 256) return launch<8, 4, 3, 1, TY>(p, codes, scales, xcodes, xscales, M, N, K, Y, s);
+    if (p.ks == 2) return launch<4, 4, 4, 2, TY>(p, codes, scales, xcodes, xscales, M, N, K, Y, s);
+    return launch<4, 4, 4, 1, TY>(p, codes, scales, xcodes, xscales, M, N, K, Y, s);
   };
   return ybf16 ? go(uint16_t{}) : go(float{});
 }
