@@ -334,21 +334,27 @@ hipError_t launch_mx_few(const uint8_t* codes, const uint8_t* scales, const void
   }
 }
 
-// Estimates in microseconds, fitted to 22 shapes of 20 to 512 tokens measured both ways: the decode
-// kernel by its products of a weight tile with 16 tokens, the GEMM, while its 128 x 128 tiles fit the
-// chip at once, by its steps of 128 columns, both by the weights' bytes.  The rule takes the faster
-// path of all but one (128 x 6912 x 2560: 10.4 against 9.7 us).  Decode and GEMM in us: 64 x 8192 x
-// 8192 12.5 and 24.9, 128 x 8192 x 8192 22.9 and 24.1, 256 x 8192 x 8192 42.6 and 25.5, 256 x 2560 x
-// 6912 14.6 and 19.6, 40 x 28672 x 8192 39.7 and 31.3, 500 x 1000 x 8000 9.5 and 23.7.
+constexpr int64_t kMxDecodeTokens = 4096;  // the most that the rule below was measured with
+
+// Estimates in microseconds, fitted to 156 shapes of 20 to 1500 tokens measured both ways.  The decode
+// kernel goes by rounds of one workgroup to a compute unit and their products of a weight tile with 16
+// tokens, the GEMM by its rounds of two workgroups to a unit and their steps of 128 columns, both by the
+// weights' bytes.  The rule takes the slower path of two of them (200 x 8192 x 1024: 7.9 against 6.4 us,
+// 20 x 28672 x 8192: 31.5 and 28.3).  Decode and GEMM in us: 64 x 8192 x 8192 11.8 and 22.0, 128 x 8192 x
+// 8192 21.9 and 23.4, 256 x 8192 x 8192 40.0 and 24.0, 256 x 2560 x 6912 13.2 and 17.6, 512 x 2560 x 2560
+// 12.4 and 9.9, 1500 x 128 x 8192 10.4 and 19.5.
 bool mx_decode_wins(int64_t M, int64_t N, int64_t K) {
   if (M <= 16) return true;
-  if (M > 512) return false;
-  const MxDecodePlan p = plan_mx_decode(M, N, K);
-  const double tiles = (double)mx_row_blocks(N) * (double)mx_tiles(K), stream = tiles * 1088.0 / 5e6;
-  const int64_t rounds = (((M + 127) / 128) * ((N + 127) / 128) + 511) / 512;
-  const double stores = 1e-6 * (double)M * (double)N;  // the decode kernel's go out in pieces of 64 bytes
-  const double decode = std::max(3.5 + 6.5e-5 * tiles * (double)(p.gy * p.tg), 5.0 + stream) + stores;
-  const double gemm = std::max(5.0 + 0.3 * (double)(mx_tiles(K) * rounds), 6.0 + stream);
+  if (M > kMxDecodeTokens) return false;
+  const auto rounds = [](int64_t workgroups, int64_t at_once) { return (double)((workgroups + at_once - 1) / at_once); };
+  const double steps = (double)mx_tiles(K), stream = (double)mx_row_blocks(N) * steps * 1088.0 / 5e6;
+  const MxDecodePlan d = plan_mx_decode(M, N, K);
+  const double decode =
+      std::max(2.8 + rounds(d.gx * d.gy, 256) * (0.4 + 0.0144 * steps * (double)(d.rb * d.tg)), 5.0 + stream);
+  const MxGemmPlan g = plan_mx_gemm(M, N, K);
+  const double step = g.tile_n == 256 ? 0.84 : g.ks == 2 ? 0.24 : 0.27;
+  const double gemm = std::max(4.8 + step * steps * rounds(g.tiles_m * g.tiles_n, 512), 6.0 + stream) +
+                      0.55e-6 * (double)M * (double)N;
   return decode <= gemm;
 }
 

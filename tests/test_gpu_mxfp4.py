@@ -128,7 +128,8 @@ PRODUCTS = [(1, 16, 32), (1, 1, 1), (2, 17, 33), (1, 6912, 2560), (3, 100, 513),
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("m,n,k", PRODUCTS + [(520, 300, 640), (2100, 4000, 390), (513, 130, 129), (1000, 257, 2000)])
+@pytest.mark.parametrize("m,n,k", PRODUCTS + [(520, 300, 640), (2100, 4000, 390), (513, 130, 129), (1000, 257, 2000),
+                                              (1500, 600, 390), (1030, 2000, 1930), (4100, 130, 3000)])
 def test_forward(m, n, k, dtype):
     print(f"case: forward_mxfp4 M={m} N={n} K={k} {dtype}", flush=True)
     x, w = outliers(m, k, seed=m + 1, dtype=DT[dtype]), outliers(n, k, seed=n + 2) * 0.02
@@ -168,7 +169,7 @@ def test_forward_exact_sums(m, n, k):
     check_equal(host(bl.forward_mxfp4_fused(wc, ws, xb, n, k)).astype(np.float64), want, "fused bf16 y")
 
 
-@pytest.mark.parametrize("m", [1, 7, 16, 20, 64, 130, 520])
+@pytest.mark.parametrize("m", [1, 7, 16, 20, 64, 130, 520, 4100])
 def test_forward_block_scales(m):
     """One block per row pair at its own power of two: each output is one product of scales."""
     k, n = 640, 48
@@ -183,7 +184,7 @@ def test_forward_block_scales(m):
     check_equal(host(bl.forward_mxfp4_fused(wc, ws, x, n, k)).astype(np.float64), want, "y")
 
 
-@pytest.mark.parametrize("m", [1, 4, 16, 40, 100, 200, 520])
+@pytest.mark.parametrize("m", [1, 4, 16, 40, 100, 200, 520, 4100])
 def test_forward_nonfinite(m):
     """A NaN or an infinity spoils its token's row of the output, or its weight's column, and
     nothing else."""
@@ -276,7 +277,8 @@ def test_largest_k():
 def test_graph_replays_and_streams():
     """The products and the quantiser captured into a graph on a side stream, replayed with new
     inputs and eager work between, and two streams at once, against eager results."""
-    shapes = [(1, 300, 2560), (16, 128, 6912), (16, 64, 8704), (40, 500, 1000), (600, 600, 1500)]
+    shapes = [(1, 300, 2560), (16, 128, 6912), (16, 64, 8704), (40, 500, 1000), (600, 600, 1500), (700, 2500, 1000),
+              (1030, 2000, 1930)]
     w = [grid_matrix(n, k, i, shift=-3) for i, (m, n, k) in enumerate(shapes)]
     wq = [bl.quantize_mxfp4(t) for t in w]
     xs = [outliers(m, k, seed=i, dtype=torch.bfloat16) for i, (m, n, k) in enumerate(shapes)]

@@ -210,10 +210,11 @@ VARIANTS = [((1, 6912, 2560), ("lds", 16, 16), 1), ((16, 64, 8704), ("lds", 16, 
             ((16, 40, 28672), ("decode", 16, 16), 2), ((16, 4100, 28672), ("decode", 16, 32), 2),
             ((17, 64, 128), ("decode", 32, 16), 2), ((20, 4100, 1100), ("decode", 32, 32), 2),
             ((64, 2560, 2560), ("decode", 64, 16), 2), ((100, 4100, 1100), ("decode", 64, 32), 2),
-            ((520, 300, 640), ("gemm", 128, 128), 2), ((2100, 4000, 390), ("gemm", 128, 256), 2),
-            ((2050, 4100, 120), ("gemm", 128, 256), 2), ((600, 515, 1029), ("gemm", 128, 128), 2),
-            ((520, 300, 1930), ("gemm", 128, 128), 2), ((600, 515, 2049), ("gemm", 128, 128), 2),
-            ((1100, 2000, 4100), ("gemm", 128, 128), 2)]
+            ((520, 300, 640), ("decode", 64, 16), 2), ((600, 515, 2049), ("decode", 64, 32), 2),
+            ((2100, 4000, 390), ("gemm", 128, 256), 2), ((2050, 4100, 120), ("gemm", 128, 256), 2),
+            ((1030, 1500, 1000), ("gemm", 128, 128), 2), ((2060, 2030, 260), ("gemm", 128, 128), 2),
+            ((4100, 300, 640), ("gemm", 128, 128), 2), ((1030, 2000, 1930), ("gemm", 128, 128), 2),
+            ((4100, 260, 2177), ("gemm", 128, 128), 2), ((1100, 2000, 4100), ("gemm", 128, 128), 2)]
 
 
 @pytest.mark.parametrize("shape,want,launches", VARIANTS)
@@ -228,12 +229,13 @@ def test_plan(shape, want, launches):
     assert p["threads"] in range(64, 1025, 64)
 
 
-@pytest.mark.parametrize("shape,threads", [((520, 300, 640), 256), ((600, 515, 1920), 256), ((520, 300, 1930), 512),
-                                           ((600, 515, 2049), 512), ((1100, 2000, 4100), 512),
+@pytest.mark.parametrize("shape,threads", [((1030, 1500, 1000), 256), ((4100, 300, 640), 256), ((1030, 2000, 1930), 512),
+                                           ((4100, 260, 2177), 512), ((1100, 2000, 4100), 512),
                                            ((2100, 2000, 4100), 256), ((2100, 4000, 4100), 256)])
 def test_plan_column_groups(shape, threads):
-    """Few output tiles with long sums: twice the waves to a tile, each group with half of the columns."""
-    assert bl.forward_mxfp4_plan(*shape)["threads"] == threads
+    """The GEMM with few output tiles and long sums: twice the waves, each group with half of the columns."""
+    p = bl.forward_mxfp4_plan(*shape)
+    assert p["kernel"] == "gemm" and p["threads"] == threads
 
 
 def test_plan_refusals():
