@@ -188,7 +188,7 @@ int bitlinear_forward_mxfp4_plan(int64_t M, int64_t N, int64_t K, int xdt, int32
     out[0] = 8, out[1] = (int32_t)(p.gx * p.gy), out[2] = 64 * p.waves, out[3] = 16 * p.tg, out[4] = 16 * p.rb;
   } else {
     const bl::MxGemmPlan p = bl::plan_mx_gemm(M, N, K);
-    out[0] = 9, out[1] = (int32_t)(p.tiles_m * p.tiles_n), out[2] = 256 * p.ks;
+    out[0] = 9, out[1] = (int32_t)(p.tiles_m * p.tiles_n), out[2] = 256;
     out[3] = (int32_t)p.tile_m, out[4] = (int32_t)p.tile_n;
   }
   return BL_OK;

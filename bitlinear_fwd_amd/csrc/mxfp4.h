@@ -244,7 +244,6 @@ struct MxGemmPlan {
   int64_t tile_m = 256, tile_n = 256;
   int64_t tiles_m = 0, tiles_n = 0;
   int64_t band = 1;  // token tiles of a band of the tile order
-  int ks = 1;        // groups of waves, each with a part of the columns
 };
 MxGemmPlan plan_mx_gemm(int64_t M, int64_t N, int64_t K);
 hipError_t launch_mx_gemm(const uint8_t* codes, const uint8_t* scales, const uint8_t* xcodes,

@@ -336,25 +336,26 @@ hipError_t launch_mx_few(const uint8_t* codes, const uint8_t* scales, const void
 
 constexpr int64_t kMxDecodeTokens = 4096;  // the most that the rule below was measured with
 
-// Estimates in microseconds, fitted to 156 shapes of 20 to 1500 tokens measured both ways.  The decode
-// kernel goes by rounds of one workgroup to a compute unit and their products of a weight tile with 16
-// tokens, the GEMM by its rounds of two workgroups to a unit and their steps of 128 columns, both by the
-// weights' bytes.  The rule takes the slower path of two of them (200 x 8192 x 1024: 7.9 against 6.4 us,
-// 20 x 28672 x 8192: 31.5 and 28.3).  Decode and GEMM in us: 64 x 8192 x 8192 11.8 and 22.0, 128 x 8192 x
-// 8192 21.9 and 23.4, 256 x 8192 x 8192 40.0 and 24.0, 256 x 2560 x 6912 13.2 and 17.6, 512 x 2560 x 2560
-// 12.4 and 9.9, 1500 x 128 x 8192 10.4 and 19.5.
+// Estimates in microseconds, fitted to 116 shapes of 130 to 4096 tokens measured both ways (and checked
+// on 50 of 20 to 128, where the decode kernel is the faster).  The decode kernel goes by rounds of one
+// workgroup to a compute unit and their products of a weight tile with 16 tokens; the GEMM by its steps
+// of 128 columns, of one or two narrow tiles to a unit or of rounds of two wide ones; both by the
+// weights' bytes.  The slower path is taken by at most 7 % (1000 x 640 x 2560: 8.9 against 8.6 us), but
+// for 20 x 28672 x 8192, 31.5 and 28.3.  Decode and GEMM in us: 64 x 8192 x 8192 11.8 and 22.0, 256 x 8192
+// x 8192 39.8 and 24.4, 256 x 2560 x 6912 13.1 and 15.6, 512 x 2560 x 2560 12.3 and 8.5, 1500 x 128 x 8192
+// 10.5 and 17.1.
 bool mx_decode_wins(int64_t M, int64_t N, int64_t K) {
   if (M <= 16) return true;
   if (M > kMxDecodeTokens) return false;
-  const auto rounds = [](int64_t workgroups, int64_t at_once) { return (double)((workgroups + at_once - 1) / at_once); };
+  const auto rounds = [](int64_t groups, int64_t at_once) { return (double)((groups + at_once - 1) / at_once); };
   const double steps = (double)mx_tiles(K), stream = (double)mx_row_blocks(N) * steps * 1088.0 / 5e6;
   const MxDecodePlan d = plan_mx_decode(M, N, K);
   const double decode =
-      std::max(2.8 + rounds(d.gx * d.gy, 256) * (0.4 + 0.0144 * steps * (double)(d.rb * d.tg)), 5.0 + stream);
+      std::max(2.8 + rounds(d.gx * d.gy, 256) * (0.4 + 0.0139 * steps * (double)(d.rb * d.tg)), 5.0 + stream);
   const MxGemmPlan g = plan_mx_gemm(M, N, K);
-  const double step = g.tile_n == 256 ? 0.84 : g.ks == 2 ? 0.24 : 0.27;
-  const double gemm = std::max(4.8 + step * steps * rounds(g.tiles_m * g.tiles_n, 512), 6.0 + stream) +
-                      0.55e-6 * (double)M * (double)N;
+  const int64_t tiles = g.tiles_m * g.tiles_n;
+  const double step = g.tile_n == 256 ? 0.8 * rounds(tiles, 512) : tiles <= 256 ? 0.22 : 0.36;
+  const double gemm = std::max(4.8 + step * steps, 5.0 + stream) + 0.45e-6 * (double)M * (double)N;
   return decode <= gemm;
 }
 

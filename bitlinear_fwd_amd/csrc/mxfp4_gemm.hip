@@ -2,35 +2,39 @@
 // scales in the layout of mxfp4.h, on the scaled matrix instructions (32x32x64, 4-bit operands).
 //
 // At 4 bits the matrix cores outrun the operands: a 32x32x64 step takes 32 cycles and eats 2 KiB, so
-// what decides is how often a loaded byte is used and what else runs meanwhile.  Output tiles of 128
-// tokens x 256 outputs by four waves of 64 x 128 (or 64 x 64, for 128 x 128, where the large tiles
-// would leave compute units idle), sized so that two workgroups share a compute unit: one's first
-// loads and output stores run under the other's matrix instructions.  Measured: tiles of 256 x 256
-// with one workgroup to a unit use each byte more often, but load, compute and store in turn (2048 x
-// 28672 x 8192 to bf16 with the quantiser 273 us, against 250; 8192^3 to bf16 283 us against 270,
-// 4.08 PFLOP/s).  What bounds the large shapes now: with all-zero operands a 256 x 256 x 128 step of a
-// compute unit took 0.71 us, with random ones 0.92 - 1.0 (0.43 at the nominal clock): power, then LDS
-// (1150 of its cycles to 1024 of the matrix cores').  2048 x 6912 x 2560 to fp32, 27.2 us: 216 tiles of
-// 256 x 256 worth of work on 256 compute units, and 57 MB of output.  Output rows are stored past the
-// caches: 26.4 us against 30.3 there.
+// what decides is how often a loaded byte is used, which way it takes, and what else runs meanwhile.
+// Output tiles of 128 tokens x 256 outputs (or 128, where the large tiles would leave compute units
+// idle) by four waves, each with all tokens and a quarter of the outputs; two or three workgroups share
+// a compute unit, and one's first loads and output stores run under the other's matrix instructions.
+// Per step of 128 columns of two wide tiles a compute unit spends 1024 cycles on matrix instructions,
+// 820 on loads (60 bytes a cycle, to LDS or to registers) and 770 on LDS (the tokens' 64 bytes a cycle
+// in, 128 out).  Measured before: both matrices through LDS, waves of 64 tokens x 128 outputs, which is
+// 1540 cycles of LDS: 2048 x 6912 x 2560 to fp32 27.4 us, 24.9 so; 1024 x 4096 x 4096 16.1 and 13.3;
+// 8192^3 to bf16 262 and 249, 4.42 PFLOP/s; and tiles of 256 x 256 with one workgroup to a unit (load,
+// compute and store in turn) 283.  What bounds the large shapes now is power: with all-zero operands
+// 8192^3 takes 163 us.  2048 x 6912 x 2560, 24.9 us: 432 tiles on 512 places, 57 MB of output; zeros 20.5.
 //   * 32x32x64 instructions: with the 16x16x128 form the waves cannot issue fast enough (5.4 against
-//     9.6 PFLOP/s from registers, one wave per SIMD).  On random data power holds both back.
-//   * The tile layout is the operand layout, so a 1 KiB tile goes from global memory straight into
-//     LDS (direct loads, no registers) and a fragment is one conflict-free 16-byte LDS read per
-//     lane.  Words of scales take the same way, once per four steps.
-//   * Ring of three or four 128-column stages, worked on by halves of 64 columns: a half's matrix
-//     instructions run on fragments already in registers, with the reads of the next half's spread
-//     between them (in one go they fill the LDS queue, and the waves wait for one another).  In the
-//     middle of a step the workgroup waits until the next stage has landed; by then every wave has
-//     read the whole of this one, and the loads of the stage after the ring go into its slot.
+//     9.6 PFLOP/s from registers, one wave per SIMD).
+//   * The tile layout is the operand layout.  A wave loads its own weights' fragments straight from
+//     global memory into registers, four steps ahead (with two, 512 x 8192 x 8192 took 40.8 us, not
+//     26.2).  The tokens' tiles, which all four waves need, go from global memory straight into LDS
+//     (direct loads, no registers), and a fragment is one conflict-free 16-byte LDS read per lane.
+//     Words of scales take that way too, once per four steps.
+//   * Ring of four 128-column stages, worked on by halves of 64 columns: a half's matrix instructions
+//     run on fragments already in registers, with the reads of the next half's spread between them.  In
+//     the middle of a step the workgroup waits until the next stage has landed; by then every wave has
+//     read the whole of this one, and the loads of the stage after the ring go into its slot.  A step
+//     has no branches: around a conditional load or wait the compiler moves the matrix instructions of
+//     the first half behind the barrier.
 //   * The direct loads are written in inline assembly (they have no output registers): for the
 //     builtin the compiler would wait for every load in flight before any LDS read, as it cannot
-//     tell which slot a load writes.  All ordering of loads against reads is by ring_wait below,
+//     tell which slot a load writes.  All ordering of those loads against reads is by ring_wait below,
 //     whose memory clobber keeps LDS reads on their side of it.
 //   * Tile order: consecutive workgroups go to different XCDs, so each XCD gets a contiguous run of
 //     tiles.  Where they do not all run at once, the run goes down bands of eight token tiles, so that
 //     the 64 tiles at work on an XCD share eight tiles of each matrix rather than read all tokens
 //     (8192^3 to bf16 271 us with tokens fastest, 263 so; 2048 x 8192 x 8192 71.8 and 69.0).
+//   * Output rows are stored past the caches (2048 x 6912 x 2560 30.3 us without, 26.4 so).
 #include "mxfp4.h"
 
 #include <algorithm>
@@ -78,36 +82,30 @@ __device__ __forceinline__ T* uniform_ptr(T* p) {
               (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
 }
 
-constexpr int kWN = 2, kWM = 2;  // waves of a workgroup along the outputs and along the tokens
+constexpr int kWaves = 4;  // of a workgroup: each has all tokens of the tile and a quarter of its outputs
+constexpr int TM = 4;      // tiles of 32 tokens
+constexpr int kR = 4;      // stages of 128 columns of the tokens in the ring
+constexpr int kRW = 4;     // stages of a wave's weights in its registers
 
-// Each wave has kN x kM blocks of 16 weight rows and 16 tokens: output tiles of 16 kWM kM tokens x 16
-// kWN kN outputs.  kR stages of 128 columns in the ring.  kKS 2: two groups of such waves, each with a
-// ring of its own, take half of the columns each (in whole groups of four stages, the first group's no
-// fewer) and add their sums through LDS; both go through the same number of barriers.
-template <int kN, int kM, int kR, int kKS, typename TY>
-__global__ __launch_bounds__(64 * kWN * kWM * kKS) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_mx_gemm(
+// Each wave has TN x TM tiles of 32 weight rows and 32 tokens: output tiles of 128 tokens x 128 TN
+// outputs.
+template <int TN, typename TY>
+__global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_mx_gemm(
     const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, const uint8_t* __restrict__ xcodes,
     const uint8_t* __restrict__ xscales, int64_t M, int64_t N, int tiles, int groups, int nblocks, int xblocks,
     int tiles_m, int tiles_n, int band, TY* __restrict__ Y) {
-  constexpr int W = kWN * kWM;
-  constexpr int BN = kWN * kN, BM = kWM * kM;     // row blocks of a stage: weights, then tokens
+  constexpr int W = kWaves;
+  constexpr int BN = 2 * TN * W, BM = 2 * TM;     // row blocks of a stage: weights, then tokens
   constexpr int kBlocks = BN + BM;
-  constexpr int kStage = kBlocks * 1024;          // bytes
-  constexpr int L = kBlocks / W;                  // direct loads per wave and stage
+  constexpr int kStage = BM * 1024;               // bytes: the tokens' tiles
+  constexpr int L = BM / W;                       // direct loads per wave and stage
   constexpr int S = (kBlocks / 4 + W - 1) / W;    // and per wave and four stages, of scales
-  constexpr int TN = kN / 2, TM = kM / 2;         // 32-row tiles of a wave
-  constexpr int kGroupLds = kR * kStage + kBlocks * 256;  // a ring and its scales
-  static_assert(L % 2 == 0, "direct loads come in pairs");
-  static_assert(kKS == 1 || (kKS == 2 && TM == 2), "the two groups keep one of two token tiles each");
-  extern __shared__ uint8_t lds_all[];            // per group a ring, then kBlocks x 256 bytes of scales
-  const int lane = threadIdx.x & 63, wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int kg = wave_all / W, wave = wave_all % W;
-  const int wn = wave % kWN, wm = wave / kWN;
-  uint8_t* lds = lds_all + kg * kGroupLds;
+  static_assert(L == 2, "direct loads come in pairs");
+  static_assert(kR == 4 && kRW == 4, "the loop is unrolled by four stages");
+  extern __shared__ uint8_t lds[];                // the ring, then kBlocks x 256 bytes of scales
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t lds0 = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)lds;
-  // this group's stages: `count` from stage `first`; `steps` for both
-  const int steps = kKS == 1 ? tiles : min(tiles, (tiles + 7) / 8 * 4);
-  const int first = kg * steps, count = kg == 0 ? steps : tiles - first;
+  const int last = tiles - 1;
 
   // tile of this workgroup: contiguous runs per XCD
   int id = blockIdx.x;
@@ -124,32 +122,43 @@ __global__ __launch_bounds__(64 * kWN * kWM * kKS) __attribute__((amdgpu_waves_p
   auto block = [&](int t, const uint8_t* w, const uint8_t* x, int64_t bytes) {
     return t < BN ? w + min(tn * BN + t, nblocks - 1) * bytes : x + min(tm * BM + t - BN, xblocks - 1) * bytes;
   };
-  // this wave's direct loads: blocks L wave .. of the stage, and of the scales KiB S wave .. (four
-  // blocks each; waves past the last repeat it, so that all have the same number in flight)
-  const uint8_t* src[L];
+  const int64_t row_bytes = (int64_t)tiles * kMxTileBytes;
+  // this wave's direct loads: two of the tokens' blocks, and of the scales KiB S wave .. (four blocks
+  // each; waves past the last repeat it, so that all have the same number in flight)
+  const uint8_t* src[2];
 #pragma unroll
-  for (int j = 0; j < L; ++j)
-    src[j] = uniform_ptr(block(L * wave + j, codes, xcodes, (int64_t)tiles * kMxTileBytes) +
-                         (int64_t)first * kMxTileBytes);
+  for (int j = 0; j < 2; ++j) src[j] = uniform_ptr(block(BN + 2 * wave + j, codes, xcodes, row_bytes));
   const uint8_t* ssrc[S];
   int sdst[S];
 #pragma unroll
   for (int j = 0; j < S; ++j) {
     sdst[j] = min(S * wave + j, kBlocks / 4 - 1);
-    ssrc[j] = block(4 * sdst[j] + (lane >> 4), scales, xscales, (int64_t)groups * 256) + (int64_t)(first >> 2) * 256 +
-              16 * (lane & 15);
+    ssrc[j] = block(4 * sdst[j] + (lane >> 4), scales, xscales, (int64_t)groups * 256) + 16 * (lane & 15);
   }
-  auto issue = [&](int c, int slot, bool with_scales) {
-#pragma unroll
-    for (int j = 0; j < L; j += 2)
-      load2_lds(src[j] + (int64_t)c * kMxTileBytes, src[j + 1] + (int64_t)c * kMxTileBytes, 16 * lane,
-                lds0 + slot * kStage + (L * wave + j) * 1024);
+  // (stages past the last: the last again, so that the same number is in flight at every step)
+  auto issue = [&](int stage, int slot, bool with_scales) {
+    const int c = min(stage, last);
+    load2_lds(src[0] + (int64_t)c * kMxTileBytes, src[1] + (int64_t)c * kMxTileBytes, 16 * lane,
+              lds0 + slot * kStage + 2 * wave * 1024);
     if (with_scales) {
 #pragma unroll
       for (int j = 0; j < S; ++j)
         load1_lds(ssrc[j] + (int64_t)(c >> 2) * 256, lds0 + kR * kStage + sdst[j] * 1024);
     }
   };
+  // this wave's weights: tile i's rows, lane's 16 bytes of a half stage
+  const int half_lane = 16 * (16 * (lane >> 5) + (lane & 15));
+  const int wb0 = min(tn * BN + 2 * TN * wave, nblocks - 1);
+  uint32_t woff[TN];
+#pragma unroll
+  for (int i = 0; i < TN; ++i)
+    woff[i] = (uint32_t)((min(tn * BN + 2 * TN * wave + 2 * i + ((lane >> 4) & 1), nblocks - 1) - wb0) * row_bytes) +
+              half_lane;
+  using GlobalBytes = const __attribute__((address_space(1))) uint8_t*;
+  GlobalBytes wsrc = (GlobalBytes)uniform_ptr(codes + wb0 * row_bytes);
+  // From here on the compiler may not assume that nothing writes what wsrc points to, so that its loads
+  // stay between the same two of the assembly statements, whose waits count them.
+  asm volatile("" : "+s"(wsrc));
 
   v16f acc[TN][TM];
 #pragma unroll
@@ -158,131 +167,102 @@ __global__ __launch_bounds__(64 * kWN * kWM * kKS) __attribute__((amdgpu_waves_p
     for (int j = 0; j < TM; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-  // fragments of 32 rows x 64 columns (two blocks' rows, half h of their columns) of this half step
-  // and of the next, and the words of scales of this group of four steps and of the next
-  v4i fa[2][TN], fb[2][TM];
-  int sa[2][2][TN], sb[2][2][TM];
-  const uint8_t* lane_codes = lds + ((lane >> 4) & 1) * 1024 + 16 * (16 * (lane >> 5) + (lane & 15));
-  const uint8_t* lane_scales = lds + kR * kStage + ((lane >> 4) & 1) * 256 + 4 * (16 * (lane >> 5) + (lane & 15));
-  // the reads of a half step, one at a time so that they can be spread over its matrix
-  // instructions: TN + TM fragments of half h, and with scales the words of both halves
-  auto read_one = [&](auto rr, int slot, auto hh, v4i (&a)[TN], v4i (&b)[TM], int (&wa)[2][TN], int (&wb)[2][TM]) {
-    constexpr int r = rr, h = hh;
-    if constexpr (r < TN)
-      a[r] = *reinterpret_cast<const v4i*>(lane_codes + slot * kStage + (kN * wn + 2 * r) * 1024 + 512 * h);
-    else if constexpr (r < TN + TM)
-      b[r - TN] =
-          *reinterpret_cast<const v4i*>(lane_codes + slot * kStage + (BN + kM * wm + 2 * (r - TN)) * 1024 + 512 * h);
-    else if constexpr (r < 3 * TN + TM)
-      wa[(r - TN - TM) / TN][(r - TN - TM) % TN] = *reinterpret_cast<const int*>(
-          lane_scales + (kN * wn + 2 * ((r - TN - TM) % TN)) * 256 + 128 * ((r - TN - TM) / TN));
-    else
-      wb[(r - 3 * TN - TM) / TM][(r - 3 * TN - TM) % TM] = *reinterpret_cast<const int*>(
-          lane_scales + (BN + kM * wm + 2 * ((r - 3 * TN - TM) % TM)) * 256 + 128 * ((r - 3 * TN - TM) / TM));
+  // fragments of 32 rows x 64 columns (two blocks' rows, half h of their columns): of the weights for
+  // kRW stages, of the tokens for this half step and the next; and the words of scales of this group of
+  // four steps
+  v4i fa[kRW][2][TN], fb[2][TM];
+  int sa[2][TN], sb[2][TM];
+  auto load_w = [&](int c, int h, v4i (&w)[TN]) {
+    const GlobalBytes p = wsrc + (int64_t)min(c, last) * kMxTileBytes + 512 * h;
+#pragma unroll
+    for (int i = 0; i < TN; ++i) w[i] = *reinterpret_cast<const __attribute__((address_space(1))) v4i*>(p + woff[i]);
   };
-  constexpr int kFrags = TN + TM, kAll = 3 * kFrags;
+  const uint8_t* lane_codes = lds + ((lane >> 4) & 1) * 1024 + half_lane;
+  const uint8_t* lane_scales = lds + kR * kStage + ((lane >> 4) & 1) * 256 + half_lane / 4;
+  // the reads of a half step, one at a time so that they can be spread over matrix instructions: TM
+  // fragments of half h of a slot, and the words of scales of half sh
+  auto read_one = [&](auto rr, int slot, auto hh, auto ss, v4i (&bf)[TM]) {
+    constexpr int r = rr, h = hh, sh = ss;
+    if constexpr (r < TM)
+      bf[r] = *reinterpret_cast<const v4i*>(lane_codes + slot * kStage + 2 * r * 1024 + 512 * h);
+    else if constexpr (r < TM + TN)
+      sa[sh][r - TM] =
+          *reinterpret_cast<const int*>(lane_scales + (2 * TN * wave + 2 * (r - TM)) * 256 + 128 * sh);
+    else
+      sb[sh][r - TM - TN] = *reinterpret_cast<const int*>(lane_scales + (BN + 2 * (r - TM - TN)) * 256 + 128 * sh);
+  };
+  constexpr int kAll = 2 * TM + TN;
   const std::integral_constant<int, 0> half0;
   const std::integral_constant<int, 1> half1;
 
-  const int last = count - 1;
 #pragma unroll
-  for (int c = 0; c < kR; ++c)
-    if (c <= last) issue(c, c, c == 0);
-  if (last >= kR - 1)
-    ring_wait<(kR - 1) * L>();
-  else
-    ring_wait<0>();
-  static_for<kAll>([&](auto r) { read_one(r, 0, half0, fa[0], fb[0], sa[0], sb[0]); });
+  for (int c = 0; c < kR; ++c) issue(c, c, c == 0);
+#pragma unroll
+  for (int c = 0; c < kRW; ++c) {
+    load_w(c, 0, fa[c][0]);
+    load_w(c, 1, fa[c][1]);
+  }
+  ring_wait<2 * TN * kRW>();
+  static_for<kAll>([&](auto r) { read_one(r, 0, half0, half0, fb[0]); });
 
-  int slot = 0;
-  for (int c0 = 0; c0 < steps; c0 += 8) {
-    bool done = false;
-    static_for<8>([&](auto tt) {
-      constexpr int u = tt, t = u % 4, g = u / 4;  // step, its byte of the scales, buffer of their words
-      const int c = c0 + u;
-      if (done || c >= steps) {
-        done = true;
-        return;
-      }
-      const bool mine = kKS == 1 || c < count;
-      // Half a step: TN batches of TM matrix instructions, with the reads of the next half in front
-      // of all but the last, whose time (and the barrier's) covers the last read's latency.
-      auto half = [&](auto hh, auto reads, int rslot) {
-        constexpr int h = hh, kReads = decltype(reads)::value, kBatch = (kReads + TN - 2) / (TN - 1);
-        static_for<TN>([&](auto bb) {
-          constexpr int i = bb;
-          static_for<kBatch>([&](auto rr) {
-            if constexpr (i * kBatch + rr < kReads)
-              read_one(std::integral_constant<int, i * kBatch + rr>{}, rslot, std::integral_constant<int, 1 - h>{},
-                       fa[1 - h], fb[1 - h], sa[1 - g], sb[1 - g]);
-          });
-#pragma unroll
-          for (int j = 0; j < TM; ++j)
-            acc[i][j] = mx_mfma32<t, t>(fa[h][i], fb[h][j], acc[i][j], sa[g][h][i], sb[g][h][j]);
-          __builtin_amdgcn_sched_barrier(0);
+  auto step = [&](auto tt, int c, auto in_loop) {
+    constexpr int t = tt;  // the step's byte of the scales and its slots
+    // Half a step: TN x TM matrix instructions on what is in registers, between them the reads of the
+    // next half.  The words of scales of half h of four steps are read in the half before their first
+    // use, after the last use of those before.
+    auto half = [&](auto hh, auto reads, int rslot) {
+      constexpr int h = hh, kReads = decltype(reads)::value, kInst = TN * TM;
+      static_for<kInst>([&](auto mm) {
+        constexpr int m = mm, i = m / TM, j = m % TM;
+        static_for<kReads>([&](auto rr) {
+          if constexpr (decltype(rr)::value * (kInst - 1) / kReads == m)
+            read_one(rr, rslot, std::integral_constant<int, 1 - h>{}, std::integral_constant<int, 1 - h>{},
+                     fb[1 - h]);
         });
-      };
-      if (mine) half(half0, std::integral_constant<int, kFrags>{}, slot);
-      // stage c + 1 has landed where at most the loads of c + 2 .. c + kR - 1 are in flight, and stage
-      // c has been read by every wave: its slot takes stage c + kR
-      if (c + kR - 1 <= last)
-        ring_wait<(kR - 2) * L + ((t == 2 || (kR == 4 && t == 1)) ? S : 0)>();
-      else
-        ring_wait<0>();
-      const int next = slot + 1 == kR ? 0 : slot + 1;
-      if (c + kR <= last) issue(c + kR, slot, (t + kR) % 4 == 0);
-      // (the reads of the step after the last fetch what is in LDS, for nothing)
-      if (mine) half(half1, std::integral_constant<int, t == 3 ? kAll : kFrags>{}, next);
-      slot = next;
-    });
+        acc[i][j] = mx_mfma32<t, t>(fa[t][h][i], fb[h][j], acc[i][j], sa[h][i], sb[h][j]);
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    };
+    half(half0, std::integral_constant<int, t == 0 ? kAll : TM>{}, t);
+    // Stage c + 1 has landed where at most the loads of weights of three steps and the direct loads of
+    // two are in flight, and stage c has been read by every wave: its slot takes stage c + kR.
+    ring_wait<in_loop ? 3 * 2 * TN + 2 * L + (t == 1 || t == 2 ? S : 0) : 2 * L>();
+    issue(c + kR, t, t == 0);
+    load_w(c + kRW, 0, fa[t][0]);
+    __builtin_amdgcn_sched_barrier(0);
+    // (the reads of the step after the last fetch what is in LDS, for nothing)
+    half(half1, std::integral_constant<int, t == 3 ? kAll : TM>{}, (t + 1) % kR);
+    load_w(c + kRW, 1, fa[t][1]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  const std::integral_constant<int, 2> third;
+  const std::integral_constant<int, 3> fourth;
+  int c = 0;
+  for (; c + 4 <= tiles; c += 4) {
+    step(half0, c, std::true_type{});
+    step(half1, c + 1, std::true_type{});
+    step(third, c + 2, std::true_type{});
+    step(fourth, c + 3, std::true_type{});
+  }
+  if (c < tiles) {
+    step(half0, c, std::false_type{});
+    if (c + 1 < tiles) {
+      step(half1, c + 1, std::false_type{});
+      if (c + 2 < tiles) step(third, c + 2, std::false_type{});
+    }
   }
 
   // Each wave turns its accumulators (lane l of a 32 x 32 tile: token l % 32, four times four
   // consecutive outputs) into whole rows through its share of the ring, 32 tokens at a time.  The
   // row stride puts the 32 tokens of a write on different banks.
-  constexpr int kRow = 16 * kN * sizeof(TY) + (sizeof(TY) == 4 ? 16 : 8);  // bytes
+  constexpr int kRow = 32 * TN * sizeof(TY) + (sizeof(TY) == 4 ? 16 : 8);  // bytes
   constexpr int kPer = 16 / sizeof(TY);                                    // outputs of a 16-byte piece
-  constexpr int kPieces = 16 * kN / kPer;                                  // pieces of a row
-  constexpr int kXchg = kKS == 1 ? 0 : 2 * W * TN * 4096;  // the two groups' exchanged tiles
-  static_assert(kXchg + kKS * W * 32 * kRow <= kKS * kGroupLds, "exchange and slabs fit the rings");
+  constexpr int kPieces = 32 * TN / kPer;                                  // pieces of a row
   const bool stream = whole_pieces(N);
-  ring_wait<0>();  // the other waves have read their last fragments
-  if constexpr (kKS == 2) {  // group kg keeps token tile kg of each wave and sends the other
-    auto send = [&](auto jj) {
-      constexpr int j = jj;
-#pragma unroll
-      for (int i = 0; i < TN; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<v4f*>(lds_all + ((wave_all * TN + i) * 4 + q) * 1024 + 16 * lane) =
-              v4f{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-    };
-    auto add = [&](auto jj) {
-      constexpr int j = jj;
-      const int from = (1 - kg) * W + wave;
-#pragma unroll
-      for (int i = 0; i < TN; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const v4f v = *reinterpret_cast<const v4f*>(lds_all + ((from * TN + i) * 4 + q) * 1024 + 16 * lane);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] += v[e];
-        }
-    };
-    if (kg == 0)
-      send(half1);
-    else
-      send(half0);
-    ring_wait<0>();
-    if (kg == 0)
-      add(half0);
-    else
-      add(half1);
-  }
-  uint8_t* slab = lds_all + kXchg + wave_all * (32 * kRow);
+  ring_wait<0>();  // no load is in flight, and the other waves have read their last fragments
+  uint8_t* slab = lds + wave * (32 * kRow);
 #pragma unroll
   for (int j = 0; j < TM; ++j) {
-    if (kKS == 2 && j != kg) continue;
 #pragma unroll
     for (int i = 0; i < TN; ++i) {
 #pragma unroll
@@ -300,9 +280,9 @@ __global__ __launch_bounds__(64 * kWN * kWM * kKS) __attribute__((amdgpu_waves_p
       }
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // a wave's own writes, read by its other lanes
-    const int64_t m0 = ((int64_t)tm * BM + kM * wm + 2 * j) * 16;
-    const int64_t n0 = ((int64_t)tn * BN + kN * wn) * 16;
-    if (stream && m0 + 32 <= M && n0 + 16 * kN <= N) {  // a whole slab, past the caches
+    const int64_t m0 = ((int64_t)tm * BM + 2 * j) * 16;
+    const int64_t n0 = ((int64_t)tn * BN + 2 * TN * wave) * 16;
+    if (stream && m0 + 32 <= M && n0 + 32 * TN <= N) {  // a whole slab, past the caches
 #pragma unroll 8
       for (int t = 0; t < 32 * kPieces / 64; ++t) {
         const int piece = 64 * t + lane, r = piece / kPieces, c = piece % kPieces;
@@ -333,17 +313,15 @@ __global__ __launch_bounds__(64 * kWN * kWM * kKS) __attribute__((amdgpu_waves_p
   }
 }
 
-template <int kN, int kM, int kR, int kKS, typename TY>
+template <int TN, typename TY>
 hipError_t launch(const MxGemmPlan& p, const uint8_t* codes, const uint8_t* scales, const uint8_t* xcodes,
                   const uint8_t* xscales, int64_t M, int64_t N, int64_t K, void* Y, hipStream_t s) {
-  constexpr int lds = kKS * (kWN * kN + kWM * kM) * (kR * 1024 + 256);
-  const auto fn = &k_mx_gemm<kN, kM, kR, kKS, TY>;
-  if (lds > 65536) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-    if (e != hipSuccess) return e;
-  }
-  fn<<<dim3((unsigned)(p.tiles_m * p.tiles_n)), 64 * kWN * kWM * kKS, lds, s>>>(
+  // the ring with its scales, then a slab of 32 rows per wave
+  constexpr int ring = kR * 2 * TM * 1024 + (2 * TN * kWaves + 2 * TM) * 256;
+  constexpr int slab = 32 * (32 * TN * (int)sizeof(TY) + (sizeof(TY) == 4 ? 16 : 8));
+  constexpr int lds = std::max(ring, kWaves * slab);
+  static_assert(lds <= 65536, "no attribute needed");
+  k_mx_gemm<TN, TY><<<dim3((unsigned)(p.tiles_m * p.tiles_n)), 64 * kWaves, lds, s>>>(
       codes, scales, xcodes, xscales, M, N, (int)mx_tiles(K), (int)mx_groups(K), (int)mx_row_blocks(N),
       (int)mx_row_blocks(M), (int)p.tiles_m, (int)p.tiles_n, (int)p.band, static_cast<TY*>(Y));
   return hipGetLastError();
@@ -353,21 +331,16 @@ hipError_t launch(const MxGemmPlan& p, const uint8_t* codes, const uint8_t* scal
 
 MxGemmPlan plan_mx_gemm(int64_t M, int64_t N, int64_t K) {
   MxGemmPlan p;
-  auto tiles = [&](int64_t tm, int64_t tn) { return ((M + tm - 1) / tm) * ((N + tn - 1) / tn); };
-  // 2048 x 6912 x 2560: 30.1 us with 256 x 128 tiles, 34.4 with 128 x 128; 512 x 8192 x 8192, where the
-  // large tiles are 128 on 256 compute units: 37.7 and 27.8
+  // A tile of 256 outputs uses its tokens' tiles more often, two of them or three of 128 share a compute
+  // unit.  128 and 256 wide, us: 512 x 8192 x 8192 (256 tiles of 128) 26.2 and 33.0, 1024 x 6912 x 2560
+  // (432) 14.3 and 15.7, 1024 x 8192 x 8192 (512) 45.9 and 38.4, 700 x 8192 x 8192 (384) 41.4 and 34.3,
+  // 2048 x 6912 x 2560 (864) 27.6 and 25.0.
+  const int64_t t128 = ((M + 127) / 128) * ((N + 127) / 128);
   p.tile_m = 128;
-  p.tile_n = tiles(128, 256) >= 256 ? 256 : 128;
+  p.tile_n = t128 > 512 || (t128 > 256 && mx_tiles(K) >= 48) ? 256 : 128;
   p.tiles_m = (M + p.tile_m - 1) / p.tile_m;
   p.tiles_n = (N + p.tile_n - 1) / p.tile_n;
   p.band = p.tiles_m * p.tiles_n > 512 ? 8 : p.tiles_m;
-  // Few tiles leave one workgroup to a compute unit, whose four waves then wait for each step's reads
-  // and barrier with nothing else to run (0.3 us a step, 0.11 of it the matrix instructions): two groups
-  // of waves halve the steps.  One group and two, us: 600 x 128 x 8192 23.6 and 19.6, 600 x 2560 x 6912
-  // 22.1 and 19.0, 1024 x 4096 x 4096 (256 tiles, 32 steps) 16.2 and 15.8.  Of more tiles two share a
-  // unit (600 x 6912 x 2560, 270 tiles, 15.3 and 19.9), and short sums do not pay for the exchange
-  // (1024^3, 8 steps, 6.3 and 7.0).
-  p.ks = p.tile_n == 128 && p.tiles_m * p.tiles_n <= 256 && mx_tiles(K) >= 16 ? 2 : 1;
   return p;
 }
 
@@ -377,9 +350,8 @@ hipError_t launch_mx_gemm(const uint8_t* codes, const uint8_t* scales, const uin
   const MxGemmPlan p = plan_mx_gemm(M, N, K);
   auto go = [&](auto yt) {
     using TY = decltype(yt);
-    if (p.tile_n == 256) return launch<8, 4, 3, 1, TY>(p, codes, scales, xcodes, xscales, M, N, K, Y, s);
-    if (p.ks == 2) return launch<4, 4, 4, 2, TY>(p, codes, scales, xcodes, xscales, M, N, K, Y, s);
-    return launch<4, 4, 4, 1, TY>(p, codes, scales, xcodes, xscales, M, N, K, Y, s);
+    return p.tile_n == 256 ? launch<2, TY>(p, codes, scales, xcodes, xscales, M, N, K, Y, s)
+                           : launch<1, TY>(p, codes, scales, xcodes, xscales, M, N, K, Y, s);
   };
   return ybf16 ? go(uint16_t{}) : go(float{});
 }

@@ -169,6 +169,21 @@ def test_forward_exact_sums(m, n, k):
     check_equal(host(bl.forward_mxfp4_fused(wc, ws, xb, n, k)).astype(np.float64), want, "fused bf16 y")
 
 
+@pytest.mark.parametrize("n,outputs", [(260, 128), (2300, 256)])
+def test_forward_every_step_count(n, outputs):
+    """The GEMM's pipeline from one step of 128 columns to ten: exact sums, as above, against products in
+    64 bits on the GPU."""
+    m = 4100
+    x, w = grid_matrix(m, 1280, 3), grid_matrix(n, 1280, 4, shift=-5)
+    for k in range(128, 1281, 128):
+        print(f"case: forward_mxfp4 M={m} N={n} K={k}", flush=True)
+        p = bl.forward_mxfp4_plan(m, n, k)
+        assert p["kernel"] == "gemm" and p["outputs"] == outputs
+        xk, wk = x[:, :k].contiguous(), w[:, :k].contiguous()
+        y = bl.forward_mxfp4(*bl.quantize_mxfp4(wk), *bl.quantize_mxfp4(xk), m, n, k)
+        assert torch.equal(y.double(), xk.double() @ wk.double().t().contiguous())
+
+
 @pytest.mark.parametrize("m", [1, 7, 16, 20, 64, 130, 520, 4100])
 def test_forward_block_scales(m):
     """One block per row pair at its own power of two: each output is one product of scales."""
