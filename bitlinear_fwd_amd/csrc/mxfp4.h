@@ -209,6 +209,19 @@ __device__ __forceinline__ void stream8(T* p, int64_t n, const float (&v)[8], bo
   }
 }
 
+// Global memory, where the compiler cannot tell by itself.
+using GlobalBytes = const __attribute__((address_space(1))) uint8_t*;
+using GlobalV4i = const __attribute__((address_space(1))) v4i*;
+using GlobalInt = const __attribute__((address_space(1))) int*;
+
+// A pointer that is the same in every lane, into scalar registers.
+template <typename T>
+__device__ __forceinline__ T* uniform_ptr(T* p) {
+  const uint64_t v = (uint64_t)p;
+  return (T*)(((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32) |
+              (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
+}
+
 // Launchers (sizes and pointers validated by the C ABI).
 hipError_t launch_mx_quant(const void* X, int bf16, int64_t R, int64_t K, uint8_t* codes, uint8_t* scales,
                            void* values, hipStream_t s);

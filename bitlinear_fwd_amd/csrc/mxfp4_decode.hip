@@ -8,11 +8,13 @@
 // loads in flight over the sums of this row block.  Loads past the caches, as the weights are read
 // once.
 // More tokens, or longer rows of up to 16 (k_mx_decode): a workgroup takes one or two 16-row blocks of
-// the weights and TG groups of 16 tokens; its waves split the columns in groups of four tiles, the
-// next group's weights in flight, and add their sums in LDS at the end, in wave order.  Each weight
-// tile is one coalesced 1 KiB wave load straight into operand registers and serves TG matrix
-// instructions; the tokens' tiles come from L2, which is what bounds it from some 32 tokens on (65 ns
-// for a thousand products of a weight tile with 16 tokens).  16 x 8192 x 28672: 22.6 us, 5.5 TB/s of
+// the weights and TG groups of 16 tokens; its waves split the columns in groups of four tiles, and add
+// their sums in LDS at the end, in wave order.  Each weight tile is one coalesced 1 KiB wave load
+// straight into operand registers and serves TG matrix instructions; the tokens' tiles come from L2,
+// which is what bounds it from some 32 tokens on (14 ns for a workgroup's product of a weight tile with
+// 16 tokens).  The next group's weights are in flight over a whole group and the tokens' next tiles over
+// most of one, without branches around the loads (those had every group wait for its own: 256 x 2560 x
+// 6912 13.0 us, 11.8 so; 64 x 8192 x 28672 32.0 and 30.6).  16 x 8192 x 28672: 22.4 us, 5.6 TB/s of
 // weights.
 #include "mxfp4.h"
 
@@ -47,25 +49,6 @@ __device__ __forceinline__ void store_y(TY* y, int64_t left, v4f v) {
 // Barrier between LDS writes and reads that leaves global loads in flight.
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-// Four tiles of a row block's codes from p (16 bytes per lane; those past `left` are zeros).  kOnce:
-// past the caches.
-template <bool kOnce>
-__device__ __forceinline__ void load_group(const uint8_t* p, int left, v4i (&v)[4]) {
-  if (left >= 4) {
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const v4i* at = reinterpret_cast<const v4i*>(p + t * kMxTileBytes);
-      v[t] = kOnce ? __builtin_nontemporal_load(at) : *at;
-    }
-  } else {
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      v[t] = v4i{0, 0, 0, 0};
-      if (t < left) v[t] = *reinterpret_cast<const v4i*>(p + t * kMxTileBytes);
-    }
-  }
-}
-
 // RB row blocks of the weights by TG groups of 16 tokens.
 template <int TG, int RB, bool kOnce, typename TY>
 __global__ __launch_bounds__(512) void k_mx_decode(const uint8_t* __restrict__ codes,
@@ -78,54 +61,90 @@ __global__ __launch_bounds__(512) void k_mx_decode(const uint8_t* __restrict__ c
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
   const int64_t xb0 = (int64_t)blockIdx.y * TG;
+  const int last = tiles - 1;
+  const uint32_t lane16 = 16 * lane, lane4 = 4 * lane;
   for (int64_t nb0 = (int64_t)blockIdx.x * RB; nb0 < nblocks; nb0 += (int64_t)gridDim.x * RB) {
-    const uint8_t *wp[RB], *xp[TG];
-    const int *sp[RB], *xsp[TG];
+    GlobalBytes wp[RB], xp[TG], sp[RB], xsp[TG];
 #pragma unroll
     for (int i = 0; i < RB; ++i) {  // row blocks and token groups past the last repeat it; not stored
       const int64_t nb = min(nb0 + i, nblocks - 1);
-      wp[i] = codes + nb * tiles * kMxTileBytes + 16 * lane;
-      sp[i] = reinterpret_cast<const int*>(scales) + nb * groups * 64 + lane;
+      wp[i] = (GlobalBytes)uniform_ptr(codes + nb * tiles * kMxTileBytes);
+      sp[i] = (GlobalBytes)uniform_ptr(scales + nb * groups * 256);
     }
 #pragma unroll
     for (int j = 0; j < TG; ++j) {
       const int64_t xb = min(xb0 + j, xblocks - 1);
-      xp[j] = xcodes + xb * tiles * kMxTileBytes + 16 * lane;
-      xsp[j] = reinterpret_cast<const int*>(xscales) + xb * groups * 64 + lane;
+      xp[j] = (GlobalBytes)uniform_ptr(xcodes + xb * tiles * kMxTileBytes);
+      xsp[j] = (GlobalBytes)uniform_ptr(xscales + xb * groups * 256);
     }
     v4f acc[RB][TG];
 #pragma unroll
     for (int i = 0; i < RB; ++i)
 #pragma unroll
       for (int j = 0; j < TG; ++j) acc[i][j] = v4f{0, 0, 0, 0};
-    v4i w[2][RB][4];
-    int sw[2][RB];
-    auto fetch = [&](int g, v4i (&v)[RB][4], int (&sc)[RB]) {
-      const int left = g < groups ? tiles - 4 * g : 0;
+    // The weights of this group of four tiles and, on their way from memory, of the wave's next; the
+    // tokens' tiles come from L2, and their registers take the next group's once they have been used.
+    // Past the last tile the last again, so that no load depends on a branch.
+    v4i w[2][RB][4], x[TG][4];
+    int sw[2][RB], sx[TG];
+    auto tile_at = [&](int g, int t) { return (int64_t)min(4 * g + t, last) * kMxTileBytes; };
+    auto fetch_w = [&](int g, v4i (&v)[RB][4], int (&sc)[RB]) {
 #pragma unroll
       for (int i = 0; i < RB; ++i) {
-        sc[i] = left > 0 ? sp[i][g * 64] : 0;
-        load_group<kOnce>(wp[i] + (int64_t)g * 4096, left, v[i]);
+        sc[i] = *reinterpret_cast<GlobalInt>(sp[i] + (int64_t)g * 256 + lane4);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const GlobalV4i at = reinterpret_cast<GlobalV4i>(wp[i] + tile_at(g, t) + lane16);
+          v[i][t] = kOnce ? __builtin_nontemporal_load(at) : *at;
+        }
       }
     };
-    fetch(wave, w[0], sw[0]);
-    for (int g0 = wave; g0 < groups; g0 += 2 * waves) {
-      static_for<2>([&](auto u) {
-        constexpr int cur = u;
-        const int g = g0 + cur * waves;
-        if (g >= groups) return;
-        fetch(g + waves, w[1 - cur], sw[1 - cur]);
+    auto fetch_x = [&](int g, int j) {
+      sx[j] = *reinterpret_cast<GlobalInt>(xsp[j] + (int64_t)g * 256 + lane4);
 #pragma unroll
-        for (int j = 0; j < TG; ++j) {
-          v4i x[4];
-          const int sx = xsp[j][g * 64];
-          load_group<false>(xp[j] + (int64_t)g * 4096, tiles - 4 * g, x);
-          static_for<4>([&](auto t) {
+      for (int t = 0; t < 4; ++t) x[j][t] = *reinterpret_cast<GlobalV4i>(xp[j] + tile_at(g, t) + lane16);
+    };
+    auto work = [&](int g, auto cur_c, auto more_c) {
+      constexpr int cur = cur_c;
+      constexpr bool more = decltype(more_c)::value;
+      if constexpr (more) fetch_w(g + waves, w[1 - cur], sw[1 - cur]);
+      __builtin_amdgcn_sched_barrier(0);
+      // Tiles past the last take part with the last one's codes and both scales 2^-127: nothing is left
+      // of their products in 32 bits.
+      const int left = tiles - 4 * g;
+      const uint32_t mask = left >= 4 ? ~0u : (1u << 8 * left) - 1;
+      int s[RB];
 #pragma unroll
-            for (int i = 0; i < RB; ++i) acc[i][j] = mx_mfma<t, t>(w[cur][i][t], x[t], acc[i][j], sw[cur][i], sx);
-          });
-        }
+      for (int i = 0; i < RB; ++i) s[i] = sw[cur][i] & mask;
+      static_for<TG>([&](auto jj) {
+        constexpr int j = jj;
+        const int sj = sx[j] & mask;
+        static_for<4>([&](auto t) {
+#pragma unroll
+          for (int i = 0; i < RB; ++i) acc[i][j] = mx_mfma<t, t>(w[cur][i][t], x[j][t], acc[i][j], s[i], sj);
+        });
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (more) fetch_x(g + waves, j);
+        __builtin_amdgcn_sched_barrier(0);
       });
+    };
+    const std::integral_constant<int, 0> even;
+    const std::integral_constant<int, 1> odd;
+    if (wave < groups) {
+      int g = wave;
+      fetch_w(g, w[0], sw[0]);
+#pragma unroll
+      for (int j = 0; j < TG; ++j) fetch_x(g, j);
+      for (; g + 2 * waves < groups; g += 2 * waves) {
+        work(g, even, std::true_type{});
+        work(g + waves, odd, std::true_type{});
+      }
+      if (g + waves < groups) {
+        work(g, even, std::true_type{});
+        work(g + waves, odd, std::false_type{});
+      } else {
+        work(g, even, std::false_type{});
+      }
     }
 #pragma unroll
     for (int i = 0; i < RB; ++i)
@@ -336,14 +355,13 @@ hipError_t launch_mx_few(const uint8_t* codes, const uint8_t* scales, const void
 
 constexpr int64_t kMxDecodeTokens = 4096;  // the most that the rule below was measured with
 
-// Estimates in microseconds, fitted to 116 shapes of 130 to 4096 tokens measured both ways (and checked
-// on 50 of 20 to 128, where the decode kernel is the faster).  The decode kernel goes by rounds of one
-// workgroup to a compute unit and their products of a weight tile with 16 tokens; the GEMM by its steps
-// of 128 columns, of one or two narrow tiles to a unit or of rounds of two wide ones; both by the
-// weights' bytes.  The slower path is taken by at most 7 % (1000 x 640 x 2560: 8.9 against 8.6 us), but
-// for 20 x 28672 x 8192, 31.5 and 28.3.  Decode and GEMM in us: 64 x 8192 x 8192 11.8 and 22.0, 256 x 8192
-// x 8192 39.8 and 24.4, 256 x 2560 x 6912 13.1 and 15.6, 512 x 2560 x 2560 12.3 and 8.5, 1500 x 128 x 8192
-// 10.5 and 17.1.
+// Estimates in microseconds, fitted to 123 shapes of 20 to 4096 tokens measured both ways.  The decode
+// kernel goes by rounds of one workgroup to a compute unit and their products of a weight tile with 16
+// tokens; the GEMM by its steps of 128 columns, of one or two narrow tiles to a unit or of rounds of two
+// wide ones; both by the weights' bytes.  Where the slower path is taken it is so by at most 5 % (200 x
+// 8192 x 1024: 6.8 against 6.5 us).  Decode and GEMM in us: 64 x 8192 x 28672 30.6 and 72.2, 64 x 28672 x
+// 8192 36.5 and 34.1, 256 x 8192 x 8192 37.7 and 24.5, 256 x 2560 x 6912 11.8 and 15.6, 512 x 2560 x 2560
+// 11.4 and 8.5, 1500 x 128 x 8192 10.2 and 17.1.
 bool mx_decode_wins(int64_t M, int64_t N, int64_t K) {
   if (M <= 16) return true;
   if (M > kMxDecodeTokens) return false;

@@ -75,13 +75,6 @@ __device__ __forceinline__ void load1_lds(const uint8_t* p, uint32_t lds) {
       : "memory");
 }
 
-template <typename T>
-__device__ __forceinline__ T* uniform_ptr(T* p) {
-  const uint64_t v = (uint64_t)p;
-  return (T*)(((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32) |
-              (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
-}
-
 constexpr int kWaves = 4;  // of a workgroup: each has all tokens of the tile and a quarter of its outputs
 constexpr int TM = 4;      // tiles of 32 tokens
 constexpr int kR = 4;      // stages of 128 columns of the tokens in the ring
@@ -154,7 +147,6 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 
   for (int i = 0; i < TN; ++i)
     woff[i] = (uint32_t)((min(tn * BN + 2 * TN * wave + 2 * i + ((lane >> 4) & 1), nblocks - 1) - wb0) * row_bytes) +
               half_lane;
-  using GlobalBytes = const __attribute__((address_space(1))) uint8_t*;
   GlobalBytes wsrc = (GlobalBytes)uniform_ptr(codes + wb0 * row_bytes);
   // From here on the compiler may not assume that nothing writes what wsrc points to, so that its loads
   // stay between the same two of the assembly statements, whose waits count them.
@@ -175,7 +167,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 
   auto load_w = [&](int c, int h, v4i (&w)[TN]) {
     const GlobalBytes p = wsrc + (int64_t)min(c, last) * kMxTileBytes + 512 * h;
 #pragma unroll
-    for (int i = 0; i < TN; ++i) w[i] = *reinterpret_cast<const __attribute__((address_space(1))) v4i*>(p + woff[i]);
+    for (int i = 0; i < TN; ++i) w[i] = *reinterpret_cast<GlobalV4i>(p + woff[i]);
   };
   const uint8_t* lane_codes = lds + ((lane >> 4) & 1) * 1024 + half_lane;
   const uint8_t* lane_scales = lds + kR * kStage + ((lane >> 4) & 1) * 256 + half_lane / 4;
