@@ -280,6 +280,31 @@ def test_forward_offsets_past_32_bits():
     check_equal(host(scales[-wsc.size:]), wsc, "scales")
 
 
+@pytest.mark.parametrize("m,n", [(20, 262192), (600, 262192), (262192, 48)])
+def test_forward_codes_past_32_bits(m, n):
+    """Codes of more than 2^32 bytes (random grid values, all scales 1, so that sums are exact): both ends
+    of the long matrix against products of its slices."""
+    k, edge = 32768, 96
+    print(f"case: forward_mxfp4 M={m} N={n} K={k}", flush=True)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(m)
+
+    def matrix(rows):
+        codes = torch.randint(0, 256, (bl.mxfp4_codes_bytes(rows, k),), generator=g, dtype=torch.uint8, device=DEV)
+        return codes, torch.full((bl.mxfp4_scales_bytes(rows, k),), 127, dtype=torch.uint8, device=DEV)
+
+    w, x = matrix(n), matrix(m)
+    assert max(w[0].numel(), x[0].numel()) > 1 << 32
+    y = bl.forward_mxfp4(*w, *x, m, n, k)
+    cb, sb = bl.mxfp4_codes_bytes(edge, k), bl.mxfp4_scales_bytes(edge, k)
+    ends = [(slice(0, cb), slice(0, sb), slice(0, edge)), (slice(-cb, None), slice(-sb, None), slice(-edge, None))]
+    for c, sc, rows in ends:
+        if n > m:
+            assert torch.equal(y[:, rows], bl.forward_mxfp4(w[0][c], w[1][sc], *x, m, edge, k))
+        else:
+            assert torch.equal(y[rows], bl.forward_mxfp4(*w, x[0][c], x[1][sc], edge, n, k))
+
+
 def test_largest_k():
     """The longest rows the calls take, one token (the quantiser, then the decode kernel)."""
     n, k = 3, 1 << 24
