@@ -326,10 +326,13 @@ MxGemmPlan plan_mx_gemm(int64_t M, int64_t N, int64_t K) {
   // A tile of 256 outputs uses its tokens' tiles more often, two of them or three of 128 share a compute
   // unit.  128 and 256 wide, us: 512 x 8192 x 8192 (256 tiles of 128) 26.2 and 33.0, 1024 x 6912 x 2560
   // (432) 14.3 and 15.7, 1024 x 8192 x 8192 (512) 45.9 and 38.4, 700 x 8192 x 8192 (384) 41.4 and 34.3,
-  // 2048 x 6912 x 2560 (864) 27.6 and 25.0.
-  const int64_t t128 = ((M + 127) / 128) * ((N + 127) / 128);
+  // 2048 x 6912 x 2560 (864) 27.6 and 25.0.  Not where more than an eighth of the wide tiles lies past the
+  // last column: 16384 x 128 x 2560 12.1 and 16.7, 65536 x 640 x 2560 67.9 and 73.7 (65536 x 256 x 2560
+  // 40.4 and 34.7, 65536 x 1100 x 2560 189.6 and 180.9).
+  const int64_t columns = (N + 127) / 128, t128 = ((M + 127) / 128) * columns;
+  const bool many = t128 > 512 || (t128 > 256 && mx_tiles(K) >= 48), waste = columns % 2 == 1 && columns < 7;
   p.tile_m = 128;
-  p.tile_n = t128 > 512 || (t128 > 256 && mx_tiles(K) >= 48) ? 256 : 128;
+  p.tile_n = many && !waste ? 256 : 128;
   p.tiles_m = (M + p.tile_m - 1) / p.tile_m;
   p.tiles_n = (N + p.tile_n - 1) / p.tile_n;
   p.band = p.tiles_m * p.tiles_n > 512 ? 8 : p.tiles_m;

@@ -215,7 +215,7 @@ VARIANTS = [((1, 6912, 2560), ("lds", 16, 16), 1), ((16, 64, 8704), ("lds", 16, 
             ((1030, 1500, 1000), ("gemm", 128, 128), 2), ((2060, 2030, 260), ("gemm", 128, 128), 2),
             ((4100, 300, 640), ("gemm", 128, 128), 2), ((1030, 2000, 1930), ("gemm", 128, 128), 2),
             ((4100, 260, 2177), ("gemm", 128, 128), 2), ((1100, 2000, 4100), ("gemm", 128, 128), 2),
-            ((2100, 2000, 6200), ("gemm", 128, 256), 2)]
+            ((2100, 2000, 6200), ("gemm", 128, 256), 2), ((33000, 130, 600), ("gemm", 128, 256), 2)]
 
 
 @pytest.mark.parametrize("shape,want,launches", VARIANTS)
@@ -228,6 +228,14 @@ def test_plan(shape, want, launches):
     if p["kernel"] != "lds":  # workgroups cover the output once
         assert p["workgroups"] == -(-m // p["tokens"]) * -(-n // p["outputs"])
     assert p["threads"] in range(64, 1025, 64)
+
+
+@pytest.mark.parametrize("n,outputs", [(48, 128), (128, 128), (129, 256), (300, 128), (512, 256), (640, 128),
+                                       (700, 256), (800, 256), (1100, 256)])
+def test_plan_tile_width(n, outputs):
+    """Wide tiles of the GEMM only where little of them lies past the last column."""
+    p = bl.forward_mxfp4_plan(65536, n, 640)
+    assert p["kernel"] == "gemm" and p["outputs"] == outputs
 
 
 def test_plan_refusals():
