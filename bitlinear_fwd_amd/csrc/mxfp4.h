@@ -254,7 +254,7 @@ bool mx_decode_wins(int64_t M, int64_t N, int64_t K);
 
 // Launch plan of the GEMM: output tiles of tile_m tokens x tile_n outputs.
 struct MxGemmPlan {
-  int64_t tile_m = 256, tile_n = 256;
+  int64_t tile_m = 128, tile_n = 128;
   int64_t tiles_m = 0, tiles_n = 0;
   int64_t band = 1;  // token tiles of a band of the tile order
 };
