@@ -3,7 +3,8 @@
 // Forward: mean = sum x / K, var = sum (x - mean)^2 / K, rstd = 1 / sqrt(var + eps),
 // y = (x - mean) rstd w + b.  The row stays in registers between the two sums, so the variance is
 // of centred values (no cancellation between a mean of squares and a squared mean) and x is read
-// once.
+// once.  The mean is taken of x less an element of the row, so its rounding goes by the spread of the
+// row (below, at k_layernorm).
 //
 // Backward, with xhat = (x - mean) rstd and g = dy w:
 //   dx = rstd (g - mean(g) - xhat mean(g xhat)),  dw = sum_m dy xhat,  db = sum_m dy.
@@ -14,12 +15,13 @@
 // Both are bound by memory: x (and dy) in, y (dx) out.  A row is shared by a wave (up to 1024
 // elements, forward) or by as many waves as hold it with one or two groups of 8 elements a thread;
 // rows longer than 32768 (backward 12288) elements are read again for each sum, with the sums in
-// fp64.  Measured (a large copy moves 5.2 TB/s): forward 8192 x 8192 bf16 49.6 us, 5.4 TB/s; 2048 x
-// 8192 fp32 27.4 us, 4.9 TB/s; 16 x 2560 bf16 3.2 us, a launch and one round trip to memory.  Backward
+// fp64.  Measured (a large copy moves 5.2 TB/s): forward 8192 x 8192 bf16 47.8 us, 5.6 TB/s; 2048 x
+// 8192 fp32 25.8 us, 5.2 TB/s; 16 x 2560 bf16 3.3 us, a launch and one round trip to memory.  Backward
 // 8192 x 8192 bf16 91 us, 4.4 TB/s; 2048 x 2560 bf16 16.6 us, of which the second launch takes 4 and the
 // first about 6 before and after its rows; 1003 x 7001 fp32 26.2 us.  The sums over a row cost most
 // after the bytes: with lane exchanges through LDS and two barriers each, 8192 x 8192 took 53 us
-// forward and 112 backward.
+// forward (50 so) and 112 backward; then the next row's loads, which the compiler had waited for before
+// this row's sum (52.8 us with the mean as it is now, 47.8 since they stay in flight).
 #include "layernorm.h"
 
 #include <algorithm>
@@ -146,17 +148,40 @@ __device__ __forceinline__ void store_group(float* row, Cols c, int64_t K, const
   }
 }
 
+// How many elements of a row a wave has.
+template <typename T, int kG>
+__device__ __forceinline__ float wave_count(int wave, int threads, int K) {
+  int n = 0;
+#pragma unroll
+  for (int g = 0; g < kG; ++g) {
+    const Cols c = cols<T>(64 * wave, g, threads);
+    constexpr int kRun = sizeof(T) == 4 ? 256 : 512;  // fp32 has two runs of four columns a lane, bf16 one of eight
+    n += min(max(K - (int)c.a, 0), kRun);
+    if (sizeof(T) == 4) n += min(max(K - (int)c.b, 0), kRun);
+  }
+  return (float)n;
+}
+
 // One row per wave (kWave) or per workgroup, kG groups of 8 elements per thread (thread i of the T
 // that share the row takes groups i, i + T, ...).  A workgroup walks over rows with the next row's
 // loads in flight and (kHold) weight and bias in registers: read for every row they are four
 // times a bf16 row's bytes.
-template <typename T, bool kWave, int kG, bool kHold>
+// The mean is taken of x less a pivot, an element of the row (of three, the middle one, so that a single
+// outlier is none; each wave has its own), and only what is returned is the sum of the two.  So what is
+// rounded goes by the spread of a row and not by its mean, and a row of one value has exactly the
+// variance 0: a sum of the elements themselves gave a constant 100000.3 a spread of 0.008, and rows of
+// 1000 +- 0.01 outputs off by 4e-3.
+// kQuads: K % 4 == 0, so that a run of four columns is of the row or behind it as a whole: its zeros
+// then take no pivot, instead of a select for every element (8192 x 8192 bf16 47.8 us, 49.3 with selects;
+// 2048 x 20000 fp32 81 and 92).
+template <typename T, bool kWave, int kG, bool kHold, bool kQuads>
 __global__ __launch_bounds__(kWave ? 256 : 1024) void k_layernorm(const T* __restrict__ X, int64_t M, int64_t K,
                                                                   const float* __restrict__ weight,
                                                                   const float* __restrict__ bias, float eps,
                                                                   T* __restrict__ Y, float* __restrict__ mean_out,
                                                                   float* __restrict__ rstd_out) {
-  __shared__ float red[2][16];
+  __shared__ float2 red_sum[16];
+  __shared__ float red_sq[16];
   const int threads = kWave ? 64 : blockDim.x;
   const int i0 = kWave ? threadIdx.x & 63 : threadIdx.x;
   const int64_t step = (int64_t)gridDim.x * (kWave ? 4 : 1);
@@ -169,8 +194,8 @@ __global__ __launch_bounds__(kWave ? 256 : 1024) void k_layernorm(const T* __res
       raw[g] = load_group(X + r * K, c8, r < M ? K : 0);
     }
   };
-  // four groups of fp32 leave no registers for a row ahead (2048 x 20000: 77 us, 125
-  // with one, which spills)
+  // four groups of fp32 leave no registers for a row ahead (2048 x 20000: 77 us, 125 with one, which
+  // spills; with the pivots 81, two registers spilled)
   constexpr bool kAhead = kG < 4 || sizeof(T) == 2;
   if constexpr (kAhead) fetch(row);
   float w[kG][8], b[kG][8];
@@ -188,31 +213,64 @@ __global__ __launch_bounds__(kWave ? 256 : 1024) void k_layernorm(const T* __res
 #pragma unroll
     for (int g = 0; g < kG; ++g) params(g);
   }
-  for (; row < M; row += step) {
-    float v[kG][8], sum[1] = {0.0f}, sq[1] = {0.0f};
-    if constexpr (!kAhead) fetch(row);
-#pragma unroll
-    for (int g = 0; g < kG; ++g) {
-      widen8(raw[g], v[g]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum[0] += v[g][i];
-    }
-    if constexpr (kAhead) fetch(row + step);
-    row_sum<kWave, 1>(sum, red[0], i0 >> 6, threads >> 6);
-    const float mean = sum[0] / (float)K;
+  // the lanes of this wave whose first element is of the row, at least one
+  const int wave = __builtin_amdgcn_readfirstlane(i0 >> 6);
+  constexpr int kFirst = sizeof(T) == 4 ? 4 : 8;  // columns between the first elements of two lanes
+  const int lanes = min(((int)K - wave * 64 * kFirst + kFirst - 1) / kFirst, 64);
+  const float others = kWave ? 0.0f : wave_count<T, kG>(threadIdx.x & 15, threads, (int)K);
+  float v[kG][8];
+  // v -= p, and zeros stay zeros behind the row's end
+  auto less = [&](float p) {
 #pragma unroll
     for (int g = 0; g < kG; ++g) {
       const Cols c8 = cols<T>(i0, g, threads);
+      const float pa = c8.a < K ? p : 0.0f, pb = c8.b < K ? p : 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[g][i] = c8.at(i) < K ? v[g][i] - mean : 0.0f;
-        sq[0] += v[g][i] * v[g][i];
+      for (int i = 0; i < 8; ++i)
+        v[g][i] = kQuads ? v[g][i] - (i < 4 ? pa : pb) : c8.at(i) < K ? v[g][i] - p : 0.0f;
+    }
+  };
+  for (; row < M; row += step) {
+    float sum[1] = {0.0f}, sq[1] = {0.0f};
+    if constexpr (!kAhead) fetch(row);
+    Raw8<T> cur[kG];
+#pragma unroll
+    for (int g = 0; g < kG; ++g) {
+      cur[g] = raw[g];
+      // here, and not behind the next row's loads, the compiler waits for this row's
+      if constexpr (kAhead) {
+#pragma unroll
+        for (uint32_t& word : cur[g].w) asm volatile("" : "+v"(word));
       }
     }
-    row_sum<kWave, 1>(sq, red[1], i0 >> 6, threads >> 6);
+    if constexpr (kAhead) fetch(row + step);
+#pragma unroll
+    for (int g = 0; g < kG; ++g) widen8(cur[g], v[g]);
+    auto of = [&](int lane) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v[0][0]), lane)); };
+    const float pivot = __builtin_amdgcn_fmed3f(of(0), of(lanes >> 1), of(lanes - 1));
+    less(pivot);
+#pragma unroll
+    for (int g = 0; g < kG; ++g)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[0] += v[g][i];
+    sum[0] = wave_sum(sum[0]);
+    if constexpr (!kWave) {  // the waves' sums, of x less this wave's pivot
+      if ((threadIdx.x & 63) == 0) red_sum[wave] = make_float2(sum[0], pivot);
+      __syncthreads();
+      const int l = threadIdx.x & 15;
+      const float2 other = red_sum[l];
+      sum[0] = sum16(l < threads >> 6 ? other.x + others * (other.y - pivot) : 0.0f);
+    }
+    const float off = sum[0] / (float)K;  // the mean less the pivot
+    less(off);
+#pragma unroll
+    for (int g = 0; g < kG; ++g)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sq[0] += v[g][i] * v[g][i];
+    row_sum<kWave, 1>(sq, red_sq, i0 >> 6, threads >> 6);
     const float rstd = 1.0f / sqrtf(sq[0] / (float)K + eps);
     if (i0 == 0) {
-      if (mean_out) mean_out[row] = mean;
+      if (mean_out) mean_out[row] = pivot + off;
       if (rstd_out) rstd_out[row] = rstd;
     }
 #pragma unroll
@@ -488,8 +546,9 @@ void launch_fwd(const void* X, int64_t M, int64_t K, const float* w, const float
     constexpr bool kWave = decltype(wave)::value;
     constexpr int kG = decltype(gc)::value, rows = kWave ? 4 : 1;
     const int64_t most = kCUs * std::max(1, resident / waves);
-    k_layernorm<T, kWave, kG, kG <= 2><<<dim3((unsigned)std::min<int64_t>((M + rows - 1) / rows, most)), 64 * waves, 0,
-                                        s>>>(x, M, K, w, b, eps, y, mean, rstd);
+    const auto fn = K % 4 == 0 ? &k_layernorm<T, kWave, kG, kG <= 2, true> : &k_layernorm<T, kWave, kG, kG <= 2, false>;
+    fn<<<dim3((unsigned)std::min<int64_t>((M + rows - 1) / rows, most)), 64 * waves, 0, s>>>(x, M, K, w, b, eps, y,
+                                                                                            mean, rstd);
   };
   const std::integral_constant<int, 1> one;
   const std::integral_constant<int, 2> two;

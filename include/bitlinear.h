@@ -412,8 +412,10 @@ int bitlinear_forward_mxfp4_fused(const uint8_t* codes, const uint8_t* scales, c
  *   weight, bias  fp32 [K] (nullable: ones, zeros).
  *   mean, rstd    out (nullable): fp32 [M], what the backward pass takes.
  *   eps     finite and > 0 (BL_ERR_INVALID_ARG otherwise).
- * Sums are taken in fp32 or more; y is rounded to dt once.  A row with a NaN or an infinity,
- * or whose squares overflow fp32, has outputs that are not meaningful; other rows are not
+ * Sums are taken in fp32 or more, the mean's of x less an element of the row: errors go by
+ * the spread of a row and not by its mean, and a row of one value has the variance 0 and
+ * y = bias exactly.  y is rounded to dt once.  A row with a NaN or an infinity,
+ * or whose (x - mean)^2 overflow fp32, has outputs that are not meaningful; other rows are not
  * affected by it.
  *
  * bitlinear_layernorm_backward: with xhat = (x - mean) * rstd and g = dy * weight,

@@ -272,3 +272,66 @@ def test_layernorm_gradients_against_differences():
         up[i], down[i] = args[i] + step * v, args[i] - step * v
         slope = (loss(*up) - loss(*down)) / (2 * step)
         assert abs(slope - float((grad.double() * v.double()).sum())) <= 0.06, i
+
+
+# (M, K) that reach each form of the forward pass: rows of a wave with one and with two groups a thread,
+# of a workgroup with one, two and four, and the long form; each with a row that fills no whole group, and
+# with one of whole runs of four columns
+FORWARD_FORMS = [(9, 1), (9, 4), (9, 33), (9, 500), (9, 509), (9, 514), (9, 1000), (9, 1023), (9, 1025), (9, 2560),
+                 (9, 8191), (1030, 2560), (1030, 2561), (9, 10000), (9, 16383), (9, 20000), (9, 20001), (9, 32767),
+                 (9, 32768), (9, 40001)]
+
+
+def check_forward_near(x, w, b, eps, dtype):
+    """check_forward with bounds that go by the distances |x - mean| and not by the mean.  With p an element of the
+    row and r the largest |x - mean|, |x - p| <= |x - mean| + r:
+    * x - p is off by U (|x - mean| + r), and its mean by 72 U of the mean of that (that rounding, 64 of the sum, those
+      of p differing between waves, the division); the returned mean is rounded once more.
+    * Of the squares, the common part of these errors enters squared and the rounding of each x - p by twice its product
+      with x - mean, together at most 4 U (1 + r rstd) of the variance and eps (the mean of |x - mean| is below 1 / rstd);
+      their sum and rstd are rounded as in check_forward."""
+    y, mean, rstd = bl.layernorm(x, w, b, eps)
+    xh = acts_host_f32(x).astype(np.float64)
+    wh, bh = host(w).astype(np.float64), host(b).astype(np.float64)
+    wy, wm, wr = ref.layernorm(xh, wh, bh, eps)
+    dist = np.abs(xh - wm[:, None])
+    r = dist.max(1)
+    off = 72 * U * (dist.mean(1) + r) + 2.0 ** -50 * np.abs(xh).mean(1)  # (the last: the plain form's own)
+    within(host(mean), wm, off + U * np.abs(wm), "mean")
+    rel = 0.5 * (72 * U + 4 * U * (1 + r * wr) + (off * wr) ** 2) + 4 * U
+    within(host(rstd), wr, rel * wr, "rstd")
+    a = dist * wr[:, None] * np.abs(wh)
+    moved = (U * (2 * dist + r[:, None]) + off[:, None]) * wr[:, None] * np.abs(wh)
+    tol = moved * (1 + rel)[:, None] + a * (rel + 6 * U)[:, None] + 2 * U * (a + np.abs(bh))
+    within(acts_host_f32(y), wy, rounded(tol, wy, dtype), "y")
+    return y, mean, rstd
+
+
+@pytest.mark.parametrize("m,k", FORWARD_FORMS)
+def test_layernorm_constant_rows(m, k):
+    """Rows of one value, large against eps and not a number whose sums are exact in fp32: the variance
+    is 0, so y is the bias, rstd that of eps alone, and the mean the value itself."""
+    print(f"case: layernorm constant rows M={m} K={k}", flush=True)
+    values = [12345.678, 100000.3, -54321.1, 1e7 + 1, 1e-3 / 3, 123456792.0, -3.3, 7.0, 0.1]
+    _, w, b, _ = data(1, k, "f32", seed=k)
+    for dtype in ("f32", "bf16"):
+        x = torch.tensor([values[i % 9] for i in range(m)], device=DEV).to(DT[dtype])[:, None].repeat(1, k)
+        for eps in (1e-5, 1e-12):
+            y, mean, rstd = check_forward_near(x, w, b, eps, dtype)
+            assert torch.equal(mean, x[:, 0].float())
+            assert torch.equal(y, b.to(DT[dtype]).repeat(m, 1))
+            assert bool(((rstd.double() * eps ** 0.5 - 1).abs() <= 4 * U).all())
+
+
+@pytest.mark.parametrize("m,k", FORWARD_FORMS)
+def test_layernorm_small_spread_about_a_large_mean(m, k):
+    """Rows of 1000 +- 0.01, 100000 +- 0.5 and -30000 +- 100: the result goes by the spread."""
+    print(f"case: layernorm small spread M={m} K={k}", flush=True)
+    z, w, b, _ = data(m, k, "f32", seed=k, offset=0.0)
+    rows = torch.arange(m, device=DEV)[:, None] % 3
+    centre = torch.tensor([1000.0, 100000.0, -30000.0], device=DEV)[rows]
+    spread = torch.tensor([0.005, 0.25, 50.0], device=DEV)[rows]
+    x = centre + spread * z
+    for eps in (1e-5, 1e-12):
+        check_forward_near(x, w, b, eps, "f32")
+    check_forward_near((centre + 30 * spread * z).to(torch.bfloat16), w, b, 1e-5, "bf16")
