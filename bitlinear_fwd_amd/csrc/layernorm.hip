@@ -390,9 +390,11 @@ __global__ __launch_bounds__(kG == 1 ? 1024 : 768) void k_layernorm_bwd(
     float c[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int g = 0; g < kG; ++g) {
+      const Cols c8 = cols<T>(i0, g, threads);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        x[g][i] = (x[g][i] - mean) * rstd;  // past the row's end d is 0, so the sums are not touched
+        // past the row's end d is 0; x has to be finite there, which mean * rstd need not be
+        x[g][i] = c8.at(i) < K ? (x[g][i] - mean) * rstd : 0.0f;
         if constexpr (kSums) {
           dw[g][i] += d[g][i] * x[g][i];
           db[g][i] += d[g][i];
@@ -469,7 +471,8 @@ __global__ __launch_bounds__(1024) void k_layernorm_bwd_long(const T* __restrict
       for (int i = 0; i < 8; ++i) {
         const float g = weight ? d[i] * w[i] : d[i];
         c[0] += (double)g;
-        c[1] += (double)g * (double)((x[i] - mean) * rstd);
+        // past the row's end g is 0, but mean * rstd need not be finite
+        c[1] += (double)g * (double)(col + i < K ? (x[i] - mean) * rstd : 0.0f);
       }
     }
     row_sum<false, 2>(c, red[turn], threadIdx.x >> 6, 16);

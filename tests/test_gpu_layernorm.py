@@ -335,3 +335,20 @@ def test_layernorm_small_spread_about_a_large_mean(m, k):
     for eps in (1e-5, 1e-12):
         check_forward_near(x, w, b, eps, "f32")
     check_forward_near((centre + 30 * spread * z).to(torch.bfloat16), w, b, 1e-5, "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("m,k", [(4, 33), (4, 500), (20, 514), (4, 1000), (4, 2561), (4, 8190), (4, 9000), (4, 12288),
+                                 (4, 12290), (3, 40001)])
+def test_layernorm_backward_of_large_constant_rows(m, k, dtype):
+    """A row of one value whose mean * rstd is beyond fp32: x - mean is 0, so dx is rstd (g - mean(g)), and the columns
+    between the row's end and the threads' must not get in the way."""
+    print(f"case: layernorm_backward large constant row M={m} K={k} {dtype}", flush=True)
+    x, w, b, dy = data(m, k, dtype, seed=k)
+    x[1] = 2.5e37
+    x[m - 1] = -3e37
+    _, mean, rstd = bl.layernorm(x, w, b, 1e-5)
+    assert torch.equal(mean[1], x[1, 0].float()) and abs(float(rstd[1]) * 1e-5 ** 0.5 - 1) < 1e-6
+    dx, dw, db = check_backward(dy, x, w, mean, rstd, dtype)
+    assert torch.isfinite(dx).all()
+    assert torch.equal(bl.layernorm_backward(dy, x, w, mean, rstd, want_params=False), dx)
