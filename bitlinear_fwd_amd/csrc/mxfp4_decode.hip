@@ -19,6 +19,7 @@
 #include "mxfp4.h"
 
 #include <algorithm>
+#include <atomic>
 
 namespace bl {
 namespace {
@@ -311,6 +312,7 @@ void launch(const MxDecodePlan& p, const uint8_t* codes, const uint8_t* scales, 
 // launch against two (graph replays; the issue of an eager call takes 9.3 and 14 us): 16 x 2560 x 2560
 // 5.6 and 7.4 us, 16 x 2560 x 6912 (3584 blocks) 9.1 and 9.3, 4 x 8192 x 28672 (3584) 25.4 and 26.3.
 constexpr int64_t kFewItems = 4096;
+constexpr int64_t kFewLds = 160 * 1024;  // of a compute unit
 
 MxFewPlan plan_mx_few(int64_t M, int64_t N, int64_t K, int src) {
   MxFewPlan p;
@@ -323,7 +325,7 @@ MxFewPlan plan_mx_few(int64_t M, int64_t N, int64_t K, int src) {
   p.waves = (int)std::min<int64_t>(16, std::max(groups, src ? (items + 63) / 64 : 1));
   p.groups = std::min<int64_t>(mx_row_blocks(N), 256 * (16 / p.waves));
   p.lds = 2 * std::min<int64_t>(p.waves, groups) * 1024 + groups * 272 * M;
-  p.ok = p.lds <= 160 * 1024;
+  p.ok = p.lds <= kFewLds;
   return p;
 }
 
@@ -334,10 +336,21 @@ hipError_t launch_mx_few(const uint8_t* codes, const uint8_t* scales, const void
   auto go = [&](auto sc, auto yt) {
     using TY = decltype(yt);
     constexpr int kSrc = decltype(sc)::value;
+    // the LDS limit above 64 KiB is raised once per device for this kernel, to the most that a plan asks
+    // for: host threads share it, and one with a smaller call must not lower it for another (a repeated
+    // set from a concurrent first call is harmless)
+    static std::atomic<uint64_t> raised{0};
     if (p.lds > 65536) {
-      const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_mx_few<kSrc, TY>),
-                                               hipFuncAttributeMaxDynamicSharedMemorySize, (int)p.lds);
+      int dev = 0;
+      hipError_t e = hipGetDevice(&dev);
       if (e != hipSuccess) return e;
+      const uint64_t bit = uint64_t(1) << (dev & 63);
+      if (!(raised.load(std::memory_order_relaxed) & bit)) {
+        e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_mx_few<kSrc, TY>),
+                                hipFuncAttributeMaxDynamicSharedMemorySize, (int)kFewLds);
+        if (e != hipSuccess) return e;
+        raised.fetch_or(bit, std::memory_order_relaxed);
+      }
     }
     k_mx_few<kSrc, TY><<<dim3((unsigned)p.groups), 64 * p.waves, p.lds, s>>>(
         codes, scales, x, xscales, (int)M, N, K, (int)mx_tiles(K), (int)mx_groups(K),

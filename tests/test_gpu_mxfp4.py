@@ -1,5 +1,7 @@
 """MXFP4 on the GPU against the plain 64-bit forms: codes, scales and values bit for bit, products
 within a bound on fp32 sums (and bit for bit where every partial sum is an fp32 number)."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -394,3 +396,37 @@ def test_norm_quantise_product_together(tokens):
     check_product(gate, yv, ref.quantize(host(wg))[2], d)
     check_product(up, yv, ref.quantize(host(wu))[2], d)
     check_product(out, ref.quantize(host(hidden))[2], ref.quantize(host(wd))[2], h)
+
+
+def test_host_threads_with_different_lds():
+    """Host threads that call at once, each on a stream of its own, with sizes of the one-launch kernel that
+    take different amounts of LDS above 64 KiB."""
+    n, calls = 64, 150
+    cases = []
+    assert bl.forward_mxfp4_plan(8, n, 8704, x="f32")["launches"] == 1
+    for i, (m, k) in enumerate([(16, 14848), (16, 8704), (8, 8704), (16, 8200)]):
+        assert bl.forward_mxfp4_plan(m, n, k)["kernel"] == "lds"
+        x, w = grid_matrix(m, k, i), grid_matrix(n, k, i + 9, shift=-5)
+        cases.append((m, k, x, bl.quantize_mxfp4(w), bl.quantize_mxfp4(x), x.double() @ w.double().t().contiguous()))
+    torch.cuda.synchronize()
+    failures = []
+
+    def work(i):
+        m, k, x, wq, xq, want = cases[i]
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                out = [bl.forward_mxfp4(*wq, *xq, m, n, k) for _ in range(calls)]
+                if m == 8:
+                    out += [bl.forward_mxfp4_fused(*wq, x, n, k) for _ in range(calls)]
+                torch.cuda.current_stream().synchronize()
+            if not all(torch.equal(y.double(), want) for y in out):
+                failures.append((i, "wrong"))
+        except Exception as e:  # reported by the main thread
+            failures.append((i, repr(e)))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failures, failures

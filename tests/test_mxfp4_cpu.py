@@ -1,6 +1,8 @@
 """MXFP4 and layer norm on the host: size helpers, refusals, and the tests' own plain forms
 checked against hand-derived values.  No call here reaches a GPU."""
 import ctypes
+import os
+import re
 
 import numpy as np
 import pytest
@@ -243,3 +245,14 @@ def test_plan_refusals():
     f = bl.lib().bitlinear_forward_mxfp4_plan
     assert f(0, 1, 1, -1, out) == BAD and f(1, 1, 1 << 25, -1, out) == BAD and f(1, 1, 1, -1, None) == BAD
     assert f(1, 1, 1, 5, out) == UNS and f(1 << 30, 1 << 30, 1, -1, out) == UNS
+
+
+def test_lds_limits_are_constants():
+    """A kernel's LDS limit is shared by all host threads, so each is set to one constant and never to a call's
+    own size, which another thread's larger call could find in its way."""
+    csrc = os.path.join(os.path.dirname(bl.__file__), "csrc")
+    sizes = []
+    for name in sorted(os.listdir(csrc)):
+        with open(os.path.join(csrc, name)) as f:
+            sizes += re.findall(r"hipFuncAttributeMaxDynamicSharedMemorySize,\s*(?:\(int\)\s*)?([\w.]+)", f.read())
+    assert len(sizes) >= 2 and all(re.fullmatch(r"k[A-Z]\w*|\d+", v) for v in sizes), sizes
