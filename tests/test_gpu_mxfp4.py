@@ -8,7 +8,7 @@ import torch
 
 import bitlinear_fwd_amd as bl
 import mxfp4_reference as ref
-from test_mxfp4_cpu import VARIANTS
+from test_mxfp4_cpu import FORMS, VARIANTS
 from gpu_helpers import acts_host_f32, check_equal, host
 
 pytestmark = pytest.mark.gpu
@@ -430,3 +430,20 @@ def test_host_threads_with_different_lds():
     for t in threads:
         t.join()
     assert not failures, failures
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("m,n,k", sorted({shape for _, shape in FORMS} | {v[0] for v in VARIANTS}))
+def test_forward_exact_sums_of_every_form(m, n, k, out):
+    """Exact sums, as above, in every form of the kernels and in both output types (bf16: the exact sum,
+    an fp32 number, rounded once); rows behind the last token are left alone."""
+    print(f"case: forward_mxfp4 form M={m} N={n} K={k} -> {out}", flush=True)
+    x, w = grid_matrix(m, k, m + 3), grid_matrix(n, k, n + 4, shift=-5)
+    wq, xq = bl.quantize_mxfp4(w), bl.quantize_mxfp4(x)
+    want = torch.from_numpy(host(x).astype(np.float64) @ host(w).astype(np.float64).T).float().to(DT[out])
+    for call in (lambda y: bl.forward_mxfp4(*wq, *xq, m, n, k, y=y), lambda y: bl.forward_mxfp4_fused(*wq, x, n, k, y=y),
+                 lambda y: bl.forward_mxfp4_fused(*wq, x.to(torch.bfloat16), n, k, y=y)):
+        y = torch.full((m + 1, n), 777.0, dtype=DT[out], device=DEV)
+        call(y[:m])
+        check_equal(acts_host_f32(y[:m]), acts_host_f32(want), "y")
+        assert (y[m:] == 777.0).all()

@@ -256,3 +256,25 @@ def test_lds_limits_are_constants():
         with open(os.path.join(csrc, name)) as f:
             sizes += re.findall(r"hipFuncAttributeMaxDynamicSharedMemorySize,\s*(?:\(int\)\s*)?([\w.]+)", f.read())
     assert len(sizes) >= 2 and all(re.fullmatch(r"k[A-Z]\w*|\d+", v) for v in sizes), sizes
+
+
+# (M, N, K) of each form of the products' kernels: the GPU tests run all of them, with both output types
+FORMS = [("lds", (7, 100, 513)), ("decode 16 16 once", (16, 40, 28672)), ("decode 16 32 once", (16, 4100, 28672)),
+         ("decode 32 16 once", (17, 64, 128)), ("decode 32 32 once", (20, 4100, 1100)),
+         ("decode 64 16 once", (64, 2560, 2560)), ("decode 64 32 once", (37, 6909, 2570)),
+         ("decode 64 32 once", (50, 4099, 1030)), ("decode 64 32 once", (64, 4112, 384)),
+         ("decode 64 16 again", (520, 300, 640)), ("decode 64 32 again", (100, 4100, 1100)),
+         ("gemm 128", (1030, 1500, 1000)), ("gemm 256", (2100, 4000, 390))]
+
+
+def form(m, n, k):
+    p = bl.forward_mxfp4_plan(m, n, k)
+    if p["kernel"] != "decode":
+        return p["kernel"] if p["kernel"] == "lds" else f"gemm {p['outputs']}"
+    once = "once" if p["workgroups"] == -(-n // p["outputs"]) else "again"
+    return f"decode {p['tokens']} {p['outputs']} {once}"
+
+
+@pytest.mark.parametrize("want,shape", FORMS)
+def test_form(want, shape):
+    assert form(*shape) == want
