@@ -50,7 +50,8 @@ __device__ __forceinline__ void store_y(TY* y, int64_t left, v4f v) {
 // Barrier between LDS writes and reads that leaves global loads in flight.
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-// RB row blocks of the weights by TG groups of 16 tokens.
+// RB row blocks of the weights by TG groups of 16 tokens.  kOnce: each weight is read by one workgroup,
+// and past the caches.
 template <int TG, int RB, bool kOnce, typename TY>
 __global__ __launch_bounds__(512) void k_mx_decode(const uint8_t* __restrict__ codes,
                                                    const uint8_t* __restrict__ scales,
@@ -300,7 +301,10 @@ __global__ __launch_bounds__(1024) void k_mx_few(const uint8_t* __restrict__ cod
 template <int TG, int RB, typename TY>
 void launch(const MxDecodePlan& p, const uint8_t* codes, const uint8_t* scales, const uint8_t* xcodes,
             const uint8_t* xscales, int64_t M, int64_t N, int64_t K, void* Y, hipStream_t s) {
-  const auto fn = p.gy == 1 ? &k_mx_decode<TG, RB, true, TY> : &k_mx_decode<TG, RB, false, TY>;
+  auto fn = &k_mx_decode<TG, RB, true, TY>;
+  if constexpr (TG == 4) {  // more than 64 tokens read the weights more than once
+    if (p.gy > 1) fn = &k_mx_decode<TG, RB, false, TY>;
+  }
   fn<<<dim3((unsigned)p.gx, (unsigned)p.gy), 64 * p.waves, p.waves * RB * TG * 1024, s>>>(
       codes, scales, xcodes, xscales, M, N, (int)mx_tiles(K), (int)mx_groups(K), mx_row_blocks(N), mx_row_blocks(M),
       static_cast<TY*>(Y));

@@ -278,3 +278,16 @@ def form(m, n, k):
 @pytest.mark.parametrize("want,shape", FORMS)
 def test_form(want, shape):
     assert form(*shape) == want
+
+
+def test_every_form_of_the_library_is_listed():
+    """The products' kernels in the built library are those of FORMS, each with both output types (and the
+    one-launch kernel with its three sources): none that no call reaches, and none that no test runs."""
+    with open(bl.LIB_PATH, "rb") as f:
+        names = f.read()
+    built = {(f"decode {16 * int(tg)} {16 * int(rb)} {'once' if once == b'1' else 'again'}", y.decode())
+             for tg, rb, once, y in re.findall(rb"k_mx_decodeILi(\d)ELi(\d)ELb(\d)E([ft])E", names)}
+    built |= {(f"gemm {128 * int(tn)}", y.decode()) for tn, y in re.findall(rb"k_mx_gemmILi(\d)E([ft])E", names)}
+    built |= {("lds", src.decode() + y.decode()) for src, y in re.findall(rb"k_mx_fewILi(\d)E([ft])E", names)}
+    listed = {(w, y) for w in {w for w, _ in FORMS} - {"lds"} for y in "ft"}
+    assert built == listed | {("lds", s + y) for s in "012" for y in "ft"}
