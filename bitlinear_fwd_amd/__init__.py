@@ -1053,19 +1053,27 @@ def forward_mxfp4(codes, scales, xcodes, xscales, m: int, n: int, k: int, y=None
     return y
 
 
+def _named_dtype(name: str) -> int:
+    """The bl_dtype of "f32" or "bf16"."""
+    if name not in ("f32", "bf16"):
+        raise ValueError(f'a type must be "f32" or "bf16", not {name!r}')
+    return BL_BF16 if name == "bf16" else BL_F32
+
+
 def forward_mxfp4_plan(m: int, n: int, k: int, x=None) -> dict:
     """The launches of forward_mxfp4 (``x`` None) or of forward_mxfp4_fused (``x`` "bf16" or "f32")
     for (M, N, K), computed on the host."""
     out = (ctypes.c_int32 * 6)()
-    xdt = -1 if x is None else BL_BF16 if x == "bf16" else BL_F32
+    xdt = -1 if x is None else _named_dtype(x)
     _check("bitlinear_forward_mxfp4_plan", lib().bitlinear_forward_mxfp4_plan(m, n, k, xdt, out))
     return {"kernel": {7: "lds", 8: "decode", 9: "gemm"}[out[0]], "workgroups": out[1], "threads": out[2],
             "tokens": out[3], "outputs": out[4], "launches": out[5]}
 
 
 def forward_mxfp4_fused_ws_bytes(m: int, n: int, k: int, dtype: str = "bf16") -> int:
-    """Workspace bytes bitlinear_forward_mxfp4_fused needs for (M, N, K) (0: none)."""
-    v = int(lib().bitlinear_forward_mxfp4_fused_ws_bytes(m, n, k, BL_BF16 if dtype == "bf16" else BL_F32))
+    """Workspace bytes bitlinear_forward_mxfp4_fused needs for (M, N, K) and x of ``dtype`` "bf16"
+    or "f32" (0: none)."""
+    v = int(lib().bitlinear_forward_mxfp4_fused_ws_bytes(m, n, k, _named_dtype(dtype)))
     if v < 0:
         raise ValueError(f"invalid shape {(m, n, k)}")
     return v

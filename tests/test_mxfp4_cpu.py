@@ -291,3 +291,12 @@ def test_every_form_of_the_library_is_listed():
     built |= {("lds", src.decode() + y.decode()) for src, y in re.findall(rb"k_mx_fewILi(\d)E([ft])E", names)}
     listed = {(w, y) for w in {w for w, _ in FORMS} - {"lds"} for y in "ft"}
     assert built == listed | {("lds", s + y) for s in "012" for y in "ft"}
+
+
+@pytest.mark.parametrize("name", ["bfloat16", "fp32", "BF16", "", 0, torch.bfloat16])
+def test_type_names(name):
+    """A type the calls do not know is refused, not described as fp32."""
+    with pytest.raises(ValueError):
+        bl.forward_mxfp4_plan(16, 64, 512, x=name)
+    with pytest.raises(ValueError):
+        bl.forward_mxfp4_fused_ws_bytes(16, 64, 512, name)
