@@ -910,7 +910,9 @@ class BitLinear:
 
 # The calls below take a few microseconds of host time each, a launch included, so what they need of
 # torch and of the library is looked up once, their checks read every attribute once, and they
-# allocate nothing that the caller has given.
+# allocate nothing that the caller has given.  The current stream and device are asked for below
+# torch's public functions, as its own generated code does (0.08 us for the stream, 1.1 through
+# torch.cuda.current_stream).
 
 
 class _Runtime:
@@ -1104,7 +1106,10 @@ def forward_mxfp4_fused(codes, scales, x, n: int, k: int, y=None, workspace=None
 
 def layernorm(x, weight=None, bias=None, eps: float = 1e-5, y=None, mean=None, rstd=None):
     """Layer normalisation of the rows of x[M][K] (fp32 or bf16) with fp32 weight and bias
-    (None: ones, zeros).  Returns ``(y, mean fp32 [M], rstd fp32 [M])``; y has x's type."""
+    (None: ones, zeros).  Returns ``(y, mean fp32 [M], rstd fp32 [M])``; y has x's type.
+
+    Like every call here it builds no autograd graph, also where an input requires a gradient:
+    a training program takes the gradients from layernorm_backward."""
     rt = _RT or _runtime()
     dt = _require_rows(rt, x, "x")
     m, k = x.shape

@@ -373,8 +373,8 @@ __global__ __launch_bounds__(kG == 1 ? 1024 : 768) void k_layernorm_bwd(
   };
   const int64_t first = (int64_t)blockIdx.x * rows, step = (int64_t)gridDim.x * rows;
   int turn = 0;
-  // two groups of fp32 leave no registers for a row ahead (2048 x 11000: 63.5 us, 83.9
-  // with one, which spills)
+  // two groups of fp32 leave no registers for a row ahead (2048 x 11000: 63.1 us, with nine registers
+  // spilled once the sums are taken; 83.9 with a row ahead)
   constexpr bool kAhead = kG == 1 || sizeof(T) == 2;
   if constexpr (kAhead) fetch(first + sub);
   for (int64_t r0 = first; r0 < M; r0 += step) {  // the same trips for every thread: barriers inside

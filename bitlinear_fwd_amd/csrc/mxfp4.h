@@ -182,10 +182,11 @@ __device__ __forceinline__ void store8(uint16_t* p, int64_t n, const float (&v)[
   }
 }
 
-// store8 past the caches, for outputs larger than they hold (quantiser with values, 6912 x 2560 fp32:
-// 28.0 us, 35.2 with ordinary stores; layer norm 8192 x 8192 bf16 61 and 65 us).  Not for rows that
-// start inside a 16-byte piece, whose partial lines it would write one by one (quantiser, 1003 x 7001
-// bf16: 9.8 against 9.1 us): whole_pieces tells.
+// store8 past the caches (quantiser with values, 6912 x 2560 fp32: 28.0 us, 35.2 with ordinary stores;
+// layer norm 8192 x 8192 bf16 61 and 65 us).  Not for rows that start inside a 16-byte piece, whose
+// partial lines it would write one by one (quantiser, 1003 x 7001 bf16: 9.8 against 9.1 us):
+// whole_pieces tells.  The choice goes by the row length alone: outputs that the caches would hold are
+// stored past them too, and what that costs a call that reads them at once has not been measured.
 __host__ __device__ __forceinline__ bool whole_pieces(int64_t K) { return K % 8 == 0; }
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef v4u v4u_unaligned __attribute__((aligned(2)));

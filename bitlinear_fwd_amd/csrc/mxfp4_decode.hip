@@ -15,7 +15,8 @@
 // 16 tokens).  The next group's weights are in flight over a whole group and the tokens' next tiles over
 // most of one, without branches around the loads (those had every group wait for its own: 256 x 2560 x
 // 6912 13.0 us, 11.8 so; 64 x 8192 x 28672 32.0 and 30.6).  16 x 8192 x 28672: 22.4 us, 5.6 TB/s of
-// weights.
+// weights.  Groups of 16 tokens past the last are loaded and multiplied for nothing where their number is
+// no multiple of TG: 33 to 48 tokens do the work of 64 (37 x 6909 x 2570 6.1 us), 65 to 80 that of 128.
 #include "mxfp4.h"
 
 #include <algorithm>
@@ -313,8 +314,10 @@ void launch(const MxDecodePlan& p, const uint8_t* codes, const uint8_t* scales, 
 }  // namespace
 
 // Blocks that a workgroup quantises by itself at most; beyond, the quantiser runs first.  Measured, one
-// launch against two (graph replays; the issue of an eager call takes 9.3 and 14 us): 16 x 2560 x 2560
-// 5.6 and 7.4 us, 16 x 2560 x 6912 (3584 blocks) 9.1 and 9.3, 4 x 8192 x 28672 (3584) 25.4 and 26.3.
+// launch against two (graph replays; the issue of an eager call takes 8.5 and 14 us): 16 x 2560 x 2560
+// 5.6 and 7.4 us, 16 x 2560 x 6912 (3584 blocks) 9.1 and 10.2, 4 x 8192 x 28672 (3584) 24.9 and 27.3; at
+// the bound 16 x 2560 x 8192 9.6 and 10.4, 16 x 28672 x 8192 26.9 and 28.6, 4 x 2560 x 32768 15.3 and
+// 16.7.  More blocks have not been measured.
 constexpr int64_t kFewItems = 4096;
 constexpr int64_t kFewLds = 160 * 1024;  // of a compute unit
 

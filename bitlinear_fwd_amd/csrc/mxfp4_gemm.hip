@@ -9,10 +9,11 @@
 // Per step of 128 columns of two wide tiles a compute unit spends 1024 cycles on matrix instructions,
 // 820 on loads (60 bytes a cycle, to LDS or to registers) and 770 on LDS (the tokens' 64 bytes a cycle
 // in, 128 out).  Measured before: both matrices through LDS, waves of 64 tokens x 128 outputs, which is
-// 1540 cycles of LDS: 2048 x 6912 x 2560 to fp32 27.4 us, 24.9 so; 1024 x 4096 x 4096 16.1 and 13.3;
-// 8192^3 to bf16 262 and 249, 4.42 PFLOP/s; and tiles of 256 x 256 with one workgroup to a unit (load,
-// compute and store in turn) 283.  What bounds the large shapes now is power: with all-zero operands
-// 8192^3 takes 163 us.  2048 x 6912 x 2560, 24.9 us: 432 tiles on 512 places, 57 MB of output; zeros 20.5.
+// 1540 cycles of LDS: 2048 x 6912 x 2560 to fp32 27.4 us, 24.4 so; 1024 x 4096 x 4096 16.1 and 13.4;
+// 8192^3 to bf16 262 and 245, 4.5 PFLOP/s (from run to run 24.4 to 26.6 and 245 to 259 us); and tiles of
+// 256 x 256 with one workgroup to a unit (load, compute and store in turn) 283.  What bounds the large
+// shapes now is power: with all-zero operands 8192^3 takes 163 us.  2048 x 6912 x 2560: 432 tiles on 512
+// places, 57 MB of output; zeros 20.5 us.
 //   * 32x32x64 instructions: with the 16x16x128 form the waves cannot issue fast enough (5.4 against
 //     9.6 PFLOP/s from registers, one wave per SIMD).
 //   * The tile layout is the operand layout.  A wave loads its own weights' fragments straight from
@@ -34,7 +35,11 @@
 //     tiles.  Where they do not all run at once, the run goes down bands of eight token tiles, so that
 //     the 64 tiles at work on an XCD share eight tiles of each matrix rather than read all tokens
 //     (8192^3 to bf16 271 us with tokens fastest, 263 so; 2048 x 8192 x 8192 71.8 and 69.0).
-//   * Output rows are stored past the caches (2048 x 6912 x 2560 30.3 us without, 26.4 so).
+//   * Output rows are stored past the caches where they are whole 16-byte pieces (2048 x 6912 x 2560
+//     30.3 us without, 26.4 so).  A width that is no multiple of 128 is slower than the next one that is:
+//     65536 x 520 x 640 to fp32 54 us, x 640 36; x 300 37, x 384 25; x 1100 103, x 1152 65; 16384 x 48 x 640
+//     7.8, x 128 5.8.  Its rows start inside cache lines, which whole slabs then store in parts, and the
+//     slabs at its edge store piece by piece (which of the two costs more has not been measured).
 #include "mxfp4.h"
 
 #include <algorithm>
@@ -326,9 +331,11 @@ MxGemmPlan plan_mx_gemm(int64_t M, int64_t N, int64_t K) {
   // A tile of 256 outputs uses its tokens' tiles more often, two of them or three of 128 share a compute
   // unit.  128 and 256 wide, us: 512 x 8192 x 8192 (256 tiles of 128) 26.2 and 33.0, 1024 x 6912 x 2560
   // (432) 14.3 and 15.7, 1024 x 8192 x 8192 (512) 45.9 and 38.4, 700 x 8192 x 8192 (384) 41.4 and 34.3,
-  // 2048 x 6912 x 2560 (864) 27.6 and 25.0.  Not where more than an eighth of the wide tiles lies past the
-  // last column: 16384 x 128 x 2560 12.1 and 16.7, 65536 x 640 x 2560 67.9 and 73.7 (65536 x 256 x 2560
-  // 40.4 and 34.7, 65536 x 1100 x 2560 189.6 and 180.9).
+  // 2048 x 6912 x 2560 (864) 27.6 and 25.0.  Not where half a tile of fewer than four lies past the last
+  // column: 16384 x 128 x 2560 12.1 and 16.7, 65536 x 640 x 2560 67.9 and 73.7 (65536 x 256 x 2560 40.4 and
+  // 34.7, 65536 x 1100 x 2560 189.6 and 180.9).  That rule goes by the number of columns alone and takes the
+  // slower side where the last one is nearly empty or the rows are long: 65536 x 520 x 640 53.4 and 50.4,
+  // 16384 x 520 x 640 18.5 and 15.9, 65536 x 520 x 8192 224 and 214, 16384 x 384 x 8192 40.7 and 38.5.
   const int64_t columns = (N + 127) / 128, t128 = ((M + 127) / 128) * columns;
   const bool many = t128 > 512 || (t128 > 256 && mx_tiles(K) >= 48), waste = columns % 2 == 1 && columns < 7;
   p.tile_m = 128;
