@@ -447,3 +447,21 @@ def test_forward_exact_sums_of_every_form(m, n, k, out):
         call(y[:m])
         check_equal(acts_host_f32(y[:m]), acts_host_f32(want), "y")
         assert (y[m:] == 777.0).all()
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("m,n,k", sorted({shape for _, shape in FORMS}) + [(2304, 2560, 512), (1, 6912, 2560)])
+def test_forward_unaligned_rows(m, n, k, out):
+    """x and y that start at an odd element of their storage: exact sums, as above, and nothing written before
+    or behind y."""
+    print(f"case: forward_mxfp4 unaligned M={m} N={n} K={k} -> {out}", flush=True)
+    x, w = grid_matrix(m, k, m + 5), grid_matrix(n, k, n + 6, shift=-5)
+    wq = bl.quantize_mxfp4(w)
+    want = torch.from_numpy(host(x).astype(np.float64) @ host(w).astype(np.float64).T).float().to(DT[out])
+    for dtype in ("f32", "bf16"):
+        flat = torch.empty(1 + m * k, dtype=DT[dtype], device=DEV)
+        flat[1:] = x.to(DT[dtype]).reshape(-1)
+        y = torch.full((m * n + 2,), 777.0, dtype=DT[out], device=DEV)
+        bl.forward_mxfp4_fused(*wq, flat[1:].view(m, k), n, k, y=y[1:-1].view(m, n))
+        check_equal(acts_host_f32(y[1:-1].view(m, n)), acts_host_f32(want), "y")
+        assert (y[[0, -1]] == 777.0).all()
