@@ -198,7 +198,7 @@ def _codes(x):
     """int8 codes [M][K_pad] and scales [M] of x: codes round(x * fl32(127 / a)), ties to even, a = max |x|."""
     x = x.float()
     a = x.abs().amax(1)
-    s = torch.where(a > 0, 127.0 / a, 0.0)
+    s = torch.where(a > 0, torch.full_like(a, 127.0) / a, 0.0)  # (127.0 / a rounds twice: a reciprocal, a product)
     q = torch.round(x * s[:, None]).clamp(-127, 127).to(torch.int8)
     return torch.nn.functional.pad(q, (0, -x.shape[1] % 256)), a
 
