@@ -14,7 +14,9 @@ building block") and the 2-bit code table of bhfrc.com news 56965, section 4.1.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+from typing import NamedTuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libbitlinear.so")
@@ -130,6 +132,21 @@ def lib() -> ctypes.CDLL:
         L.bitlinear_layernorm.argtypes = [p, c_int, i64, i64, p, p, f32, p, p, p, p]
         L.bitlinear_layernorm_backward.restype = c_int
         L.bitlinear_layernorm_backward.argtypes = [p, p, c_int, i64, i64, p, p, p, p, p, p, p, i64, p]
+        for name in ("bitlinear_forward_experts_combine_ws_bytes", "bitlinear_route_experts_ws_bytes"):
+            getattr(L, name).restype = i64
+            getattr(L, name).argtypes = [i64, i64]
+        L.bitlinear_forward_epilogue.restype = c_int
+        L.bitlinear_forward_epilogue.argtypes = [p, p, p, c_int, p, p, i64, i64, i64, p, p]
+        L.bitlinear_forward_epilogue_plan.restype = c_int
+        L.bitlinear_forward_epilogue_plan.argtypes = [i64, i64, i64, c_int, p]
+        L.bitlinear_forward_experts.restype = c_int
+        L.bitlinear_forward_experts.argtypes = [p, p, c_int, p, p, i64, i64, p, p]
+        L.bitlinear_forward_experts_plan.restype = c_int
+        L.bitlinear_forward_experts_plan.argtypes = [i64, i64, i64, i64, c_int, p]
+        L.bitlinear_forward_experts_combine.restype = c_int
+        L.bitlinear_forward_experts_combine.argtypes = [p, p, c_int, p, p, i64, i64, p, p, i64, i64, p, p, i64, p]
+        L.bitlinear_route_experts.restype = c_int
+        L.bitlinear_route_experts.argtypes = [p, c_int, i64, i64, i64, c_int, p, p, p, p, p, p, i64, p]
         _lib = L
     return _lib
 
@@ -150,6 +167,9 @@ EXPORTED_SYMBOLS = (
     "bitlinear_mxfp4_scales_bytes", "bitlinear_quantize_mxfp4", "bitlinear_forward_mxfp4",
     "bitlinear_forward_mxfp4_fused_ws_bytes", "bitlinear_forward_mxfp4_fused", "bitlinear_layernorm",
     "bitlinear_layernorm_backward_ws_bytes", "bitlinear_layernorm_backward", "bitlinear_forward_mxfp4_plan",
+    "bitlinear_forward_epilogue", "bitlinear_forward_epilogue_plan", "bitlinear_forward_experts",
+    "bitlinear_forward_experts_plan", "bitlinear_forward_experts_combine",
+    "bitlinear_forward_experts_combine_ws_bytes", "bitlinear_route_experts", "bitlinear_route_experts_ws_bytes",
 )
 
 MAX_GROUP = 8
@@ -159,6 +179,19 @@ class BlMatrix(ctypes.Structure):
     """bl_matrix of bitlinear.h: one weight matrix of a grouped call."""
     _fields_ = [("packed", ctypes.c_void_p), ("gamma", ctypes.c_void_p), ("N", ctypes.c_int64),
                 ("Y", ctypes.c_void_p), ("acc", ctypes.c_void_p)]
+
+
+class BlEpilogue(ctypes.Structure):
+    """bl_epilogue of bitlinear.h: bias, activation and residual of a product, and its output."""
+    _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("Y", ctypes.c_void_p),
+                ("residual_ld", ctypes.c_int64), ("y_ld", ctypes.c_int64), ("act", ctypes.c_int),
+                ("residual_dt", ctypes.c_int), ("y_dt", ctypes.c_int)]
+
+
+class BlExperts(ctypes.Structure):
+    """bl_experts of bitlinear.h: the matrices of a layer with experts, and their slots."""
+    _fields_ = [("packed", ctypes.c_void_p), ("gamma", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
+                ("rows", ctypes.c_void_p), ("E", ctypes.c_int64), ("T", ctypes.c_int64), ("N", ctypes.c_int64)]
 
 
 def _check(fn: str, status: int) -> None:
@@ -933,6 +966,11 @@ class _Runtime:
         self.layernorm = L.bitlinear_layernorm
         self.layernorm_backward = L.bitlinear_layernorm_backward
         self.backward_ws_bytes = L.bitlinear_layernorm_backward_ws_bytes
+        self.i8, self.i32 = torch.int8, torch.int32
+        self.forward_epilogue = L.bitlinear_forward_epilogue
+        self.forward_experts = L.bitlinear_forward_experts
+        self.forward_experts_combine = L.bitlinear_forward_experts_combine
+        self.route_experts = L.bitlinear_route_experts
 
 
 _RT = None
@@ -1168,3 +1206,235 @@ def layernorm_backward(dy, x, weight, mean, rstd, dx=None, dweight=None, dbias=N
           (dy.data_ptr(), x.data_ptr(), dt, m, k, _ptr(weight), mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(),
            _ptr(dweight), _ptr(dbias), _ptr(workspace), workspace.numel() if workspace is not None else 0))
     return (dx, dweight, dbias) if want_params else dx
+
+
+ACTIVATIONS = {"none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu": 4, "gelu_tanh": 5}
+
+
+@functools.lru_cache(maxsize=4096)
+def _products_plan(e: int, t: int, n: int, k: int, xdt: int):
+    """out[0..5] of the plan calls (e = 0: one matrix); the rule goes by sizes and types alone."""
+    out = (ctypes.c_int32 * 6)()
+    if e:
+        _check("bitlinear_forward_experts_plan", lib().bitlinear_forward_experts_plan(e, t, n, k, xdt, out))
+    else:
+        _check("bitlinear_forward_epilogue_plan", lib().bitlinear_forward_epilogue_plan(t, n, k, xdt, out))
+    return tuple(out)
+
+
+def _products_plan_dict(e: int, t: int, n: int, k: int, x) -> dict:
+    out = _products_plan(e, t, n, k, -1 if x is None else _named_dtype(x))
+    return {"kernel": {10: "plain"}[out[0]], "workgroups": out[1], "threads": out[2], "rows": out[3],
+            "outputs": out[4], "launches": out[5]}
+
+
+def forward_epilogue_plan(m: int, n: int, k: int, x=None) -> dict:
+    """The launches of forward_epilogue for (M, N, K) and an x of int8 codes (``x`` None), "bf16" or
+    "f32", computed on the host."""
+    return _products_plan_dict(0, m, n, k, x)
+
+
+def forward_experts_plan(e: int, t: int, n: int, k: int, x=None) -> dict:
+    """The launches of forward_experts for E experts and T slots, as forward_epilogue_plan."""
+    if e < 1:
+        raise ValueError("at least one expert")
+    return _products_plan_dict(e, t, n, k, x)
+
+
+def _strided(rt, t, name: str, rows: int, n: int, index: int):
+    """(bl_dtype, row distance) of a [rows][n] matrix on the device whose rows are contiguous."""
+    if t.get_device() != index or t.shape != (rows, n) or (n > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a [{rows}, {n}] tensor with contiguous rows on cuda:{index}")
+    ld = t.stride(0) if rows > 1 else n
+    if ld < n:
+        raise ValueError(f"{name} must not have rows that overlap")
+    return _dtype_code(rt, t.dtype, name), ld
+
+
+def _vector(rt, t, name: str, shape, dtype, index: int) -> int:
+    """The address of a contiguous tensor of this shape and type on the device."""
+    if t.get_device() != index or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}")
+    return t.data_ptr()
+
+
+def _tokens(rt, x, k: int, absmax, e: int, t, n: int):
+    """The token rows x: (address of x or None, its bl_dtype, codes, scales, rows, what has to stay alive)."""
+    dev = x.get_device()
+    if x.dtype == rt.i8:
+        if dev < 0 or x.dim() != 2 or not x.is_contiguous() or not x.numel() or x.shape[1] != (k + 255) // 256 * 256:
+            raise ValueError("codes must be a non-empty contiguous [tokens, K_pad] GPU tensor")
+        if absmax is None:
+            raise ValueError("codes need their scales, absmax")
+        r = x.shape[0]
+        return None, 0, x.data_ptr(), _vector(rt, absmax, "absmax", (r,), rt.f32, dev), r, None
+    if absmax is not None:
+        raise ValueError("absmax goes with int8 codes")
+    dt = _require_rows(rt, x, "x")
+    r, cols = x.shape
+    if cols != k:
+        raise ValueError("x must be [tokens, K]")
+    if n < 1 or _products_plan(e, r if t is None else t, n, k, dt)[5] == 1:
+        return x.data_ptr(), dt, None, None, r, None
+    xq = rt.empty(r, (k + 255) // 256 * 256, dtype=rt.i8, device=x.device)
+    a = rt.empty(r, dtype=rt.f32, device=x.device)
+    return x.data_ptr(), dt, xq.data_ptr(), a.data_ptr(), r, (xq, a)
+
+
+def _epilogue(rt, y, out_dtype, rows: int, n: int, like, bias, bias_shape, act: str, residual):
+    """(y, its bl_epilogue)."""
+    dev = like.get_device()
+    if y is None:
+        y = rt.empty(rows, max(n, 0), dtype=out_dtype or rt.f32, device=like.device)
+    elif out_dtype is not None and y.dtype != out_dtype:
+        raise ValueError(f"y must be {out_dtype}")
+    ydt, yld = _strided(rt, y, "y", rows, n, dev)
+    rdt, rld, rptr = 0, 0, None
+    if residual is not None:
+        rdt, rld = _strided(rt, residual, "residual", rows, n, dev)
+        rptr = residual.data_ptr()
+    code = ACTIVATIONS.get(act)
+    if code is None:
+        raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}, not {act!r}")
+    bptr = _vector(rt, bias, "bias", bias_shape, rt.f32, dev) if bias is not None else None
+    return y, BlEpilogue(bptr, rptr, y.data_ptr(), rld, yld, code, rdt, ydt)
+
+
+def forward_epilogue(packed, gamma, x, n: int, k: int, absmax=None, bias=None, act: str = "none", residual=None,
+                     y=None, out_dtype=None):
+    """y[M][N] = act(x W^T + bias) + residual in one call, for weights from quantize_weights.
+
+    x: [M][K] fp32 or bf16, or the int8 codes [M][K_pad] with their scales ``absmax`` (quantize_acts).
+    bias: fp32 [N].  act: a name of ``ACTIVATIONS``.  residual: [M][N] fp32 or bf16; it may be ``y``
+    itself.  y: [M][N] in ``out_dtype`` (fp32, or bf16), or the given tensor; rows of y and residual
+    may be parts of longer ones."""
+    rt = _RT or _runtime()
+    dev = x.get_device()
+    wp = _bytes_at_least(rt, packed, "packed", (n + 15) // 16 * 4 * ((k + 255) // 256 * 256), dev)
+    gp = _vector(rt, gamma, "gamma", (1,), rt.f32, dev)
+    xp, dt, xq, a, m, keep = _tokens(rt, x, k, absmax, 0, None, n)
+    y, ep = _epilogue(rt, y, out_dtype, m, n, x, bias, (n,), act, residual)
+    _call(rt, rt.forward_epilogue, dev, (wp, gp, xp, dt, xq, a, m, n, k, ctypes.byref(ep)))
+    return y
+
+
+def _experts(rt, packed, gamma, offsets, rows, t: int, n: int, k: int, dev: int) -> BlExperts:
+    e = gamma.shape[0] if gamma.dim() == 1 else 0
+    if e < 1:
+        raise ValueError("gamma must hold a scale per expert")
+    wp = _bytes_at_least(rt, packed, "packed", e * ((n + 15) // 16 * 4 * ((k + 255) // 256 * 256)), dev)
+    return BlExperts(wp, _vector(rt, gamma, "gamma", (e,), rt.f32, dev),
+                     _vector(rt, offsets, "offsets", (e + 1,), rt.i32, dev),
+                     _vector(rt, rows, "rows", (t,), rt.i32, dev) if rows is not None else None, e, t, n)
+
+
+def quantize_expert_weights(W):
+    """Ternary weights of E experts, W[E][N][K] fp32 on the GPU, each with its own scale: (packed uint8
+    [E][packed_bytes], gamma fp32 [E])."""
+    import torch
+
+    _require_cuda(W, "W")
+    if W.dim() != 3 or not W.numel():
+        raise ValueError("W must be a non-empty [experts, N, K] tensor")
+    e, n, k = W.shape
+    packed = torch.empty((e, packed_bytes(n, k)), dtype=torch.uint8, device=W.device)
+    gamma = torch.empty(e, dtype=torch.float32, device=W.device)
+    workspace = torch.empty(wq_workspace_bytes(n, k), dtype=torch.uint8, device=W.device)
+    for i in range(e):
+        quantize_weights(W[i], packed[i], gamma[i:i + 1], workspace)
+    return packed, gamma
+
+
+def forward_experts(packed, gamma, offsets, x, n: int, k: int, rows=None, absmax=None, bias=None, act: str = "none",
+                    residual=None, y=None, out_dtype=None):
+    """Products grouped by expert: slot s of expert e (offsets[e] <= s < offsets[e + 1]) is token row
+    rows[s] of x (row s without ``rows``) through matrix e; y[T][N] has a row per slot, with act, bias
+    ([E][N]) and residual ([T][N]) as forward_epilogue.  Rows of slots without an expert, or with a row
+    that x does not have, stay as they were.
+
+    packed, gamma: quantize_expert_weights.  offsets, rows: int32 tables of route_experts."""
+    rt = _RT or _runtime()
+    dev = x.get_device()
+    t = rows.shape[0] if rows is not None else x.shape[0]
+    ex = _experts(rt, packed, gamma, offsets, rows, t, n, k, dev)
+    xp, dt, xq, a, r, keep = _tokens(rt, x, k, absmax, ex.E, t, n)
+    y, ep = _epilogue(rt, y, out_dtype, t, n, x, bias, (ex.E, n), act, residual)
+    _call(rt, rt.forward_experts, dev, (ctypes.byref(ex), xp, dt, xq, a, r, k, ctypes.byref(ep)))
+    return y
+
+
+def forward_experts_combine_ws_bytes(t: int, n: int) -> int:
+    """Workspace bytes of forward_experts_combine for T slots of N outputs."""
+    v = int(lib().bitlinear_forward_experts_combine_ws_bytes(t, n))
+    if v < 0:
+        raise ValueError(f"invalid shape {(t, n)}")
+    return v
+
+
+def forward_experts_combine(packed, gamma, offsets, x, n: int, k: int, slots, weights, rows=None, absmax=None,
+                            bias=None, act: str = "none", residual=None, y=None, out_dtype=None, workspace=None):
+    """forward_experts with the slots of each token added up: y[m] = residual[m] + sum_j weights[m][j]
+    act(...) at slot slots[m][j] (-1: none).  slots int32 and weights fp32 [M][k] of route_experts."""
+    rt = _RT or _runtime()
+    dev = x.get_device()
+    t = rows.shape[0] if rows is not None else x.shape[0]
+    ex = _experts(rt, packed, gamma, offsets, rows, t, n, k, dev)
+    if slots.dim() != 2 or not slots.numel():
+        raise ValueError("slots must be a non-empty [tokens, choices] tensor")
+    m, top = slots.shape
+    sp = _vector(rt, slots, "slots", (m, top), rt.i32, dev)
+    wt = _vector(rt, weights, "weights", (m, top), rt.f32, dev)
+    xp, dt, xq, a, r, keep = _tokens(rt, x, k, absmax, ex.E, t, n)
+    y, ep = _epilogue(rt, y, out_dtype, m, n, x, bias, (ex.E, n), act, residual)
+    need = forward_experts_combine_ws_bytes(t, n)
+    if workspace is None:
+        workspace = rt.empty(need, dtype=rt.u8, device=x.device)
+    ws = _bytes_at_least(rt, workspace, "workspace", need, dev)
+    _call(rt, rt.forward_experts_combine, dev, (ctypes.byref(ex), xp, dt, xq, a, r, k, sp, wt, m, top,
+                                                ctypes.byref(ep), ws, workspace.numel()))
+    return y
+
+
+class Route(NamedTuple):
+    """What route_experts chose: experts and weights [M][k], and the slots by expert, then token:
+    offsets [E + 1], rows [M k] (the token of each slot) and slots [M][k] (the slot of each choice)."""
+    experts: object
+    weights: object
+    offsets: object
+    rows: object
+    slots: object
+
+
+def route_experts_ws_bytes(m: int, e: int) -> int:
+    """Workspace bytes of route_experts for M tokens and E experts (0: none)."""
+    v = int(lib().bitlinear_route_experts_ws_bytes(m, e))
+    if v < 0:
+        raise ValueError(f"invalid shape {(m, e)}")
+    return v
+
+
+def route_experts(logits, k: int, renormalize: bool = True, out: Route = None, workspace=None) -> Route:
+    """The k largest of each token's logits[M][E] (fp32 or bf16; equal ones: the lowest index first),
+    their weights (softmax over the chosen ones, or over all E without ``renormalize``), and the slots
+    that forward_experts takes.  -inf and NaN are never chosen; missing choices are -1 with weight 0."""
+    rt = _RT or _runtime()
+    dt = _require_rows(rt, logits, "logits")
+    m, e = logits.shape
+    dev = logits.get_device()
+    if out is None:
+        if not 0 < k <= e:
+            raise ValueError(f"k must be 1 .. {e}")
+        new = functools.partial(rt.empty, device=logits.device)
+        out = Route(new(m, k, dtype=rt.i32), new(m, k, dtype=rt.f32), new(e + 1, dtype=rt.i32),
+                    new(m * k, dtype=rt.i32), new(m, k, dtype=rt.i32))
+    ptrs = (_vector(rt, out.experts, "experts", (m, k), rt.i32, dev), _vector(rt, out.weights, "weights", (m, k), rt.f32, dev),
+            _vector(rt, out.offsets, "offsets", (e + 1,), rt.i32, dev), _vector(rt, out.rows, "rows", (m * k,), rt.i32, dev),
+            _vector(rt, out.slots, "slots", (m, k), rt.i32, dev))
+    need = route_experts_ws_bytes(m, e)
+    if workspace is not None:
+        _bytes_at_least(rt, workspace, "workspace", need, dev)
+    elif need > 0:
+        workspace = rt.empty(need, dtype=rt.u8, device=logits.device)
+    _call(rt, rt.route_experts, dev, (logits.data_ptr(), dt, m, e, k, int(bool(renormalize)), *ptrs, _ptr(workspace),
+                                      workspace.numel() if workspace is not None else 0))
+    return out

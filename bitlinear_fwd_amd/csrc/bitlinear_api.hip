@@ -5,6 +5,7 @@
 #include "bl_internal.h"
 #include "gemv_lut.h"
 #include "binary.h"
+#include "experts.h"
 #include "layernorm.h"
 #include "mxfp4.h"
 
@@ -43,6 +44,89 @@ hipError_t mx_forward(const uint8_t* codes, const uint8_t* scales, const uint8_t
 // Sizes of an MXFP4 product: both matrices addressable, and a launchable number of output tiles.
 bool mx_product_ok(int64_t M, int64_t N, int64_t K) {
   return M <= kMaxCount / K && N <= kMaxCount / K && (M + 127) / 128 <= (int64_t(1) << 23) / ((N + 127) / 128);
+}
+
+// Products with an epilogue.  K and the rows of tokens or slots as rows_ok.
+constexpr int64_t kMaxExperts = 4096;
+constexpr int64_t kMaxCombined = 64;  // slots of one token
+
+// ep for outputs of N columns, checked and turned into the kernels' form.
+int epilogue_of(const bl_epilogue* ep, int64_t N, bl::Epilogue* out) {
+  if (!ep || !ep->Y || ep->act < BL_ACT_NONE || ep->act > BL_ACT_GELU_TANH) return BL_ERR_INVALID_ARG;
+  if (!dtype_ok(ep->y_dt) || (ep->residual && !dtype_ok(ep->residual_dt))) return BL_ERR_UNSUPPORTED;
+  out->ldy = ep->y_ld ? ep->y_ld : N;
+  out->ldr = ep->residual_ld ? ep->residual_ld : N;
+  if (out->ldy < N || out->ldr < N || out->ldy > kMaxCount || out->ldr > kMaxCount) return BL_ERR_INVALID_ARG;
+  if (!aligned(ep->bias, 4) || !aligned(ep->Y, dtype_align(ep->y_dt)) ||
+      (ep->residual && !aligned(ep->residual, dtype_align(ep->residual_dt))))
+    return BL_ERR_INVALID_ARG;
+  out->bias = ep->bias;
+  out->residual = ep->residual;
+  out->Y = ep->Y;
+  out->act = ep->act;
+  out->res_bf16 = ep->residual && ep->residual_dt == BL_BF16;
+  out->y_bf16 = ep->y_dt == BL_BF16;
+  return BL_OK;
+}
+
+// A launch can be counted: units of 16 slots by 64 outputs in 31 bits, matrices in 40 bits of bytes.
+bool products_countable(int64_t E, int64_t T, int64_t N, int64_t K) {
+  if (E > kMaxExperts || bl::n_pad(N) > kMaxCount / bl::k_pad(K) / E) return false;
+  return T / 16 + 1 + (E < T ? E : T) <= (kMaxDim - 1) / ((N + 63) / 64);
+}
+
+// The operands of g (its R rows of codes, or of X), checked.
+int products_ok(const bl::Groups& g, const void* X, int dt, const int8_t* Xq, const float* absmax) {
+  if (!g.packed || !g.gamma || !rows_ok(g.T, g.K) || !rows_ok(g.R, g.K) || !rows_ok(g.N, g.K) || g.E < 1)
+    return BL_ERR_INVALID_ARG;
+  if (!aligned(g.packed, 16) || !aligned(g.gamma, 4) || !aligned(g.offsets, 4) || !aligned(g.rows, 4))
+    return BL_ERR_INVALID_ARG;
+  if (!X && (!Xq || !absmax)) return BL_ERR_INVALID_ARG;
+  if (!aligned(Xq, 16) || !aligned(absmax, 4)) return BL_ERR_INVALID_ARG;
+  if (X && !dtype_ok(dt)) return BL_ERR_UNSUPPORTED;
+  if (X && !aligned(X, dtype_align(dt))) return BL_ERR_INVALID_ARG;
+  if (!products_countable(g.E, g.T, g.N, g.K)) return BL_ERR_UNSUPPORTED;
+  if (g.R > kMaxCount / g.K) return BL_ERR_UNSUPPORTED;
+  return BL_OK;
+}
+
+// The products, behind the quantiser where X is given and the kernel does not take it itself.
+int products(const bl::Groups& g, const void* X, int dt, int8_t* Xq, float* absmax, const bl::Epilogue& ep,
+             hipStream_t s) {
+  int src = X ? mx_src(dt) : 0;
+  if (X && !bl::plan_experts(g.offsets ? g.E : 0, g.T, g.N, g.K, src).quantizes) {
+    if (!Xq || !absmax) return BL_ERR_INVALID_ARG;
+    const hipError_t e = bl::launch_act_quant(X, dt == BL_BF16, g.R, g.K, Xq, absmax, s);
+    if (e != hipSuccess) return BL_ERR_HIP;
+    src = 0;
+  }
+  return hip_status(bl::launch_experts(g, X, src, Xq, absmax, ep, s));
+}
+
+int products_plan(int64_t E, int64_t T, int64_t N, int64_t K, int xdt, int32_t out[6]) {
+  if (!out || !rows_ok(T, K) || !rows_ok(N, K)) return BL_ERR_INVALID_ARG;
+  if (xdt != -1 && !dtype_ok(xdt)) return BL_ERR_UNSUPPORTED;
+  if (!products_countable(E ? E : 1, T, N, K)) return BL_ERR_UNSUPPORTED;
+  bl::ExpertsPlan p = bl::plan_experts(E, T, N, K, xdt == -1 ? 0 : mx_src(xdt));
+  const bool one = xdt == -1 || p.quantizes;
+  if (!one) p = bl::plan_experts(E, T, N, K, 0);
+  out[0] = p.kernel, out[1] = (int32_t)p.groups, out[2] = p.threads, out[3] = p.height, out[4] = p.width;
+  out[5] = one ? 1 : 2;
+  return BL_OK;
+}
+
+bl::Groups groups_of(const bl_experts* x, int64_t R, int64_t K) {
+  bl::Groups g;
+  g.packed = x->packed;
+  g.gamma = x->gamma;
+  g.offsets = x->offsets;
+  g.rows = x->rows;
+  g.E = x->E < 1 ? 0 : x->E > kMaxExperts ? (int)kMaxExperts + 1 : (int)x->E;
+  g.T = x->T;
+  g.N = x->N;
+  g.R = R;
+  g.K = K;
+  return g;
 }
 
 int grouped_impl(const bl_matrix* mats, int count, const void* X, int dt, int64_t M, int64_t K, const float* gain,
@@ -217,6 +301,85 @@ int bitlinear_forward_mxfp4_fused(const uint8_t* codes, const uint8_t* scales, c
   const hipError_t e = bl::launch_mx_quant(X, dt == BL_BF16, M, K, xcodes, xscales, nullptr, s);
   if (e != hipSuccess) return BL_ERR_HIP;
   return hip_status(mx_forward(codes, scales, xcodes, xscales, M, N, K, Y, ydt, s));
+}
+
+int bitlinear_forward_epilogue(const uint8_t* packed, const float* gamma, const void* X, int dt, int8_t* Xq,
+                               float* absmax, int64_t M, int64_t N, int64_t K, const bl_epilogue* ep, void* stream) {
+  const bl_experts one = {packed, gamma, nullptr, nullptr, 1, M, N};
+  const bl::Groups g = groups_of(&one, M, K);
+  bl::Epilogue e;
+  int st = products_ok(g, X, dt, Xq, absmax);
+  if (st == BL_OK) st = epilogue_of(ep, N, &e);
+  return st == BL_OK ? products(g, X, dt, Xq, absmax, e, static_cast<hipStream_t>(stream)) : st;
+}
+
+int bitlinear_forward_epilogue_plan(int64_t M, int64_t N, int64_t K, int xdt, int32_t out[6]) {
+  return products_plan(0, M, N, K, xdt, out);
+}
+
+int bitlinear_forward_experts_plan(int64_t E, int64_t T, int64_t N, int64_t K, int xdt, int32_t out[6]) {
+  return E < 1 ? BL_ERR_INVALID_ARG : products_plan(E, T, N, K, xdt, out);
+}
+
+int bitlinear_forward_experts(const bl_experts* experts, const void* X, int dt, int8_t* Xq, float* absmax, int64_t R,
+                              int64_t K, const bl_epilogue* ep, void* stream) {
+  if (!experts || !experts->offsets) return BL_ERR_INVALID_ARG;
+  const bl::Groups g = groups_of(experts, R, K);
+  bl::Epilogue e;
+  int st = products_ok(g, X, dt, Xq, absmax);
+  if (st == BL_OK) st = epilogue_of(ep, g.N, &e);
+  return st == BL_OK ? products(g, X, dt, Xq, absmax, e, static_cast<hipStream_t>(stream)) : st;
+}
+
+int64_t bitlinear_forward_experts_combine_ws_bytes(int64_t T, int64_t N) {
+  return T < 1 || N < 1 || T >= kMaxDim || N >= kMaxDim || T > kMaxCount / N ? -1 : T * N * 4;
+}
+
+int bitlinear_forward_experts_combine(const bl_experts* experts, const void* X, int dt, int8_t* Xq, float* absmax,
+                                      int64_t R, int64_t K, const int32_t* slots, const float* weights, int64_t M,
+                                      int64_t k, const bl_epilogue* ep, void* workspace, int64_t ws_bytes,
+                                      void* stream) {
+  if (!experts || !experts->offsets || !slots || !weights || M < 1 || M >= kMaxDim || k < 1) return BL_ERR_INVALID_ARG;
+  const bl::Groups g = groups_of(experts, R, K);
+  bl::Epilogue e, out;
+  int st = products_ok(g, X, dt, Xq, absmax);
+  if (st == BL_OK) st = epilogue_of(ep, g.N, &out);
+  if (st != BL_OK) return st;
+  if (k > kMaxCombined || M > (kMaxDim - 1) * 256 / ((g.N + 3) / 4)) return BL_ERR_UNSUPPORTED;
+  const int64_t need = bitlinear_forward_experts_combine_ws_bytes(g.T, g.N);
+  if (need < 0) return BL_ERR_UNSUPPORTED;
+  if (!aligned(slots, 4) || !aligned(weights, 4) || !workspace || !aligned(workspace, 16) || ws_bytes < need)
+    return BL_ERR_INVALID_ARG;
+  e = out;  // the slots' own: fp32 rows in the workspace, the residual comes with the sum
+  e.residual = nullptr;
+  e.Y = workspace;
+  e.ldy = g.N;
+  e.y_bf16 = 0;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  st = products(g, X, dt, Xq, absmax, e, s);
+  if (st != BL_OK) return st;
+  return hip_status(bl::launch_combine(g, static_cast<const float*>(workspace), slots, weights, M, (int)k, out, s));
+}
+
+int64_t bitlinear_route_experts_ws_bytes(int64_t M, int64_t E) {
+  return M < 1 || E < 1 || M >= kMaxDim || E >= kMaxDim ? -1 : bl::plan_route(M, E).ws_bytes;
+}
+
+int bitlinear_route_experts(const void* logits, int dt, int64_t M, int64_t E, int64_t k, int renormalize,
+                            int32_t* experts, float* weights, int32_t* offsets, int32_t* rows, int32_t* slots,
+                            void* workspace, int64_t ws_bytes, void* stream) {
+  if (!logits || !experts || !weights || !offsets || !rows || !slots || M < 1 || E < 1 || k < 1 || M >= kMaxDim ||
+      E >= kMaxDim || k > E || (renormalize != 0 && renormalize != 1))
+    return BL_ERR_INVALID_ARG;
+  if (!dtype_ok(dt) || E > bl::kMaxRouteExperts || k > bl::kMaxRouteChoices || M > (kMaxDim - 1) / k)
+    return BL_ERR_UNSUPPORTED;
+  const int64_t need = bl::plan_route(M, E).ws_bytes;
+  if (!aligned(logits, dtype_align(dt)) || !aligned(experts, 4) || !aligned(weights, 4) || !aligned(offsets, 4) ||
+      !aligned(rows, 4) || !aligned(slots, 4) || !aligned(workspace, 4) || (need > 0 && (!workspace || ws_bytes < need)))
+    return BL_ERR_INVALID_ARG;
+  const bl::RouteArgs a = {logits,  dt == BL_BF16, renormalize, M,     (int)E, (int)k,
+                           experts, weights,       offsets,     rows, slots,  static_cast<int32_t*>(workspace)};
+  return hip_status(bl::launch_route(a, static_cast<hipStream_t>(stream)));
 }
 
 int bitlinear_layernorm(const void* X, int dt, int64_t M, int64_t K, const float* weight, const float* bias,

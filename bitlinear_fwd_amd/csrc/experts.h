@@ -1,0 +1,223 @@
+// Ternary products with an epilogue, for one matrix or for a matrix per expert, and the router in front
+// of them: arguments, device helpers and launchers shared by the kernels.
+//
+// A product's rows are slots: slot s of group e (offsets[e] <= s < offsets[e + 1]) multiplies token row
+// rows[s] of the int8 codes by matrix e.  One matrix is the case of one group that holds all rows.
+#pragma once
+#include "bl_internal.h"
+#include "mxfp4.h"  // bf16_pair, load8, uniform_ptr, v4f
+
+namespace bl {
+
+// What happens to a product on its way out (a host struct of the C ABI, checked there).
+struct Epilogue {
+  const float* bias;     // [N], or [E][N] where there are experts; null: none
+  const void* residual;  // null: none.  May be Y itself, so neither pointer is __restrict__
+  void* Y;
+  int64_t ldr, ldy;      // elements between rows
+  int act;               // bl_activation
+  int res_bf16, y_bf16;
+};
+
+// The matrices and which rows each of them takes.
+struct Groups {
+  const uint8_t* packed;  // [E][n_pad k_pad / 4]
+  const float* gamma;     // [E]
+  const int32_t* offsets; // [E + 1], null: one group with the slots 0 .. T - 1
+  const int32_t* rows;    // [T], null: slot s takes row s
+  int E;
+  int64_t T, R;           // slots; rows of the codes
+  int64_t N, K;
+};
+
+// Slots of group e, kept within 0 .. T whatever the offsets hold.
+__device__ __forceinline__ int2 group_slots(const Groups& g, int e) {
+  if (!g.offsets) return make_int2(0, (int)g.T);
+  const int lo = max(0, min(g.offsets[e], (int)g.T));
+  return make_int2(lo, max(lo, min(g.offsets[e + 1], (int)g.T)));
+}
+
+// Token row of slot s, -1 for a slot without one.
+__device__ __forceinline__ int slot_row(const Groups& g, int s) {
+  const int r = g.rows ? g.rows[s] : s;
+  return (uint32_t)r < (uint32_t)g.R ? r : -1;
+}
+
+// Work is dealt in units of up to `height` consecutive slots of one group; the units of all groups are
+// numbered in order.  find_unit gives unit u's group and slots (lo >= hi: there is no such unit).
+// Every lane of the wave calls it with the same u; 64 groups are looked at together.
+struct Unit {
+  int e, lo, hi;
+};
+__device__ __forceinline__ Unit find_unit(const Groups& g, int height, int u) {
+  if (!g.offsets) {
+    const int64_t lo = (int64_t)u * height;
+    if (lo >= g.T) return Unit{0, 0, 0};
+    return Unit{0, (int)lo, (int)min(lo + height, g.T)};
+  }
+  const int lane = threadIdx.x & 63;
+  for (int e0 = 0; e0 < g.E; e0 += 64) {
+    int2 s = make_int2(0, 0);
+    if (e0 + lane < g.E) s = group_slots(g, e0 + lane);
+    const int mine = (s.y - s.x + height - 1) / height;
+    int incl = mine;  // units of this and the groups before it
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(incl, d, 64);
+      if (lane >= d) incl += v;
+    }
+    const uint64_t after = __ballot(incl > u);
+    if (after) {
+      const int l = __builtin_ctzll(after);
+      const int first = __builtin_amdgcn_readlane(incl - mine, l);
+      const int slo = __builtin_amdgcn_readlane(s.x, l), shi = __builtin_amdgcn_readlane(s.y, l);
+      const int lo = slo + (u - first) * height;
+      return Unit{e0 + l, lo, min(lo + height, shi)};
+    }
+    u -= __builtin_amdgcn_readlane(incl, 63);
+  }
+  return Unit{0, 0, 0};
+}
+
+// A launch cannot have more units than this (groups with slots have at most one unit that is not full).
+inline int64_t most_units(int64_t E, int64_t T, int height) { return T / height + (E < T ? E : T); }
+
+// e^-x / (1 + e^-x) and the like need e^x only to a few units in the last place: 2^(x log2 e) with the
+// product's rounding error put back.  x is kept in -104 .. 87: below, e^x is nothing in fp32, and above
+// nothing overflows.
+__device__ __forceinline__ float exp_of(float x) {
+  constexpr float kLog2e = 1.44269502e+00f, kLog2eLow = 1.92596303e-08f, kLn2 = 6.93147182e-01f;
+  x = __builtin_amdgcn_fmed3f(x, -104.0f, 87.0f);
+  const float t = x * kLog2e;
+  const float low = __builtin_fmaf(x, kLog2eLow, __builtin_fmaf(x, kLog2e, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(e, low * kLn2, e);
+}
+__device__ __forceinline__ float sigmoid_of(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_of(-x)); }
+
+// The activations of bl_activation, in fp32.
+__device__ __forceinline__ float activate(float v, int act) {
+  switch (act) {
+    case 1: return fmaxf(v, 0.0f);
+    case 2: {
+      const float r = fmaxf(v, 0.0f);
+      return r * r;
+    }
+    case 3: return v * sigmoid_of(v);
+    case 4: return 0.5f * v * (1.0f + erff(v * 0.70710678f));
+    case 5:  // (1 + tanh u) / 2 = sigmoid(2 u)
+      return v * sigmoid_of(1.59576912f * __builtin_fmaf(0.044715f * v * v, v, v));
+    default: return v;
+  }
+}
+
+__device__ __forceinline__ float bf16_float(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+
+// Four consecutive values of row p, those of columns before the end (left of them; the others 0).
+__device__ __forceinline__ v4f load4(const void* base, int64_t at, int left, int bf16) {
+  v4f r = {0, 0, 0, 0};
+  if (bf16) {
+    const uint16_t* p = static_cast<const uint16_t*>(base) + at;
+    uint16_t h[4] = {0, 0, 0, 0};
+    if (left >= 4) {
+      __builtin_memcpy(h, p, 8);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 3; ++q)
+        if (q < left) h[q] = p[q];
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) r[q] = bf16_float(h[q]);
+  } else {
+    const float* p = static_cast<const float*>(base) + at;
+    if (left >= 4) {
+      __builtin_memcpy(&r, p, 16);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 3; ++q)
+        if (q < left) r[q] = p[q];
+    }
+  }
+  return r;
+}
+__device__ __forceinline__ void store4(void* base, int64_t at, int left, int bf16, v4f v) {
+  if (bf16) {
+    uint16_t* p = static_cast<uint16_t*>(base) + at;
+    if (left >= 4) {
+      const uint32_t w[2] = {bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+      __builtin_memcpy(p, w, 8);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 3; ++q)
+        if (q < left) p[q] = bf16_bits(v[q]);
+    }
+  } else {
+    float* p = static_cast<float*>(base) + at;
+    if (left >= 4) {
+      __builtin_memcpy(p, &v, 16);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 3; ++q)
+        if (q < left) p[q] = v[q];
+    }
+  }
+}
+
+// A token's scale: the exact products are multiplied by gamma a / 127.
+__device__ __forceinline__ float token_scale(float gamma, float a) { return gamma * a / 127.0f; }
+
+// The epilogue of four consecutive outputs n .. n + 3 of slot s (left of them before column N).
+__device__ __forceinline__ void finish4(const Epilogue& ep, int64_t e, int64_t N, int64_t s, int64_t n, int left, v4i acc,
+                                        float scale) {
+  v4f b = {0, 0, 0, 0}, v;
+  if (ep.bias) b = load4(ep.bias, e * N + n, left, 0);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) v[q] = activate(__builtin_fmaf((float)acc[q], scale, b[q]), ep.act);
+  if (ep.residual) v += load4(ep.residual, s * ep.ldr + n, left, ep.res_bf16);
+  store4(ep.Y, s * ep.ldy + n, left, ep.y_bf16, v);
+}
+
+// How the products of T slots of E matrices (E = 0: one matrix, no tables) are computed.
+enum { kPlainKernel = 10 };
+struct ExpertsPlan {
+  int kernel = kPlainKernel;
+  int threads = 256;
+  int64_t groups = 0;         // workgroups
+  int height = 16, width = 64;  // slots and outputs of a workgroup at a time
+  bool quantizes = false;     // takes x itself
+};
+// src: 0 codes, 1 bf16 x, 2 fp32 x
+ExpertsPlan plan_experts(int64_t E, int64_t T, int64_t N, int64_t K, int src);
+// The products of every slot; sizes and pointers are validated by the C ABI.  X: where the plan for src
+// says that the kernel quantises.
+hipError_t launch_experts(const Groups& g, const void* X, int src, const int8_t* Xq, const float* absmax,
+                          const Epilogue& ep, hipStream_t s);
+
+// Y[m] = residual[m] + sum over j of weights[m][j] H[slots[m][j]], H fp32 [T][N] the products of the
+// slots.  Slots that no group holds or that have no token row are left out.
+hipError_t launch_combine(const Groups& g, const float* H, const int32_t* slots, const float* weights, int64_t M, int k,
+                          const Epilogue& ep, hipStream_t s);
+
+// The router: chunks of tokens, one workgroup each; one chunk is one launch.
+struct RoutePlan {
+  int chunks = 1, chunk = 0;  // chunk: tokens of one
+  int64_t ws_bytes = 0;       // [chunks][E] counts where there are several
+};
+RoutePlan plan_route(int64_t M, int64_t E);
+constexpr int kMaxRouteExperts = 512;  // 8 logits to a lane; the waves' counts fit LDS
+constexpr int kMaxRouteChoices = 16;
+struct RouteArgs {
+  const void* logits;
+  int bf16, renorm;
+  int64_t M;
+  int E, k;
+  int32_t* experts;  // [M][k]
+  float* weights;    // [M][k]
+  int32_t* offsets;  // [E + 1]
+  int32_t* rows;     // [M k]
+  int32_t* slots;    // [M][k]
+  int32_t* counts;   // workspace
+};
+hipError_t launch_route(const RouteArgs& a, hipStream_t s);
+
+}  // namespace bl

@@ -1,0 +1,306 @@
+// The router of a layer with experts: each token's k largest logits, their weights, and the slots (a
+// token at one of its experts) ordered by expert, then token.
+//
+// A counting sort whose order does not depend on timing.  Tokens are cut into chunks, one workgroup
+// each.  k_route_top chooses and counts per chunk; k_route_place adds up the counts of the chunks before
+// its own and of the experts before, and deals out the places in order: a wave takes 64 choices at a time
+// and finds by ballots over the bits of the expert's number which lanes share one, so that a choice's
+// place is its expert's next place plus the number of such lanes before it.  One chunk does both in one
+// launch.
+//
+// Bound by latency where tokens are few, else by the logits' bytes.
+#include "experts.h"
+
+#include <algorithm>
+
+namespace bl {
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kWaves = kThreads / 64;
+
+// A logit as an integer of the same order; 0: never chosen (-inf, NaN).  +inf counts as the largest
+// finite number, -0 as 0, so that numbers that are equal have equal keys.
+__device__ __forceinline__ uint32_t key_of(float x) {
+  if (!(x > -__builtin_inff())) return 0;
+  x = fminf(x, 3.402823466e38f) + 0.0f;
+  const uint32_t b = __float_as_uint(x);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+}
+
+// Over each row of 16 lanes, in every lane of it.
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+  v = quad_max(v);
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xf, 0xf, true));         // row_half_mirror
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xf, 0xf, true));      // row_mirror
+}
+__device__ __forceinline__ float row_sum(float v) {
+  auto step = [&](auto c) {
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(c)::value, 0xf, 0xf, true));
+  };
+  step(std::integral_constant<int, 0xB1>{});
+  step(std::integral_constant<int, 0x4E>{});
+  step(std::integral_constant<int, 0x141>{});
+  step(std::integral_constant<int, 0x140>{});
+  return v;
+}
+// Over G lanes (16, or the wave).
+template <int G>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  v = row_max(v);
+  if constexpr (G == 16) return v;
+  const uint32_t a = __builtin_amdgcn_readlane(v, 0), b = __builtin_amdgcn_readlane(v, 16);
+  const uint32_t c = __builtin_amdgcn_readlane(v, 32), d = __builtin_amdgcn_readlane(v, 48);
+  return max(max(a, b), max(c, d));
+}
+template <int G>
+__device__ __forceinline__ float lanes_sum(float v) {
+  v = row_sum(v);
+  if constexpr (G == 16) return v;
+  auto at = [&](int l) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l)); };
+  return (at(0) + at(16)) + (at(32) + at(48));
+}
+
+// The choices of token m, by G lanes with V consecutive logits each.  Lane j of them returns the j-th
+// choice (-1: none) in `id` and its weight.
+template <int G, int V>
+__device__ __forceinline__ void choose(const RouteArgs& a, int64_t m, bool live, int& id, float& weight) {
+  const int lane = threadIdx.x & 63, l = lane % G;
+  uint32_t key[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int e = l * V + v;
+    key[v] = 0;
+    if (live && e < a.E)
+      key[v] = key_of(a.bf16 ? bf16_float(static_cast<const uint16_t*>(a.logits)[m * a.E + e])
+                             : static_cast<const float*>(a.logits)[m * a.E + e]);
+  }
+  // the lane's largest, at its lowest place
+  uint32_t best = 0;
+  int at = 0;
+  auto pick = [&]() {
+    best = key[0];
+    at = 0;
+#pragma unroll
+    for (int v = 1; v < V; ++v)
+      if (key[v] > best) best = key[v], at = v;
+  };
+  pick();
+  const uint32_t peak_key = lanes_max<G>(best);
+  const float peak = peak_key ? value_of(peak_key) : 0.0f;
+  float total = 0.0f;
+  if (!a.renorm) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) total += key[v] ? exp_of(value_of(key[v]) - peak) : 0.0f;
+    total = lanes_sum<G>(total);
+  }
+  id = -1;
+  uint32_t mine = 0;  // the key of choice l
+  for (int j = 0; j < a.k; ++j) {
+    const uint32_t top = j ? lanes_max<G>(best) : peak_key;
+    uint64_t holders = __ballot(best == top);
+    int first;  // lane that holds it
+    if constexpr (G == 64) {
+      first = __builtin_ctzll(holders);
+    } else {
+      holders = holders >> (lane & 48) & 0xffff;
+      first = (lane & 48) + __builtin_ctzll(holders);
+    }
+    const int where = G == 64 ? __builtin_amdgcn_readlane(at, first) : __shfl(at, first, 64);
+    if (l == j && top) id = (first % G) * V + where, mine = top;
+    if (lane == first) {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (v == at) key[v] = 0;
+      pick();
+    }
+  }
+  const float p = mine ? exp_of(value_of(mine) - peak) : 0.0f;
+  if (a.renorm) total = lanes_sum<G>(p);
+  weight = mine ? p / total : 0.0f;
+}
+
+// Choices and weights of the tokens [m0, m1), and how often each expert was chosen into `count` (LDS).
+template <int G, int V>
+__device__ __forceinline__ void choose_chunk(const RouteArgs& a, int64_t m0, int64_t m1, int32_t* count) {
+  constexpr int kPer = 64 / G;  // tokens of a wave
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = lane % G;
+  for (int64_t m = m0 + wave * kPer; m < m1; m += (blockDim.x >> 6) * kPer) {
+    const int64_t mine = m + lane / G;
+    int id;
+    float w;
+    choose<G, V>(a, mine, mine < m1, id, w);
+    if (mine < m1 && l < a.k) {
+      a.experts[mine * a.k + l] = id;
+      a.weights[mine * a.k + l] = w;
+      if (id >= 0) atomicAdd(&count[id], 1);
+    }
+  }
+}
+
+// Places of the choices [i0, i1) of chunk c.  LDS: base [waves][E], of which row 0 starts as the number
+// of this chunk's choices per expert; total [E + 1].
+__device__ __forceinline__ void place_chunk(const RouteArgs& a, int c, int chunks, int64_t i0, int64_t i1, int32_t* base,
+                                            int32_t* total) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int E = a.E, waves = blockDim.x >> 6;
+  // each expert's choices in all chunks, and in those before this one
+  int32_t* before = base;  // [E]
+  if (chunks > 1) {
+    for (int e = tid; e < E; e += blockDim.x) before[e] = total[e] = 0;
+    __syncthreads();
+    // groups of threads take the chunks in turn (integer sums: any order)
+    const int width = 64 * ((E + 63) / 64), parts = max(1, (int)blockDim.x / width);
+    for (int t = tid; t < width * parts; t += blockDim.x) {
+      const int e = t % width, p = t / width;
+      if (e >= E) continue;
+      int all = 0, left = 0;
+#pragma unroll 8
+      for (int h = p; h < chunks; h += parts) {
+        const int n = a.counts[(int64_t)h * E + e];
+        all += n;
+        left += h < c ? n : 0;
+      }
+      atomicAdd(&total[e], all);
+      atomicAdd(&before[e], left);
+    }
+  } else {
+    for (int e = tid; e < E; e += blockDim.x) {
+      total[e] = base[e];
+      before[e] = 0;
+    }
+  }
+  __syncthreads();
+  // total: to the first place of each expert
+  if (wave == 0) {
+    int run = 0;
+    for (int e0 = 0; e0 < E; e0 += 64) {
+      const int n = e0 + lane < E ? total[e0 + lane] : 0;
+      int incl = n;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int v = __shfl_up(incl, d, 64);
+        if (lane >= d) incl += v;
+      }
+      if (e0 + lane < E) total[e0 + lane] = run + incl - n;
+      run += __builtin_amdgcn_readlane(incl, 63);
+    }
+    if (lane == 0) total[E] = run;
+  }
+  __syncthreads();
+  for (int e = tid; e < E; e += blockDim.x) {
+    total[e] += before[e];  // this chunk's first place
+    if (c == 0) a.offsets[e] = total[e];  // (before is 0 in chunk 0)
+  }
+  if (c == 0 && tid == 0) a.offsets[E] = total[E];
+  const int64_t used = total[E], T = a.M * a.k;
+  for (int64_t s = used + (int64_t)c * blockDim.x + tid; s < T; s += (int64_t)chunks * blockDim.x) a.rows[s] = -1;
+  __syncthreads();
+  // the waves share the choices in order; how often each expert comes up in each share
+  for (int e = tid; e < E * waves; e += blockDim.x) base[e] = 0;
+  __syncthreads();
+  const int64_t share = ((i1 - i0 + waves - 1) / waves + 63) / 64 * 64;
+  const int64_t lo = min(i0 + wave * share, i1), hi = min(lo + share, i1);
+  int32_t* mine = base + wave * E;
+  for (int64_t i = lo + lane; i < hi; i += 64) {
+    const int e = a.experts[i];
+    if (e >= 0) atomicAdd(&mine[e], 1);
+  }
+  __syncthreads();
+  for (int e = tid; e < E; e += blockDim.x) {
+    int run = total[e];
+    for (int w = 0; w < waves; ++w) {
+      const int n = base[w * E + e];
+      base[w * E + e] = run;
+      run += n;
+    }
+  }
+  __syncthreads();
+  const int bits = 32 - __builtin_clz(max(E - 1, 1));
+  for (int64_t i = lo; i < hi; i += 64) {
+    const int64_t at = i + lane;
+    const int e = at < hi ? a.experts[at] : -1;
+    uint64_t same = __ballot(e >= 0);
+    for (int b = 0; b < bits; ++b) {
+      const uint64_t set = __ballot(e >> b & 1);
+      same &= (e >> b & 1) ? set : ~set;
+    }
+    int place = -1;
+    if (e >= 0) {
+      const int next = mine[e];
+      place = next + __popcll(same & ((1ull << lane) - 1));
+      a.rows[place] = (int32_t)(at / a.k);
+      if (lane == 63 - __builtin_clzll(same)) mine[e] = place + 1;
+    }
+    if (at < hi) a.slots[at] = place;
+  }
+}
+
+template <int G, int V>
+__global__ __launch_bounds__(kThreads) void k_route_one(RouteArgs a) {
+  extern __shared__ int32_t lds[];  // [waves][E], [E + 1]
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) lds[e] = 0;
+  __syncthreads();
+  choose_chunk<G, V>(a, 0, a.M, lds);
+  __threadfence_block();  // the choices are read again by other waves
+  __syncthreads();
+  place_chunk(a, 0, 1, 0, a.M * a.k, lds, lds + (blockDim.x >> 6) * a.E);
+}
+
+template <int G, int V>
+__global__ __launch_bounds__(kThreads) void k_route_top(RouteArgs a, int chunk) {
+  extern __shared__ int32_t lds[];  // [E]
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) lds[e] = 0;
+  __syncthreads();
+  const int64_t m0 = (int64_t)blockIdx.x * chunk;
+  choose_chunk<G, V>(a, m0, min(m0 + chunk, a.M), lds);
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.counts[(int64_t)blockIdx.x * a.E + e] = lds[e];
+}
+
+__global__ __launch_bounds__(kThreads) void k_route_place(RouteArgs a, int chunk) {
+  extern __shared__ int32_t lds[];  // [waves][E], [E + 1]
+  const int64_t m0 = (int64_t)blockIdx.x * chunk;
+  place_chunk(a, blockIdx.x, gridDim.x, m0 * a.k, min(m0 + chunk, a.M) * a.k, lds, lds + (blockDim.x >> 6) * a.E);
+}
+
+template <int G, int V>
+hipError_t launch(const RouteArgs& a, const RoutePlan& p, hipStream_t s) {
+  const size_t lds = (size_t)((kWaves + 1) * a.E + 1) * 4;
+  if (p.chunks == 1) {
+    k_route_one<G, V><<<1, kThreads, lds, s>>>(a);
+    return hipGetLastError();
+  }
+  k_route_top<G, V><<<p.chunks, kThreads, (size_t)a.E * 4, s>>>(a, p.chunk);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  k_route_place<<<p.chunks, kThreads, lds, s>>>(a, p.chunk);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+RoutePlan plan_route(int64_t M, int64_t E) {
+  RoutePlan p;
+  p.chunk = (int)M;
+  if (M > 256) {
+    p.chunk = (int)std::max<int64_t>(64, (M + 255) / 256);
+    p.chunks = (int)((M + p.chunk - 1) / p.chunk);
+    p.ws_bytes = (int64_t)p.chunks * E * 4;
+  }
+  return p;
+}
+
+hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
+  const RoutePlan p = plan_route(a.M, a.E);
+  if (a.E <= 16 && a.k <= 16) return launch<16, 1>(a, p, s);
+  if (a.E <= 64) return launch<64, 1>(a, p, s);
+  if (a.E <= 128) return launch<64, 2>(a, p, s);
+  if (a.E <= 256) return launch<64, 4>(a, p, s);
+  return launch<64, 8>(a, p, s);
+}
+
+}  // namespace bl

@@ -340,6 +340,128 @@ int bitlinear_forward_binary(const uint8_t* packed, const float* beta, const int
 int bitlinear_forward_binary_plan(int64_t M, int64_t N, int64_t K, int32_t out[6]);
 
 /*
+ * Products with an epilogue: what a model does right behind a BitLinear layer, done while the
+ * result is still in registers, and the result in the type that the next layer takes.
+ *     Y[m][n] = act(acc[m][n] * gamma * a[m] / 127 + bias[n]) + residual[m][n]
+ * in fp32, rounded once to Y's type (ties to even); acc is the exact int32 product of
+ * bitlinear_forward.
+ *   act   relu(v) = max(v, 0); relu2(v) = relu(v)^2; silu(v) = v / (1 + e^-v);
+ *         gelu(v) = v (1 + erf(v / sqrt 2)) / 2;
+ *         gelu_tanh(v) = v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2.
+ */
+typedef enum {
+  BL_ACT_NONE = 0,
+  BL_ACT_RELU = 1,
+  BL_ACT_RELU2 = 2,
+  BL_ACT_SILU = 3,
+  BL_ACT_GELU = 4,
+  BL_ACT_GELU_TANH = 5
+} bl_activation;
+
+typedef struct {
+  const float* bias;     /* fp32 [N] ([E][N] where there are experts), or NULL                */
+  const void* residual;  /* rows of N values of type residual_dt, or NULL; may be Y itself    */
+  void* Y;               /* out: rows of N values of type y_dt; element-aligned               */
+  int64_t residual_ld;   /* elements from one row of residual to the next, 0: N               */
+  int64_t y_ld;          /* the same of Y                                                     */
+  int act;               /* bl_activation                                                     */
+  int residual_dt;       /* bl_dtype; ignored where residual is NULL                          */
+  int y_dt;              /* bl_dtype                                                          */
+} bl_epilogue;
+
+/*
+ * One matrix.  packed, gamma, M, N, K as bitlinear_forward.
+ *   X     [M][K] fp32 or bf16 (dt), quantised within the call as bitlinear_quantize_acts does;
+ *         or NULL: Xq and absmax then are inputs that hold the codes and scales (dt is ignored).
+ *   Xq, absmax  with X: scratch of bitlinear_quantize_acts' sizes and alignments, with
+ *         unspecified contents afterwards; both may be NULL where
+ *         bitlinear_forward_epilogue_plan reports a single launch.
+ *   ep    a HOST struct.  A residual that overlaps Y must be Y (same address, row distance and
+ *         type); no other buffers of one call may overlap.
+ * Errors: BL_ERR_INVALID_ARG for null pointers, sizes, misaligned pointers, row distances below
+ * N and an unknown act; BL_ERR_UNSUPPORTED for other types and for launches that are too large
+ * (M and N of more than 2^31 tiles of 16 x 64).
+ */
+int bitlinear_forward_epilogue(const uint8_t* packed, const float* gamma, const void* X, int dt, int8_t* Xq,
+                               float* absmax, int64_t M, int64_t N, int64_t K, const bl_epilogue* ep, void* stream);
+
+/*
+ * Host-only: the launches of bitlinear_forward_epilogue for (M, N, K) and x of type xdt (-1: codes).
+ * out[0] = kernel (10), out[1] = its workgroups, out[2] = threads per workgroup, out[3] and out[4] =
+ * token rows and outputs of a workgroup at a time, out[5] = launches (2: the quantiser first).
+ * Returns BL_OK, BL_ERR_INVALID_ARG or BL_ERR_UNSUPPORTED as the call does.
+ */
+int bitlinear_forward_epilogue_plan(int64_t M, int64_t N, int64_t K, int xdt, int32_t out[6]);
+
+/*
+ * Experts: E matrices of one shape, and each token row goes through some of them.  The products
+ * are slots: slot s of expert e, offsets[e] <= s < offsets[e + 1], is token row rows[s] times
+ * matrix e, and row s of Y (and of the residual).  How many slots an expert has is known on the
+ * device only; none, or all of them, is fine.  bitlinear_route_experts makes these tables.
+ * A HOST struct of DEVICE pointers.
+ */
+typedef struct {
+  const uint8_t* packed;  /* [E] buffers of bitlinear_packed_bytes(N, K), one behind the other;
+                             16-byte aligned                                                    */
+  const float* gamma;     /* [E] their scales                                                   */
+  const int32_t* offsets; /* [E + 1], 0 <= offsets[0], rising (or equal), offsets[E] <= T       */
+  const int32_t* rows;    /* [T], or NULL: slot s takes row s                                   */
+  int64_t E, T, N;        /* experts; slots; outputs                                            */
+} bl_experts;
+
+/*
+ * Y[s] = act(acc * gamma[e] * a[rows[s]] / 127 + bias[e]) + residual[s] for every slot s of
+ * every expert e.
+ *   X, dt, Xq, absmax  the R token rows, as bitlinear_forward_epilogue (scratch may be NULL where
+ *         bitlinear_forward_experts_plan reports a single launch).
+ * Slots outside offsets[0] .. offsets[E] - 1, and those whose row is not in 0 .. R - 1, are left
+ * out: their rows of Y stay as they were.  (Offsets that break their rule give unspecified rows of
+ * Y, and touch nothing else.)
+ *   Limits: E <= 4096 (BL_ERR_UNSUPPORTED beyond), 1 <= T, R < 2^31.
+ */
+int bitlinear_forward_experts(const bl_experts* experts, const void* X, int dt, int8_t* Xq, float* absmax, int64_t R,
+                              int64_t K, const bl_epilogue* ep, void* stream);
+
+/* Host-only: its launches for E experts and T slots, as bitlinear_forward_epilogue_plan. */
+int bitlinear_forward_experts_plan(int64_t E, int64_t T, int64_t N, int64_t K, int xdt, int32_t out[6]);
+
+/*
+ * The same, the slots of a token added up:
+ *     Y[m] = residual[m] + sum over j < k of weights[m][j] * act(acc * gamma[e] * a / 127 + bias[e])
+ * at slot slots[m][j], summed in fp32 in the order of j.  Y and the residual have M rows.  Slots
+ * that are left out above, and entries outside 0 .. T - 1 (-1), add nothing.
+ *   slots   int32 [M][k]; weights fp32 [M][k], finite; 1 <= k <= 64.
+ *   workspace  at least bitlinear_forward_experts_combine_ws_bytes(T, N) bytes, 16-byte aligned.
+ *         Its contents on entry do not matter and nothing carries over.  Calls that share one must
+ *         not overlap.
+ */
+int64_t bitlinear_forward_experts_combine_ws_bytes(int64_t T, int64_t N); /* -1 for invalid sizes */
+int bitlinear_forward_experts_combine(const bl_experts* experts, const void* X, int dt, int8_t* Xq, float* absmax,
+                                      int64_t R, int64_t K, const int32_t* slots, const float* weights, int64_t M,
+                                      int64_t k, const bl_epilogue* ep, void* workspace, int64_t ws_bytes,
+                                      void* stream);
+
+/*
+ * The router: the k largest of each token's E logits, in falling order (of equal ones the lowest
+ * index first), their weights, and the slots ordered by expert, then token.
+ *   logits  [M][E] fp32 or bf16 (dt).  -inf and NaN are never chosen, +inf counts as the largest
+ *           finite number: a token with fewer than k others has choices missing (a padded token,
+ *           all -inf, has none).
+ *   experts out: int32 [M][k], -1 for a missing choice.
+ *   weights out: fp32 [M][k], e^logit over the sum of the chosen ones (renormalize = 1) or of all E
+ *           (0); 0 for a missing choice.
+ *   offsets out: int32 [E + 1]; rows out: int32 [M k], the token of each slot, -1 behind the last;
+ *   slots   out: int32 [M][k], the slot of each choice, -1 for a missing one.
+ *   workspace  at least bitlinear_route_experts_ws_bytes(M, E) bytes, 4-byte aligned; may be NULL
+ *           where that is 0.  Contents as above.
+ * Limits: 1 <= k <= E, k <= 16, E <= 512, M k < 2^31 (BL_ERR_UNSUPPORTED for the last three).
+ */
+int64_t bitlinear_route_experts_ws_bytes(int64_t M, int64_t E); /* -1 for invalid sizes */
+int bitlinear_route_experts(const void* logits, int dt, int64_t M, int64_t E, int64_t k, int renormalize,
+                            int32_t* experts, float* weights, int32_t* offsets, int32_t* rows, int32_t* slots,
+                            void* workspace, int64_t ws_bytes, void* stream);
+
+/*
  * Microscaled 4-bit floating point (MXFP4), the 4-bit format the gfx950 matrix cores take
  * directly: a quantiser for weights and activations alike, and the product of two matrices
  * held in it.  Per row, a block of 32 consecutive columns shares one power of two; every
