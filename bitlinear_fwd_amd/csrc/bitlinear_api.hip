@@ -66,12 +66,14 @@ int epilogue_of(const bl_epilogue* ep, int64_t N, bl::Epilogue* out) {
   out->act = ep->act;
   out->res_bf16 = ep->residual && ep->residual_dt == BL_BF16;
   out->y_bf16 = ep->y_dt == BL_BF16;
+  out->stream = aligned(ep->Y, 16) && out->ldy * (int64_t)dtype_align(ep->y_dt) % 16 == 0;
   return BL_OK;
 }
 
-// A launch can be counted: units of 16 slots by 64 outputs in 31 bits, matrices in 40 bits of bytes.
+// A launch can be counted: slots and units of 16 slots by 64 outputs in 31 bits (with room for the rows of a
+// tile behind the last slot), matrices in 40 bits of bytes.
 bool products_countable(int64_t E, int64_t T, int64_t N, int64_t K) {
-  if (E > kMaxExperts || bl::n_pad(N) > kMaxCount / bl::k_pad(K) / E) return false;
+  if (E > kMaxExperts || T > kMaxDim - 4096 || bl::n_pad(N) > kMaxCount / bl::k_pad(K) / E) return false;
   return T / 16 + 1 + (E < T ? E : T) <= (kMaxDim - 1) / ((N + 63) / 64);
 }
 
@@ -355,6 +357,7 @@ int bitlinear_forward_experts_combine(const bl_experts* experts, const void* X, 
   e.Y = workspace;
   e.ldy = g.N;
   e.y_bf16 = 0;
+  e.stream = 0;  // read again at once
   hipStream_t s = static_cast<hipStream_t>(stream);
   st = products(g, X, dt, Xq, absmax, e, s);
   if (st != BL_OK) return st;

@@ -17,6 +17,7 @@ struct Epilogue {
   int64_t ldr, ldy;      // elements between rows
   int act;               // bl_activation
   int res_bf16, y_bf16;
+  int stream;            // rows of Y and the pieces of 16 bytes in them are aligned
 };
 
 // The matrices and which rows each of them takes.
@@ -44,11 +45,24 @@ __device__ __forceinline__ int slot_row(const Groups& g, int s) {
 }
 
 // Work is dealt in units of up to `height` consecutive slots of one group; the units of all groups are
-// numbered in order.  find_unit gives unit u's group and slots (lo >= hi: there is no such unit).
-// Every lane of the wave calls it with the same u; 64 groups are looked at together.
+// numbered in order.  Every lane of a wave calls these with the same arguments.  Offsets that break their
+// rule may give units that overlap or are passed over, but never one outside 0 .. T.
 struct Unit {
-  int e, lo, hi;
+  int e, lo, hi;  // group and slots (lo >= hi: there is no such unit)
 };
+__device__ __forceinline__ int units_of(int2 s, int height) {
+  return (int)(((uint32_t)(s.y - s.x) + height - 1) / height);
+}
+// Units of all groups, at most `most`.
+__device__ __forceinline__ int count_units(const Groups& g, int height, int most) {
+  if (!g.offsets) return (int)((g.T + height - 1) / height);
+  int n = 0;
+  for (int e = threadIdx.x & 63; e < g.E; e += 64) n = min(n + min(units_of(group_slots(g, e), height), most), most);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) n = min(n + __shfl_xor(n, d, 64), most);
+  return __builtin_amdgcn_readfirstlane(n);
+}
+// Unit u; 64 groups are looked at together.
 __device__ __forceinline__ Unit find_unit(const Groups& g, int height, int u) {
   if (!g.offsets) {
     const int64_t lo = (int64_t)u * height;
@@ -59,7 +73,7 @@ __device__ __forceinline__ Unit find_unit(const Groups& g, int height, int u) {
   for (int e0 = 0; e0 < g.E; e0 += 64) {
     int2 s = make_int2(0, 0);
     if (e0 + lane < g.E) s = group_slots(g, e0 + lane);
-    const int mine = (s.y - s.x + height - 1) / height;
+    const int mine = units_of(s, height);
     int incl = mine;  // units of this and the groups before it
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -69,10 +83,10 @@ __device__ __forceinline__ Unit find_unit(const Groups& g, int height, int u) {
     const uint64_t after = __ballot(incl > u);
     if (after) {
       const int l = __builtin_ctzll(after);
-      const int first = __builtin_amdgcn_readlane(incl - mine, l);
-      const int slo = __builtin_amdgcn_readlane(s.x, l), shi = __builtin_amdgcn_readlane(s.y, l);
-      const int lo = slo + (u - first) * height;
-      return Unit{e0 + l, lo, min(lo + height, shi)};
+      const int at = u - __builtin_amdgcn_readlane(incl - mine, l);
+      if ((uint32_t)at >= (uint32_t)__builtin_amdgcn_readlane(mine, l)) return Unit{0, 0, 0};
+      const int lo = __builtin_amdgcn_readlane(s.x, l) + at * height, hi = __builtin_amdgcn_readlane(s.y, l);
+      return Unit{e0 + l, lo, hi - lo < height ? hi : lo + height};
     }
     u -= __builtin_amdgcn_readlane(incl, 63);
   }
@@ -95,19 +109,44 @@ __device__ __forceinline__ float exp_of(float x) {
 }
 __device__ __forceinline__ float sigmoid_of(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_of(-x)); }
 
+// v (1 + erf(v / sqrt 2)) / 2 by Abramowitz and Stegun's 7.1.26: erfc(x) = (a1 t + .. + a5 t^5) e^(-x^2) + 1.5e-7 at
+// most, t = 1 / (1 + p x), x >= 0: off by 1.3 half steps of |v| (with erff a 2048 x 6912 output took 16 us longer).
+__device__ __forceinline__ float gelu_of(float v) {
+  const float x = fabsf(v) * 0.70710678f, t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f, x, 1.0f));
+  float q = __builtin_fmaf(1.061405429f, t, -1.453152027f);
+  q = __builtin_fmaf(q, t, 1.421413741f);
+  q = __builtin_fmaf(q, t, -0.284496736f);
+  q = __builtin_fmaf(q, t, 0.254829592f) * t;
+  const float half = 0.5f * q * __builtin_amdgcn_exp2f(-1.44269504f * x * x) * v;  // erfc(|x|) v / 2
+  return v > 0.0f ? v - half : half;
+}
+
 // The activations of bl_activation, in fp32.
-__device__ __forceinline__ float activate(float v, int act) {
+template <int kAct>
+__device__ __forceinline__ float activate(float v) {
+  if constexpr (kAct == 1) return fmaxf(v, 0.0f);
+  else if constexpr (kAct == 2) return fmaxf(v, 0.0f) * fmaxf(v, 0.0f);
+  else if constexpr (kAct == 3) return v * sigmoid_of(v);
+  else if constexpr (kAct == 4) return gelu_of(v);
+  // (1 + tanh u) / 2 = sigmoid(2 u)
+  else if constexpr (kAct == 5) return v * sigmoid_of(1.59576912f * __builtin_fmaf(0.044715f * v * v, v, v));
+  else return v;
+}
+template <int H>
+__device__ __forceinline__ void activate_all(v4f (&v)[H], int act) {
+  auto go = [&](auto a) {
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[h][e] = activate<decltype(a)::value>(v[h][e]);
+  };
   switch (act) {
-    case 1: return fmaxf(v, 0.0f);
-    case 2: {
-      const float r = fmaxf(v, 0.0f);
-      return r * r;
-    }
-    case 3: return v * sigmoid_of(v);
-    case 4: return 0.5f * v * (1.0f + erff(v * 0.70710678f));
-    case 5:  // (1 + tanh u) / 2 = sigmoid(2 u)
-      return v * sigmoid_of(1.59576912f * __builtin_fmaf(0.044715f * v * v, v, v));
-    default: return v;
+    case 1: return go(std::integral_constant<int, 1>{});
+    case 2: return go(std::integral_constant<int, 2>{});
+    case 3: return go(std::integral_constant<int, 3>{});
+    case 4: return go(std::integral_constant<int, 4>{});
+    case 5: return go(std::integral_constant<int, 5>{});
+    default: return;
   }
 }
 
@@ -166,19 +205,57 @@ __device__ __forceinline__ void store4(void* base, int64_t at, int left, int bf1
 // A token's scale: the exact products are multiplied by gamma a / 127.
 __device__ __forceinline__ float token_scale(float gamma, float a) { return gamma * a / 127.0f; }
 
+// 4 H consecutive values at element `at`; and the same to Y, past the caches (whole aligned pieces of 16 bytes).
+template <typename H>
+__device__ __forceinline__ void load_row(const void* base, int64_t at, int bf16, v4f* v, H) {
+  if (bf16) {
+    uint16_t h[4 * H::value];
+    __builtin_memcpy(h, static_cast<const uint16_t*>(base) + at, 8 * H::value);
+#pragma unroll
+    for (int i = 0; i < 4 * H::value; ++i) v[i / 4][i % 4] = bf16_float(h[i]);
+  } else {
+    __builtin_memcpy(v, static_cast<const float*>(base) + at, 16 * H::value);
+  }
+}
+template <typename H>
+__device__ __forceinline__ void stream_row(const Epilogue& ep, int64_t at, const v4f* v, H) {
+  if constexpr (H::value == 2) {
+    const v4u w = {bf16_pair(v[0][0], v[0][1]), bf16_pair(v[0][2], v[0][3]), bf16_pair(v[1][0], v[1][1]),
+                   bf16_pair(v[1][2], v[1][3])};
+    __builtin_nontemporal_store(w, reinterpret_cast<v4u*>(static_cast<uint16_t*>(ep.Y) + at));
+  } else {
+    __builtin_nontemporal_store(__builtin_bit_cast(v4u, v[0]), reinterpret_cast<v4u*>(static_cast<float*>(ep.Y) + at));
+  }
+}
+
+// The end of the epilogue: residual, rounding and store of 4 H consecutive outputs n .. of row s (left of them before
+// column N).
+template <int H>
+__device__ __forceinline__ void finish_row(const Epilogue& ep, int64_t s, int64_t n, int left, v4f (&v)[H]) {
+  if (ep.residual) {
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+      if (left > 4 * h) v[h] += load4(ep.residual, s * ep.ldr + n + 4 * h, min(left - 4 * h, 4), ep.res_bf16);
+  }
+  const int64_t at = s * ep.ldy + n;
+#pragma unroll
+  for (int h = 0; h < H; ++h)
+    if (left > 4 * h) store4(ep.Y, at + 4 * h, min(left - 4 * h, 4), ep.y_bf16, v[h]);
+}
+
 // The epilogue of four consecutive outputs n .. n + 3 of slot s (left of them before column N).
 __device__ __forceinline__ void finish4(const Epilogue& ep, int64_t e, int64_t N, int64_t s, int64_t n, int left, v4i acc,
                                         float scale) {
-  v4f b = {0, 0, 0, 0}, v;
+  v4f b = {0, 0, 0, 0}, v[1];
   if (ep.bias) b = load4(ep.bias, e * N + n, left, 0);
 #pragma unroll
-  for (int q = 0; q < 4; ++q) v[q] = activate(__builtin_fmaf((float)acc[q], scale, b[q]), ep.act);
-  if (ep.residual) v += load4(ep.residual, s * ep.ldr + n, left, ep.res_bf16);
-  store4(ep.Y, s * ep.ldy + n, left, ep.y_bf16, v);
+  for (int q = 0; q < 4; ++q) v[0][q] = __builtin_fmaf((float)acc[q], scale, b[q]);
+  activate_all(v, ep.act);
+  finish_row(ep, s, n, left, v);
 }
 
 // How the products of T slots of E matrices (E = 0: one matrix, no tables) are computed.
-enum { kPlainKernel = 10 };
+enum { kPlainKernel = 10, kGemmKernel = 11 };
 struct ExpertsPlan {
   int kernel = kPlainKernel;
   int threads = 256;
@@ -192,6 +269,9 @@ ExpertsPlan plan_experts(int64_t E, int64_t T, int64_t N, int64_t K, int src);
 // says that the kernel quantises.
 hipError_t launch_experts(const Groups& g, const void* X, int src, const int8_t* Xq, const float* absmax,
                           const Epilogue& ep, hipStream_t s);
+
+hipError_t launch_experts_gemm(const ExpertsPlan& p, const Groups& g, const int8_t* Xq, const float* absmax,
+                               const Epilogue& ep, hipStream_t s);
 
 // Y[m] = residual[m] + sum over j of weights[m][j] H[slots[m][j]], H fp32 [T][N] the products of the
 // slots.  Slots that no group holds or that have no token row are left out.

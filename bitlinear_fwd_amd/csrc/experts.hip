@@ -1,6 +1,9 @@
 // Ternary products with an epilogue, plainly: a wave per 16 slots x 16 outputs, operands from global memory.
 #include "experts.h"
 
+#include <algorithm>
+#include <cmath>
+
 namespace bl {
 namespace {
 
@@ -55,8 +58,35 @@ __global__ __launch_bounds__(256) void k_combine(Groups g, const float* __restri
 
 }  // namespace
 
+// The GEMM's tile.  A unit of `height` slots by `width` outputs takes `first` us where each compute unit has at
+// most one tile (a stage of 128 columns has its latency) and `more` us where several share it; `end` is what else a
+// tile costs.  Fitted to 37 shapes from 64 to 65536 rows, 128 to 8192 outputs and 900 to 8192 columns.
+namespace {
+struct Tile {
+  int height, width;
+  double first, more, end;
+};
+constexpr Tile kTiles[] = {{128, 256, .63, .66, 1.5}, {96, 256, .49, .475, 1.5}, {64, 256, .40, .365, 1.2},
+                           {64, 128, .255, .218, 1.0}, {32, 256, .31, .25, .9}, {32, 128, .225, .137, .9}};
+}  // namespace
+
 ExpertsPlan plan_experts(int64_t E, int64_t T, int64_t N, int64_t K, int src) {
   ExpertsPlan p;
+  const int64_t groups = E ? std::min(E, T) : 1;  // that have slots, at most
+  if (T > 16 * groups) {
+    const double stages = (double)(k_pad(K) / 128), each = (double)T / groups;
+    double best = 1e300;
+    for (const Tile& t : kTiles) {
+      // units of groups of different sizes end half full
+      const double units = E ? groups * std::max(1.0, each / t.height + 0.5) : (double)((T + t.height - 1) / t.height);
+      const double rounds = std::ceil(units * ((N + t.width - 1) / t.width) / 256.0);
+      const double us = rounds > 1 ? rounds * (stages * t.more + t.end) : stages * t.first + t.end;
+      if (us < best) best = us, p.height = t.height, p.width = t.width;
+    }
+    p.kernel = kGemmKernel;
+    p.groups = (N + p.width - 1) / p.width * (E ? most_units(E, T, p.height) : (T + p.height - 1) / p.height);
+    return p;
+  }
   p.groups = (n_pad(N) / kTileRows + 3) / 4 * (E ? most_units(E, T, 16) : (T + 15) / 16);
   return p;
 }
@@ -66,6 +96,7 @@ hipError_t launch_experts(const Groups& g, const void* X, int src, const int8_t*
   const int chunks = (int)(k_pad(g.K) / kTileCols);
   const int64_t nblocks = n_pad(g.N) / kTileRows;
   const ExpertsPlan p = plan_experts(g.offsets ? g.E : 0, g.T, g.N, g.K, src);
+  if (p.kernel == kGemmKernel) return launch_experts_gemm(p, g, Xq, absmax, ep, s);
   k_experts<<<dim3((unsigned)p.groups), p.threads, 0, s>>>(g, Xq, absmax, ep, chunks, nblocks, (int)((nblocks + 3) / 4));
   return hipGetLastError();
 }
