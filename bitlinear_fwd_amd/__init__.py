@@ -1224,7 +1224,7 @@ def _products_plan(e: int, t: int, n: int, k: int, xdt: int):
 
 def _products_plan_dict(e: int, t: int, n: int, k: int, x) -> dict:
     out = _products_plan(e, t, n, k, -1 if x is None else _named_dtype(x))
-    return {"kernel": {10: "plain", 11: "gemm"}[out[0]], "workgroups": out[1], "threads": out[2], "rows": out[3],
+    return {"kernel": {10: "fused", 11: "gemm", 12: "decode"}[out[0]], "workgroups": out[1], "threads": out[2], "rows": out[3],
             "outputs": out[4], "launches": out[5]}
 
 

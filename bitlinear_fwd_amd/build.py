@@ -14,7 +14,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libbitlinear.so")
 SOURCES = ["bitlinear_api.hip", "weight_quant.hip", "act_quant.hip", "gemv.hip", "gemv_lut.hip", "gemv_bin.hip",
            "gemm.hip", "probes.hip", "mxfp4_quant.hip", "mxfp4_decode.hip",
-           "mxfp4_gemm.hip", "layernorm.hip", "experts.hip", "experts_gemm.hip", "route.hip"]
+           "mxfp4_gemm.hip", "layernorm.hip", "experts.hip", "experts_gemm.hip", "experts_few.hip", "route.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

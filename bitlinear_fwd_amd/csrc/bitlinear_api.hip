@@ -70,11 +70,12 @@ int epilogue_of(const bl_epilogue* ep, int64_t N, bl::Epilogue* out) {
   return BL_OK;
 }
 
-// A launch can be counted: slots and units of 16 slots by 64 outputs in 31 bits (with room for the rows of a
-// tile behind the last slot), matrices in 40 bits of bytes.
+// A launch can be counted: slots, outputs and tiles of 16 x 16 in 31 bits (with room for the rows and columns of a tile
+// behind the last), matrices in 40 bits of bytes.
 bool products_countable(int64_t E, int64_t T, int64_t N, int64_t K) {
-  if (E > kMaxExperts || T > kMaxDim - 4096 || bl::n_pad(N) > kMaxCount / bl::k_pad(K) / E) return false;
-  return T / 16 + 1 + (E < T ? E : T) <= (kMaxDim - 1) / ((N + 63) / 64);
+  if (E > kMaxExperts || T > kMaxDim - 4096 || N > kMaxDim - 4096 || bl::n_pad(N) > kMaxCount / bl::k_pad(K) / E)
+    return false;
+  return T / 16 + 1 + (E < T ? E : T) <= (kMaxDim - 1) / ((N + 15) / 16);
 }
 
 // The operands of g (its R rows of codes, or of X), checked.

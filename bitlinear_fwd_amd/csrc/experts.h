@@ -255,12 +255,14 @@ __device__ __forceinline__ void finish4(const Epilogue& ep, int64_t e, int64_t N
 }
 
 // How the products of T slots of E matrices (E = 0: one matrix, no tables) are computed.
-enum { kPlainKernel = 10, kGemmKernel = 11 };
+enum { kFewKernel = 10, kGemmKernel = 11, kMidKernel = 12 };
 struct ExpertsPlan {
-  int kernel = kPlainKernel;
+  int kernel = kFewKernel;
   int threads = 256;
   int64_t groups = 0;         // workgroups
   int height = 16, width = 64;  // slots and outputs of a workgroup at a time
+  int per = 1;                // few, mid: row blocks of a workgroup
+  int64_t lds = 0;            // few: bytes
   bool quantizes = false;     // takes x itself
 };
 // src: 0 codes, 1 bf16 x, 2 fp32 x
@@ -270,6 +272,13 @@ ExpertsPlan plan_experts(int64_t E, int64_t T, int64_t N, int64_t K, int src);
 hipError_t launch_experts(const Groups& g, const void* X, int src, const int8_t* Xq, const float* absmax,
                           const Epilogue& ep, hipStream_t s);
 
+// LDS of the kernel for few slots: the waves' sums and the codes of `rows` token rows; a compute unit has kFewLds.
+constexpr int kFewLds = 160 * 1024;
+int64_t few_lds(int waves, int64_t rows, int64_t K);
+hipError_t launch_experts_few(const ExpertsPlan& p, const Groups& g, const void* X, int src, const Epilogue& ep,
+                              hipStream_t s);
+hipError_t launch_experts_mid(const ExpertsPlan& p, const Groups& g, const int8_t* Xq, const float* absmax,
+                              const Epilogue& ep, hipStream_t s);
 hipError_t launch_experts_gemm(const ExpertsPlan& p, const Groups& g, const int8_t* Xq, const float* absmax,
                                const Epilogue& ep, hipStream_t s);
 

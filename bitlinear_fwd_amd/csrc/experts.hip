@@ -1,4 +1,5 @@
-// Ternary products with an epilogue, plainly: a wave per 16 slots x 16 outputs, operands from global memory.
+// Ternary products with an epilogue, for one matrix or by expert: which kernel takes them, and the sum over the
+// slots of a token.
 #include "experts.h"
 
 #include <algorithm>
@@ -6,32 +7,6 @@
 
 namespace bl {
 namespace {
-
-__global__ __launch_bounds__(256) void k_experts(Groups g, const int8_t* __restrict__ Xq,
-                                                 const float* __restrict__ absmax, Epilogue ep, int chunks,
-                                                 int64_t nblocks, int columns) {
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r = lane & 15, q = lane >> 4;
-  const int64_t nb = (int64_t)(blockIdx.x % columns) * 4 + wave;
-  const Unit u = find_unit(g, 16, blockIdx.x / columns);
-  if (u.lo >= u.hi || nb >= nblocks) return;
-  const int slot = u.lo + r, row = slot < u.hi ? slot_row(g, slot) : -1;
-  const int8_t* x = Xq + (int64_t)max(row, 0) * chunks * kTileCols + 64 * q;
-  const uint4* w = reinterpret_cast<const uint4*>(g.packed + ((int64_t)u.e * nblocks + nb) * chunks * kTileBytes) + lane;
-  v4i acc = {0, 0, 0, 0};
-  for (int c = 0; c < chunks; ++c) {
-    const uint4 t = w[(int64_t)c * 64];
-    const uint32_t word[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const v4i xv = *reinterpret_cast<const v4i*>(x + (int64_t)c * kTileCols + 16 * i);
-      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(decode16(word[i]), xv, acc, 0, 0, 0);
-    }
-  }
-  if (row < 0) return;
-  const int64_t n = nb * 16 + 4 * q, left = g.N - n;
-  if (left > 0) finish4(ep, u.e, g.N, slot, n, (int)min(left, (int64_t)4), acc, token_scale(g.gamma[u.e], absmax[row]));
-}
 
 // One thread per four outputs of a token.
 __global__ __launch_bounds__(256) void k_combine(Groups g, const float* __restrict__ H,
@@ -58,47 +33,80 @@ __global__ __launch_bounds__(256) void k_combine(Groups g, const float* __restri
 
 }  // namespace
 
-// The GEMM's tile.  A unit of `height` slots by `width` outputs takes `first` us where each compute unit has at
-// most one tile (a stage of 128 columns has its latency) and `more` us where several share it; `end` is what else a
-// tile costs.  Fitted to 37 shapes from 64 to 65536 rows, 128 to 8192 outputs and 900 to 8192 columns.
 namespace {
+
+// Estimates in us, fitted to measured shapes (1 to 65536 rows, 128 to 8192 outputs, 900 to 28672 columns).
+// The GEMM's tiles of `height` slots by `width` outputs: a stage of 128 columns takes `first` where each compute unit
+// has at most one tile (its latency) and `more` a tile where several share it, `end` is what else a tile costs.
+// 2048 x 6912 x 2560 in tiles of 128 x 256, 96 x 256, 64 x 256, 64 x 128: 35.3, 39.1, 38.6, 42.3 us; 2048 x 2560 x
+// 6912: 43.1, 35.8, 43.1, 44.4; 512 x 2560 x 2560: 20.0, 16.4, 13.4, 10.1.
 struct Tile {
   int height, width;
   double first, more, end;
 };
 constexpr Tile kTiles[] = {{128, 256, .63, .66, 1.5}, {96, 256, .49, .475, 1.5}, {64, 256, .40, .365, 1.2},
                            {64, 128, .255, .218, 1.0}, {32, 256, .31, .25, .9}, {32, 128, .225, .137, .9}};
+constexpr double kGemmStart = 3.5;
+// The decode kernel's workgroups of `height` slots by `per` row blocks: a chunk of 256 columns takes `chunk` on a
+// compute unit (the rows' codes from L2 bound it).  32 x 8192 x 8192 by 16 x 1, 2, 4 and 32 x 4: 21.8, 13.3, 9.0,
+// 13.7 us, 16 x 2560 x 6912: 6.5, 6.6, 7.2, 8.6; the GEMM 21.2 and 18.7.
+struct Decode {
+  int height, per;
+  double chunk;
+};
+constexpr Decode kDecodes[] = {{16, 1, .118}, {16, 2, .125}, {16, 4, .143}, {32, 4, .243}};
+constexpr double kDecodeStart = 2.85, kDecodeEnd = .35;
+
 }  // namespace
 
 ExpertsPlan plan_experts(int64_t E, int64_t T, int64_t N, int64_t K, int src) {
   ExpertsPlan p;
-  const int64_t groups = E ? std::min(E, T) : 1;  // that have slots, at most
-  if (T > 16 * groups) {
-    const double stages = (double)(k_pad(K) / 128), each = (double)T / groups;
-    double best = 1e300;
-    for (const Tile& t : kTiles) {
-      // units of groups of different sizes end half full
-      const double units = E ? groups * std::max(1.0, each / t.height + 0.5) : (double)((T + t.height - 1) / t.height);
-      const double rounds = std::ceil(units * ((N + t.width - 1) / t.width) / 256.0);
-      const double us = rounds > 1 ? rounds * (stages * t.more + t.end) : stages * t.first + t.end;
-      if (us < best) best = us, p.height = t.height, p.width = t.width;
-    }
-    p.kernel = kGemmKernel;
-    p.groups = (N + p.width - 1) / p.width * (E ? most_units(E, T, p.height) : (T + p.height - 1) / p.height);
-    return p;
+  const int64_t blocks = n_pad(N) / kTileRows, chunks = k_pad(K) / kTileCols;
+  // groups that have slots, and units of them: groups of different sizes end half full
+  const double some = E ? (double)E * (1.0 - std::pow(1.0 - 1.0 / (double)E, (double)T)) : 1.0;
+  auto units = [&](int height) {
+    return E ? some * std::max(1.0, (double)T / some / height + (T > 4 * some ? 0.5 : 0.0)) : (double)((T + height - 1) / height);
+  };
+  double best = 1e300;
+  for (const Tile& t : kTiles) {
+    const double stages = (double)(2 * chunks), rounds = std::ceil(units(t.height) * (double)((N + t.width - 1) / t.width) / 256.0);
+    const double us = kGemmStart + (rounds > 1 ? rounds * (stages * t.more + t.end) : stages * t.first + t.end);
+    if (us < best) best = us, p.kernel = kGemmKernel, p.height = t.height, p.width = t.width;
   }
-  p.groups = (n_pad(N) / kTileRows + 3) / 4 * (E ? most_units(E, T, 16) : (T + 15) / 16);
+  for (const Decode& d : kDecodes) {
+    const double rounds = std::ceil(units(d.height) * (double)((blocks + d.per - 1) / d.per) / 256.0);
+    const double us = kDecodeStart + rounds * ((double)chunks * d.chunk + kDecodeEnd);
+    if (us < best) {
+      best = us, p.kernel = kMidKernel, p.height = d.height, p.per = d.per;
+      // the waves of a workgroup split the columns; many workgroups keep a compute unit busy by themselves
+      p.threads = 64 * (int)std::min<int64_t>(rounds > 5 ? 2 : rounds > 2 ? 4 : 8, chunks);
+    }
+  }
+  // Up to four slots of small matrices in one launch with the quantiser, which every workgroup then does for itself
+  // (bf16 x, one launch and two: 1 x 6912 x 2560 5.3 and 6.4 us, 4 x 6912 x 2560 5.9 and 6.7, 1 x 2560 x 6912 5.3 and
+  // 7.2, 4 x 2560 x 6912 7.1 and 7.9, 2 of 16 experts 6912 x 2560 7.0 and 7.5; 1 x 28672 x 8192 16.2 and 15.9, 4 x 8192 x
+  // 28672 20.1 and 16.0).
+  if (src && T <= 4 && K % 8 == 0 && some * (double)(blocks * chunks) <= 10000) {
+    const double rows = std::ceil((double)T / some);
+    const int waves = (int)std::min<int64_t>(std::min<int64_t>(16, chunks), (int64_t)std::ceil((double)chunks * rows / 3.5));
+    const int64_t lds = few_lds(waves, T, K);
+    if (lds <= kFewLds) {
+      p.kernel = kFewKernel, p.height = 16, p.per = 1, p.quantizes = true;
+      p.threads = 64 * waves;
+      p.lds = lds;
+    }
+  }
+  if (p.kernel != kGemmKernel) p.width = 16 * p.per;
+  p.groups = (N + p.width - 1) / p.width * (E ? most_units(E, T, p.height) : (T + p.height - 1) / p.height);
   return p;
 }
 
 hipError_t launch_experts(const Groups& g, const void* X, int src, const int8_t* Xq, const float* absmax,
                           const Epilogue& ep, hipStream_t s) {
-  const int chunks = (int)(k_pad(g.K) / kTileCols);
-  const int64_t nblocks = n_pad(g.N) / kTileRows;
   const ExpertsPlan p = plan_experts(g.offsets ? g.E : 0, g.T, g.N, g.K, src);
   if (p.kernel == kGemmKernel) return launch_experts_gemm(p, g, Xq, absmax, ep, s);
-  k_experts<<<dim3((unsigned)p.groups), p.threads, 0, s>>>(g, Xq, absmax, ep, chunks, nblocks, (int)((nblocks + 3) / 4));
-  return hipGetLastError();
+  if (p.kernel == kMidKernel) return launch_experts_mid(p, g, Xq, absmax, ep, s);
+  return launch_experts_few(p, g, X, src, ep, s);
 }
 
 hipError_t launch_combine(const Groups& g, const float* H, const int32_t* slots, const float* weights, int64_t M, int k,

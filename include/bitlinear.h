@@ -380,14 +380,14 @@ typedef struct {
  *         type); no other buffers of one call may overlap.
  * Errors: BL_ERR_INVALID_ARG for null pointers, sizes, misaligned pointers, row distances below
  * N and an unknown act; BL_ERR_UNSUPPORTED for other types and for launches that are too large
- * (M and N of more than 2^31 tiles of 16 x 64).
+ * (M or N beyond 2^31 - 4096, 2^31 tiles of 16 x 16, matrices of 2^40 bytes).
  */
 int bitlinear_forward_epilogue(const uint8_t* packed, const float* gamma, const void* X, int dt, int8_t* Xq,
                                float* absmax, int64_t M, int64_t N, int64_t K, const bl_epilogue* ep, void* stream);
 
 /*
  * Host-only: the launches of bitlinear_forward_epilogue for (M, N, K) and x of type xdt (-1: codes).
- * out[0] = kernel (10: plain, 11: GEMM), out[1] = its workgroups, out[2] = threads per workgroup, out[3] and out[4] =
+ * out[0] = kernel (10: decode with the quantiser, 11: GEMM, 12: decode), out[1] = its workgroups, out[2] = threads per workgroup, out[3] and out[4] =
  * token rows and outputs of a workgroup at a time, out[5] = launches (2: the quantiser first).
  * Returns BL_OK, BL_ERR_INVALID_ARG or BL_ERR_UNSUPPORTED as the call does.
  */
@@ -417,7 +417,7 @@ typedef struct {
  * Slots outside offsets[0] .. offsets[E] - 1, and those whose row is not in 0 .. R - 1, are left
  * out: their rows of Y stay as they were.  (Offsets that break their rule give unspecified rows of
  * Y, and touch nothing else.)
- *   Limits: E <= 4096 and T <= 2^31 - 4096 (BL_ERR_UNSUPPORTED beyond), 1 <= T, R < 2^31.
+ *   Limits: E <= 4096, T and N <= 2^31 - 4096 (BL_ERR_UNSUPPORTED beyond), 1 <= T, R < 2^31.
  */
 int bitlinear_forward_experts(const bl_experts* experts, const void* X, int dt, int8_t* Xq, float* absmax, int64_t R,
                               int64_t K, const bl_epilogue* ep, void* stream);

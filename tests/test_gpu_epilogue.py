@@ -152,3 +152,39 @@ def test_graph_replays_and_other_stream(m):
         q, a = ref.quantize(new)
         ref.check(y, *ref.product(q, a, q_w, gamma, b, "silu"), f"replay {i}")
         assert torch.equal(y, bl.forward_epilogue(packed, gm, x, n, k, bias=bd, act="silu"))
+
+
+def exact_on_gpu(q_w, q, a, gamma):
+    """The products of codes in 64 bits on the GPU (whole numbers: exact), and the allowed error."""
+    raw = (q.to(DEV).double() @ q_w.to(DEV).double().t().contiguous()) * (a.to(DEV) * float(gamma) / 127)[:, None]
+    return raw, 3.01 * ref.U * raw.abs()
+
+
+FORMS = [(1, 700, 1280, "bf16"), (4, 301, 2568, "f32"), (1, 64, 90000, "bf16"), (2, 64, 40000, "f32"), (4, 300, 40000, "f32"),
+         (3, 65, 2571, "f32"), (9, 200, 700, "i8"), (9, 4500, 600, "i8"), (33, 9000, 300, "i8"), (1500, 1000, 512, "i8"),
+         (1247, 1641, 635, "i8"), (65, 19498, 300, "i8"), (200, 6917, 2560, "i8"), (300, 300, 300, "i8"), (133, 15252, 33, "i8"),
+         (700, 3000, 1000, "i8"), (1500, 6900, 1100, "i8"), (6090, 526, 34, "i8"), (2050, 6912, 600, "i8"), (13197, 345, 33, "i8")]
+
+
+def test_every_form_is_tested():
+    plans = [bl.forward_epilogue_plan(m, n, k, None if x == "i8" else x) for m, n, k, x in FORMS]
+    seen = {(p["kernel"], p["rows"], p["outputs"]) for p in plans}
+    assert {("fused", 16, 16), ("decode", 16, 16), ("decode", 16, 32), ("decode", 16, 64), ("decode", 32, 64)} <= seen
+    assert {("gemm", h, w) for h, w in ((32, 128), (64, 128), (64, 256), (96, 256), (128, 256))} <= seen, seen
+    assert {p["launches"] for p in plans} == {1, 2}
+
+
+@pytest.mark.parametrize("form", FORMS, ids=str)
+def test_forms(form):
+    m, n, k, x = form
+    q_w, xv, gamma, _, _ = make(m, n, k, "f32" if x == "i8" else x)
+    arg, absmax = codes_of(xv) if x == "i8" else (xv.to(DEV), None)
+    q, a = ref.quantize(xv)
+    packed, gm = ref.pack(q_w).to(DEV), gamma.to(DEV)
+    raw, err = exact_on_gpu(q_w, q, a, gamma)
+    y = bl.forward_epilogue(packed, gm, arg, n, k, absmax=absmax)
+    assert ((y.double() - raw).abs() <= err).all()
+    r = torch.randn(m, n, device=DEV, dtype=torch.bfloat16)
+    y = bl.forward_epilogue(packed, gm, arg, n, k, absmax=absmax, act="relu", residual=r, out_dtype=torch.bfloat16)
+    v = raw.clamp(min=0) + r.double()
+    assert ((y.double() - v).abs() <= err + 1.01 * (2.0 ** -8 + ref.U) * v.abs() + 2 * ref.U * raw.abs()).all()
