@@ -1276,19 +1276,23 @@ def _tokens(rt, x, k: int, absmax, e: int, t, n: int):
         raise ValueError("x must be [tokens, K]")
     if n < 1 or _products_plan(e, r if t is None else t, n, k, dt)[5] == 1:
         return x.data_ptr(), dt, None, None, r, None
-    xq = rt.empty(r, (k + 255) // 256 * 256, dtype=rt.i8, device=x.device)
-    a = rt.empty(r, dtype=rt.f32, device=x.device)
-    return x.data_ptr(), dt, xq.data_ptr(), a.data_ptr(), r, (xq, a)
+    codes = r * ((k + 255) // 256 * 256)
+    scratch = rt.empty(codes + 4 * r, dtype=rt.u8, device=x.device)  # the codes, then the scales
+    at = scratch.data_ptr()
+    return x.data_ptr(), dt, at, at + codes, r, scratch
 
 
 def _epilogue(rt, y, out_dtype, rows: int, n: int, like, bias, bias_shape, act: str, residual):
     """(y, its bl_epilogue)."""
     dev = like.get_device()
     if y is None:
-        y = rt.empty(rows, max(n, 0), dtype=out_dtype or rt.f32, device=like.device)
-    elif out_dtype is not None and y.dtype != out_dtype:
-        raise ValueError(f"y must be {out_dtype}")
-    ydt, yld = _strided(rt, y, "y", rows, n, dev)
+        dtype = out_dtype or rt.f32
+        ydt, yld = _dtype_code(rt, dtype, "out_dtype"), 0
+        y = rt.empty(rows, max(n, 0), dtype=dtype, device=like.device)
+    else:
+        if out_dtype is not None and y.dtype != out_dtype:
+            raise ValueError(f"y must be {out_dtype}")
+        ydt, yld = _strided(rt, y, "y", rows, n, dev)
     rdt, rld, rptr = 0, 0, None
     if residual is not None:
         rdt, rld = _strided(rt, residual, "residual", rows, n, dev)
@@ -1363,6 +1367,7 @@ def forward_experts(packed, gamma, offsets, x, n: int, k: int, rows=None, absmax
     return y
 
 
+@functools.lru_cache(maxsize=4096)
 def forward_experts_combine_ws_bytes(t: int, n: int) -> int:
     """Workspace bytes of forward_experts_combine for T slots of N outputs."""
     v = int(lib().bitlinear_forward_experts_combine_ws_bytes(t, n))
@@ -1405,6 +1410,7 @@ class Route(NamedTuple):
     slots: object
 
 
+@functools.lru_cache(maxsize=4096)
 def route_experts_ws_bytes(m: int, e: int) -> int:
     """Workspace bytes of route_experts for M tokens and E experts (0: none)."""
     v = int(lib().bitlinear_route_experts_ws_bytes(m, e))
@@ -1424,12 +1430,14 @@ def route_experts(logits, k: int, renormalize: bool = True, out: Route = None, w
     if out is None:
         if not 0 < k <= e:
             raise ValueError(f"k must be 1 .. {e}")
-        new = functools.partial(rt.empty, device=logits.device)
-        out = Route(new(m, k, dtype=rt.i32), new(m, k, dtype=rt.f32), new(e + 1, dtype=rt.i32),
-                    new(m * k, dtype=rt.i32), new(m, k, dtype=rt.i32))
-    ptrs = (_vector(rt, out.experts, "experts", (m, k), rt.i32, dev), _vector(rt, out.weights, "weights", (m, k), rt.f32, dev),
-            _vector(rt, out.offsets, "offsets", (e + 1,), rt.i32, dev), _vector(rt, out.rows, "rows", (m * k,), rt.i32, dev),
-            _vector(rt, out.slots, "slots", (m, k), rt.i32, dev))
+        new, on = rt.empty, logits.device
+        out = Route(new(m, k, dtype=rt.i32, device=on), new(m, k, dtype=rt.f32, device=on),
+                    new(e + 1, dtype=rt.i32, device=on), new(m * k, dtype=rt.i32, device=on),
+                    new(m, k, dtype=rt.i32, device=on))
+        ptrs = [t.data_ptr() for t in out]
+    else:
+        ptrs = [_vector(rt, t, name, shape, dtype, dev) for t, name, shape, dtype in zip(
+            out, Route._fields, ((m, k), (m, k), (e + 1,), (m * k,), (m, k)), (rt.i32, rt.f32, rt.i32, rt.i32, rt.i32))]
     need = route_experts_ws_bytes(m, e)
     if workspace is not None:
         _bytes_at_least(rt, workspace, "workspace", need, dev)

@@ -96,23 +96,24 @@ int products_ok(const bl::Groups& g, const void* X, int dt, const int8_t* Xq, co
 // The products, behind the quantiser where X is given and the kernel does not take it itself.
 int products(const bl::Groups& g, const void* X, int dt, int8_t* Xq, float* absmax, const bl::Epilogue& ep,
              hipStream_t s) {
+  const int64_t E = g.offsets ? g.E : 0;
   int src = X ? mx_src(dt) : 0;
-  if (X && !bl::plan_experts(g.offsets ? g.E : 0, g.T, g.N, g.K, src).quantizes) {
+  bl::ExpertsPlan p = bl::plan_experts(E, g.T, g.N, g.K, src);
+  if (src && !p.quantizes) {
     if (!Xq || !absmax) return BL_ERR_INVALID_ARG;
     const hipError_t e = bl::launch_act_quant(X, dt == BL_BF16, g.R, g.K, Xq, absmax, s);
     if (e != hipSuccess) return BL_ERR_HIP;
-    src = 0;
+    src = 0;  // (the plan is the one for codes)
   }
-  return hip_status(bl::launch_experts(g, X, src, Xq, absmax, ep, s));
+  return hip_status(bl::launch_experts(p, g, X, src, Xq, absmax, ep, s));
 }
 
 int products_plan(int64_t E, int64_t T, int64_t N, int64_t K, int xdt, int32_t out[6]) {
   if (!out || !rows_ok(T, K) || !rows_ok(N, K)) return BL_ERR_INVALID_ARG;
   if (xdt != -1 && !dtype_ok(xdt)) return BL_ERR_UNSUPPORTED;
   if (!products_countable(E ? E : 1, T, N, K)) return BL_ERR_UNSUPPORTED;
-  bl::ExpertsPlan p = bl::plan_experts(E, T, N, K, xdt == -1 ? 0 : mx_src(xdt));
+  const bl::ExpertsPlan p = bl::plan_experts(E, T, N, K, xdt == -1 ? 0 : mx_src(xdt));
   const bool one = xdt == -1 || p.quantizes;
-  if (!one) p = bl::plan_experts(E, T, N, K, 0);
   out[0] = p.kernel, out[1] = (int32_t)p.groups, out[2] = p.threads, out[3] = p.height, out[4] = p.width;
   out[5] = one ? 1 : 2;
   return BL_OK;

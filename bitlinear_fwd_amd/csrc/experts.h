@@ -267,10 +267,10 @@ struct ExpertsPlan {
 };
 // src: 0 codes, 1 bf16 x, 2 fp32 x
 ExpertsPlan plan_experts(int64_t E, int64_t T, int64_t N, int64_t K, int src);
-// The products of every slot; sizes and pointers are validated by the C ABI.  X: where the plan for src
-// says that the kernel quantises.
-hipError_t launch_experts(const Groups& g, const void* X, int src, const int8_t* Xq, const float* absmax,
-                          const Epilogue& ep, hipStream_t s);
+// The products of every slot by a plan for these sizes and src; sizes and pointers are validated by the C ABI.  X:
+// where the plan says that the kernel quantises.
+hipError_t launch_experts(const ExpertsPlan& p, const Groups& g, const void* X, int src, const int8_t* Xq,
+                          const float* absmax, const Epilogue& ep, hipStream_t s);
 
 // LDS of the kernel for few slots: the waves' sums and the codes of `rows` token rows; a compute unit has kFewLds.
 constexpr int kFewLds = 160 * 1024;

@@ -87,7 +87,7 @@ ExpertsPlan plan_experts(int64_t E, int64_t T, int64_t N, int64_t K, int src) {
   // 7.2, 4 x 2560 x 6912 7.1 and 7.9, 2 of 16 experts 6912 x 2560 7.0 and 7.5; 1 x 28672 x 8192 16.2 and 15.9, 4 x 8192 x
   // 28672 20.1 and 16.0).
   if (src && T <= 4 && K % 8 == 0 && some * (double)(blocks * chunks) <= 10000) {
-    const double rows = std::ceil((double)T / some);
+    const double rows = E ? std::round((double)T / some) : (double)T;
     const int waves = (int)std::min<int64_t>(std::min<int64_t>(16, chunks), (int64_t)std::ceil((double)chunks * rows / 3.5));
     const int64_t lds = few_lds(waves, T, K);
     if (lds <= kFewLds) {
@@ -101,9 +101,8 @@ ExpertsPlan plan_experts(int64_t E, int64_t T, int64_t N, int64_t K, int src) {
   return p;
 }
 
-hipError_t launch_experts(const Groups& g, const void* X, int src, const int8_t* Xq, const float* absmax,
-                          const Epilogue& ep, hipStream_t s) {
-  const ExpertsPlan p = plan_experts(g.offsets ? g.E : 0, g.T, g.N, g.K, src);
+hipError_t launch_experts(const ExpertsPlan& p, const Groups& g, const void* X, int src, const int8_t* Xq,
+                          const float* absmax, const Epilogue& ep, hipStream_t s) {
   if (p.kernel == kGemmKernel) return launch_experts_gemm(p, g, Xq, absmax, ep, s);
   if (p.kernel == kMidKernel) return launch_experts_mid(p, g, Xq, absmax, ep, s);
   return launch_experts_few(p, g, X, src, ep, s);
