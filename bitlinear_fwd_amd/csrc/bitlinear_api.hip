@@ -336,7 +336,8 @@ int bitlinear_forward_experts(const bl_experts* experts, const void* X, int dt, 
 }
 
 int64_t bitlinear_forward_experts_combine_ws_bytes(int64_t T, int64_t N) {
-  return T < 1 || N < 1 || T >= kMaxDim || N >= kMaxDim || T > kMaxCount / N ? -1 : T * N * 4;
+  return T < 1 || N < 1 || T >= kMaxDim || N >= kMaxDim || T > kMaxCount / bl::combine_ld(N) ? -1
+                                                                                             : T * bl::combine_ld(N) * 4;
 }
 
 int bitlinear_forward_experts_combine(const bl_experts* experts, const void* X, int dt, int8_t* Xq, float* absmax,
@@ -357,7 +358,7 @@ int bitlinear_forward_experts_combine(const bl_experts* experts, const void* X, 
   e = out;  // the slots' own: fp32 rows in the workspace, the residual comes with the sum
   e.residual = nullptr;
   e.Y = workspace;
-  e.ldy = g.N;
+  e.ldy = bl::combine_ld(g.N);
   e.y_bf16 = 0;
   e.stream = 0;  // read again at once
   hipStream_t s = static_cast<hipStream_t>(stream);

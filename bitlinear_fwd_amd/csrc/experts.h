@@ -17,7 +17,7 @@ struct Epilogue {
   int64_t ldr, ldy;      // elements between rows
   int act;               // bl_activation
   int res_bf16, y_bf16;
-  int stream;            // rows of Y and the pieces of 16 bytes in them are aligned
+  int stream;            // Y is written past the caches: its rows and their pieces of 16 bytes are aligned
 };
 
 // The matrices and which rows each of them takes.
@@ -205,7 +205,8 @@ __device__ __forceinline__ void store4(void* base, int64_t at, int left, int bf1
 // A token's scale: the exact products are multiplied by gamma a / 127.
 __device__ __forceinline__ float token_scale(float gamma, float a) { return gamma * a / 127.0f; }
 
-// 4 H consecutive values at element `at`; and the same to Y, past the caches (whole aligned pieces of 16 bytes).
+// 4 H consecutive values at element `at`; and the same to Y, past the caches where its pieces of 16 bytes are aligned
+// (2048 x 6912 fp32 outputs of MXFP4 products: 30.3 us without, 26.4 so).
 template <typename H>
 __device__ __forceinline__ void load_row(const void* base, int64_t at, int bf16, v4f* v, H) {
   if (bf16) {
@@ -218,14 +219,13 @@ __device__ __forceinline__ void load_row(const void* base, int64_t at, int bf16,
   }
 }
 template <typename H>
-__device__ __forceinline__ void stream_row(const Epilogue& ep, int64_t at, const v4f* v, H) {
-  if constexpr (H::value == 2) {
-    const v4u w = {bf16_pair(v[0][0], v[0][1]), bf16_pair(v[0][2], v[0][3]), bf16_pair(v[1][0], v[1][1]),
-                   bf16_pair(v[1][2], v[1][3])};
-    __builtin_nontemporal_store(w, reinterpret_cast<v4u*>(static_cast<uint16_t*>(ep.Y) + at));
-  } else {
-    __builtin_nontemporal_store(__builtin_bit_cast(v4u, v[0]), reinterpret_cast<v4u*>(static_cast<float*>(ep.Y) + at));
-  }
+__device__ __forceinline__ void store_row(const Epilogue& ep, int64_t at, const v4f* v, H) {
+  v4u w = __builtin_bit_cast(v4u, v[0]);
+  if constexpr (H::value == 2)
+    w = v4u{bf16_pair(v[0][0], v[0][1]), bf16_pair(v[0][2], v[0][3]), bf16_pair(v[1][0], v[1][1]), bf16_pair(v[1][2], v[1][3])};
+  char* y = static_cast<char*>(ep.Y) + at * (H::value == 2 ? 2 : 4);
+  if (ep.stream) __builtin_nontemporal_store(w, reinterpret_cast<v4u*>(y));
+  else __builtin_memcpy(y, &w, 16);
 }
 
 // The end of the epilogue: residual, rounding and store of 4 H consecutive outputs n .. of row s (left of them before
@@ -282,7 +282,9 @@ hipError_t launch_experts_mid(const ExpertsPlan& p, const Groups& g, const int8_
 hipError_t launch_experts_gemm(const ExpertsPlan& p, const Groups& g, const int8_t* Xq, const float* absmax,
                                const Epilogue& ep, hipStream_t s);
 
-// Y[m] = residual[m] + sum over j of weights[m][j] H[slots[m][j]], H fp32 [T][N] the products of the
+// Elements between the rows of H below.
+inline int64_t combine_ld(int64_t N) { return (N + 3) / 4 * 4; }
+// Y[m] = residual[m] + sum over j of weights[m][j] H[slots[m][j]], H fp32 [T][combine_ld(N)] the products of the
 // slots.  Slots that no group holds or that have no token row are left out.
 hipError_t launch_combine(const Groups& g, const float* H, const int32_t* slots, const float* weights, int64_t M, int k,
                           const Epilogue& ep, hipStream_t s);

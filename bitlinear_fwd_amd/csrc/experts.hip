@@ -22,7 +22,7 @@ __global__ __launch_bounds__(256) void k_combine(Groups g, const float* __restri
   for (int j = 0; j < k; ++j) {
     const int s = slots[m * k + j];
     if (s < first || s >= last || slot_row(g, s) < 0) continue;
-    const v4f h = load4(H, (int64_t)s * g.N + n, left, 0);
+    const v4f h = *reinterpret_cast<const v4f*>(H + (int64_t)s * (4 * quads) + n);  // (columns past N: not stored)
     const float w = weights[m * k + j];
 #pragma unroll
     for (int q = 0; q < 4; ++q) v[q] = __builtin_fmaf(w, h[q], v[q]);

@@ -214,7 +214,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     constexpr bool bf16 = decltype(kind)::value;
     constexpr int per = bf16 ? 8 : 4, pieces = 32 * TN / per, rows = 64 / pieces;  // rows: of a wave's stores
     constexpr int H = per / 4;
-    const bool whole = ep.stream && n0 + 32 * TN <= g.N;
+    const bool whole = n0 + 32 * TN <= g.N;
     const int o = lane % pieces * per, left = (int)min(g.N - n0 - o, (int64_t)per);
     v4f b[per / 4];
 #pragma unroll
@@ -240,33 +240,40 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
             *reinterpret_cast<v4i*>(slab + (16 * h + lr) * kRow + 4 * (16 * i + 4 * lq)) = acc[i][2 * decltype(jj)::value + h];
       });
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // a wave's own writes, read by its other lanes
-      if (whole && there == ~0u) {  // no column and no row is missing: without a branch
+      if (whole) {  // no column is missing: rows at once, and no branch but for rows that are not there
         const Epilogue& e = ep;
-        constexpr int kIt = 32 / rows;
-        const int64_t s0 = slot0 + lane / pieces;
-        v4f v[kIt * H], r4[kIt * H];
-        if (e.residual) {
+        constexpr int kIt = 16 / rows;  // in two halves: registers
+#pragma unroll 1
+        for (int r0 = lane / pieces; r0 < 32; r0 += 16) {
+          const int64_t s0 = slot0 + r0;
+          v4f v[kIt * H], r4[kIt * H];
+          if (e.residual) {
 #pragma unroll
-          for (int k = 0; k < kIt; ++k) load_row(e.residual, (s0 + k * rows) * e.ldr + n0 + o, e.res_bf16, &r4[k * H], std::integral_constant<int, H>{});
-        }
-#pragma unroll
-        for (int k = 0; k < kIt; ++k) {
-          const uint8_t* row = slab + (lane / pieces + k * rows) * kRow;
-          const float f = *reinterpret_cast<const float*>(row + 128 * TN);
-#pragma unroll
-          for (int h = 0; h < H; ++h) {
-            const v4i a = *reinterpret_cast<const v4i*>(row + 4 * o + 16 * h);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) v[k * H + h][q] = __builtin_fmaf((float)a[q], f, b[h][q]);
+            for (int k = 0; k < kIt; ++k)
+              if (there >> (r0 + k * rows) & 1)
+                load_row(e.residual, (s0 + k * rows) * e.ldr + n0 + o, e.res_bf16, &r4[k * H], std::integral_constant<int, H>{});
           }
-        }
-        activate_all(v, e.act);
-        if (e.residual) {
 #pragma unroll
-          for (int k = 0; k < kIt * H; ++k) v[k] += r4[k];
-        }
+          for (int k = 0; k < kIt; ++k) {
+            const uint8_t* row = slab + (r0 + k * rows) * kRow;
+            const float f = *reinterpret_cast<const float*>(row + 128 * TN);
 #pragma unroll
-        for (int k = 0; k < kIt; ++k) stream_row(e, (s0 + k * rows) * e.ldy + n0 + o, &v[k * H], std::integral_constant<int, H>{});
+            for (int h = 0; h < H; ++h) {
+              const v4i a = *reinterpret_cast<const v4i*>(row + 4 * o + 16 * h);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) v[k * H + h][q] = __builtin_fmaf((float)a[q], f, b[h][q]);
+            }
+          }
+          activate_all(v, e.act);
+          if (e.residual) {
+#pragma unroll
+            for (int k = 0; k < kIt * H; ++k) v[k] += r4[k];
+          }
+#pragma unroll
+          for (int k = 0; k < kIt; ++k)
+            if (there >> (r0 + k * rows) & 1)
+              store_row(e, (s0 + k * rows) * e.ldy + n0 + o, &v[k * H], std::integral_constant<int, H>{});
+        }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         continue;
       }

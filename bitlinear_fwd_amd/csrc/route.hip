@@ -19,17 +19,41 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / 64;
 
-// A logit as an integer of the same order; 0: never chosen (-inf, NaN).  +inf counts as the largest
-// finite number, -0 as 0, so that numbers that are equal have equal keys.
+// A logit as an integer of the same order; 0: never chosen (-inf, NaN).  +inf counts as the largest finite number, -0 as 0,
+// so that numbers that are equal have equal keys.
 __device__ __forceinline__ uint32_t key_of(float x) {
   if (!(x > -__builtin_inff())) return 0;
-  x = fminf(x, 3.402823466e38f) + 0.0f;
-  const uint32_t b = __float_as_uint(x);
+  const uint32_t b = __float_as_uint(fminf(x, 3.402823466e38f) + 0.0f);
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 __device__ __forceinline__ float value_of(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
 }
+
+// A logit's key and, below it, its index turned round, so that of equal logits the one with the lowest index is the
+// largest.  A bf16 logit's key has 16 bits: both fit 32.
+template <typename T>
+struct Entry {
+  using Type = uint64_t;
+  static __device__ __forceinline__ Type make(T x, bool there, int e) {
+    return (uint64_t)(there ? key_of(x) : 0u) << 32 | (uint32_t)~e;
+  }
+  static __device__ __forceinline__ bool any(Type x) { return x >> 32; }
+  static __device__ __forceinline__ float value(Type x) { return value_of((uint32_t)(x >> 32)); }
+  static __device__ __forceinline__ int index(Type x) { return (int)~(uint32_t)x; }
+};
+template <>
+struct Entry<uint16_t> {
+  using Type = uint32_t;
+  static __device__ __forceinline__ Type make(uint16_t x, bool there, int e) {
+    return (there ? key_of(bf16_float(x)) & 0xffff0000u : 0u) | (0xffffu - (uint32_t)e);
+  }
+  static __device__ __forceinline__ bool any(Type x) { return x >> 16; }
+  static __device__ __forceinline__ float value(Type x) {  // the key of a negative number ends in ones
+    return value_of(x & 0x80000000u ? x & 0xffff0000u : x | 0xffffu);
+  }
+  static __device__ __forceinline__ int index(Type x) { return (int)(0xffffu - (x & 0xffffu)); }
+};
 
 // Over each row of 16 lanes, in every lane of it.
 __device__ __forceinline__ uint32_t row_max(uint32_t v) {
@@ -57,6 +81,11 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
   return max(max(a, b), max(c, d));
 }
 template <int G>
+__device__ __forceinline__ uint64_t lanes_max(uint64_t v) {
+  const uint32_t high = (uint32_t)(v >> 32), top = lanes_max<G>(high);
+  return (uint64_t)top << 32 | lanes_max<G>(high == top ? (uint32_t)v : 0u);
+}
+template <int G>
 __device__ __forceinline__ float lanes_sum(float v) {
   v = row_sum(v);
   if constexpr (G == 16) return v;
@@ -64,75 +93,84 @@ __device__ __forceinline__ float lanes_sum(float v) {
   return (at(0) + at(16)) + (at(32) + at(48));
 }
 
-// The choices of token m, by G lanes with V consecutive logits each.  Lane j of them returns the j-th
-// choice (-1: none) in `id` and its weight.
-template <int G, int V>
-__device__ __forceinline__ void choose(const RouteArgs& a, int64_t m, bool live, int& id, float& weight) {
-  const int lane = threadIdx.x & 63, l = lane % G;
-  uint32_t key[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = l * V + v;
-    key[v] = 0;
-    if (live && e < a.E)
-      key[v] = key_of(a.bf16 ? bf16_float(static_cast<const uint16_t*>(a.logits)[m * a.E + e])
-                             : static_cast<const float*>(a.logits)[m * a.E + e]);
-  }
-  // the lane's largest, at its lowest place
-  uint32_t best = 0;
-  int at = 0;
-  auto pick = [&]() {
-    best = key[0];
-    at = 0;
-#pragma unroll
-    for (int v = 1; v < V; ++v)
-      if (key[v] > best) best = key[v], at = v;
+// Descending order of a lane's V entries (Batcher's odd-even merge sort).
+template <typename X, int V>
+__device__ __forceinline__ void sort_entries(X (&x)[V]) {
+  auto order = [&](int i, int j) {
+    const X a = x[i], b = x[j];
+    x[i] = max(a, b);
+    x[j] = min(a, b);
   };
-  pick();
-  const uint32_t peak_key = lanes_max<G>(best);
-  const float peak = peak_key ? value_of(peak_key) : 0.0f;
+#pragma unroll
+  for (int p = 1; p < V; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < V; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < V && (i + j) / (2 * p) == (i + j + k) / (2 * p)) order(i + j, i + j + k);
+}
+
+// The choices of a token, by G lanes with V consecutive logits each.  Lane j of them returns the j-th choice (-1: none)
+// in `id` and its weight.  Each lane sorts its entries, and each choice is the largest of the lanes' first.
+template <typename T, int G, int V>
+__device__ __forceinline__ void choose(const RouteArgs& a, const T (&raw)[V], bool live, int& id, float& weight) {
+  using E = Entry<T>;
+  using X = typename E::Type;
+  const int l = (threadIdx.x & 63) % G;
+  X x[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) x[v] = E::make(raw[v], live && l * V + v < a.E, l * V + v);
+  sort_entries(x);
+  X top = lanes_max<G>(x[0]), mine = 0;  // mine: choice l
+  const float peak = E::any(top) ? E::value(top) : 0.0f;
   float total = 0.0f;
   if (!a.renorm) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) total += key[v] ? exp_of(value_of(key[v]) - peak) : 0.0f;
+    for (int v = 0; v < V; ++v) total += E::any(x[v]) ? exp_of(E::value(x[v]) - peak) : 0.0f;
     total = lanes_sum<G>(total);
   }
-  id = -1;
-  uint32_t mine = 0;  // the key of choice l
   for (int j = 0; j < a.k; ++j) {
-    const uint32_t top = j ? lanes_max<G>(best) : peak_key;
-    uint64_t holders = __ballot(best == top);
-    int first;  // lane that holds it
-    if constexpr (G == 64) {
-      first = __builtin_ctzll(holders);
-    } else {
-      holders = holders >> (lane & 48) & 0xffff;
-      first = (lane & 48) + __builtin_ctzll(holders);
-    }
-    const int where = G == 64 ? __builtin_amdgcn_readlane(at, first) : __shfl(at, first, 64);
-    if (l == j && top) id = (first % G) * V + where, mine = top;
-    if (lane == first) {
+    if (j) top = lanes_max<G>(x[0]);
+    if (l == j) mine = top;
+    const bool taken = x[0] == top;
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (v == at) key[v] = 0;
-      pick();
-    }
+    for (int v = 0; v < V; ++v) x[v] = !taken ? x[v] : v + 1 < V ? x[v + 1 < V ? v + 1 : v] : 0;
   }
-  const float p = mine ? exp_of(value_of(mine) - peak) : 0.0f;
+  const bool have = E::any(mine);
+  const float p = have ? exp_of(E::value(mine) - peak) : 0.0f;
   if (a.renorm) total = lanes_sum<G>(p);
-  weight = mine ? p / total : 0.0f;
+  id = have ? E::index(mine) : -1;
+  weight = have ? p / total : 0.0f;
 }
 
 // Choices and weights of the tokens [m0, m1), and how often each expert was chosen into `count` (LDS).
-template <int G, int V>
+template <typename T, int G, int V>
 __device__ __forceinline__ void choose_chunk(const RouteArgs& a, int64_t m0, int64_t m1, int32_t* count) {
   constexpr int kPer = 64 / G;  // tokens of a wave
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = lane % G;
+  // the lane's logits of token m (past the last: the last again; past column E: anything)
+  auto fetch = [&](int64_t m, T (&raw)[V]) {
+    const T* p = static_cast<const T*>(a.logits) + min(m, m1 - 1) * a.E;
+    if (l * V + V <= a.E) {
+      __builtin_memcpy(raw, p + l * V, V * sizeof(T));
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) raw[v] = p[min(l * V + v, a.E - 1)];
+    }
+  };
+  T next[V];
+  fetch(m0 + wave * kPer + lane / G, next);
   for (int64_t m = m0 + wave * kPer; m < m1; m += (blockDim.x >> 6) * kPer) {
     const int64_t mine = m + lane / G;
+    T raw[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) raw[v] = next[v];
+    fetch(mine + (blockDim.x >> 6) * kPer, next);
     int id;
     float w;
-    choose<G, V>(a, mine, mine < m1, id, w);
+    choose<T, G, V>(a, raw, mine < m1, id, w);
     if (mine < m1 && l < a.k) {
       a.experts[mine * a.k + l] = id;
       a.weights[mine * a.k + l] = w;
@@ -239,24 +277,24 @@ __device__ __forceinline__ void place_chunk(const RouteArgs& a, int c, int chunk
   }
 }
 
-template <int G, int V>
+template <typename T, int G, int V>
 __global__ __launch_bounds__(kThreads) void k_route_one(RouteArgs a) {
   extern __shared__ int32_t lds[];  // [waves][E], [E + 1]
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) lds[e] = 0;
   __syncthreads();
-  choose_chunk<G, V>(a, 0, a.M, lds);
+  choose_chunk<T, G, V>(a, 0, a.M, lds);
   __threadfence_block();  // the choices are read again by other waves
   __syncthreads();
   place_chunk(a, 0, 1, 0, a.M * a.k, lds, lds + (blockDim.x >> 6) * a.E);
 }
 
-template <int G, int V>
+template <typename T, int G, int V>
 __global__ __launch_bounds__(kThreads) void k_route_top(RouteArgs a, int chunk) {
   extern __shared__ int32_t lds[];  // [E]
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) lds[e] = 0;
   __syncthreads();
   const int64_t m0 = (int64_t)blockIdx.x * chunk;
-  choose_chunk<G, V>(a, m0, min(m0 + chunk, a.M), lds);
+  choose_chunk<T, G, V>(a, m0, min(m0 + chunk, a.M), lds);
   __syncthreads();
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.counts[(int64_t)blockIdx.x * a.E + e] = lds[e];
 }
@@ -267,14 +305,14 @@ __global__ __launch_bounds__(kThreads) void k_route_place(RouteArgs a, int chunk
   place_chunk(a, blockIdx.x, gridDim.x, m0 * a.k, min(m0 + chunk, a.M) * a.k, lds, lds + (blockDim.x >> 6) * a.E);
 }
 
-template <int G, int V>
+template <typename T, int G, int V>
 hipError_t launch(const RouteArgs& a, const RoutePlan& p, hipStream_t s) {
   const size_t lds = (size_t)((kWaves + 1) * a.E + 1) * 4;
   if (p.chunks == 1) {
-    k_route_one<G, V><<<1, kThreads, lds, s>>>(a);
+    k_route_one<T, G, V><<<1, kThreads, lds, s>>>(a);
     return hipGetLastError();
   }
-  k_route_top<G, V><<<p.chunks, kThreads, (size_t)a.E * 4, s>>>(a, p.chunk);
+  k_route_top<T, G, V><<<p.chunks, kThreads, (size_t)a.E * 4, s>>>(a, p.chunk);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   k_route_place<<<p.chunks, kThreads, lds, s>>>(a, p.chunk);
@@ -296,11 +334,22 @@ RoutePlan plan_route(int64_t M, int64_t E) {
 
 hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
   const RoutePlan p = plan_route(a.M, a.E);
-  if (a.E <= 16 && a.k <= 16) return launch<16, 1>(a, p, s);
-  if (a.E <= 64) return launch<64, 1>(a, p, s);
-  if (a.E <= 128) return launch<64, 2>(a, p, s);
-  if (a.E <= 256) return launch<64, 4>(a, p, s);
-  return launch<64, 8>(a, p, s);
+  auto go = [&](auto g, auto v) {
+    constexpr int G = decltype(g)::value, V = decltype(v)::value;
+    return a.bf16 ? launch<uint16_t, G, V>(a, p, s) : launch<float, G, V>(a, p, s);
+  };
+  const std::integral_constant<int, 1> one;
+  const std::integral_constant<int, 2> two;
+  const std::integral_constant<int, 4> four;
+  const std::integral_constant<int, 8> eight;
+  const std::integral_constant<int, 16> row;
+  const std::integral_constant<int, 64> wave;
+  if (a.E <= 16) return go(row, one);
+  if (a.E <= 32) return go(row, two);
+  if (a.E <= 64) return go(row, four);
+  if (a.E <= 128) return go(row, eight);
+  if (a.E <= 256) return go(wave, four);
+  return go(wave, eight);
 }
 
 }  // namespace bl

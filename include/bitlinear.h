@@ -445,7 +445,7 @@ int bitlinear_forward_experts_combine(const bl_experts* experts, const void* X, 
  * The router: the k largest of each token's E logits, in falling order (of equal ones the lowest
  * index first), their weights, and the slots ordered by expert, then token.
  *   logits  [M][E] fp32 or bf16 (dt).  -inf and NaN are never chosen, +inf counts as the largest
- *           finite number: a token with fewer than k others has choices missing (a padded token,
+ *           finite number of the type: a token with fewer than k others has choices missing (a padded token,
  *           all -inf, has none).
  *   experts out: int32 [M][k], -1 for a missing choice.
  *   weights out: fp32 [M][k], e^logit over the sum of the chosen ones (renormalize = 1) or of all E
