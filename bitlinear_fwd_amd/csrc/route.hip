@@ -96,20 +96,26 @@ __device__ __forceinline__ float lanes_sum(float v) {
 // Descending order of a lane's V entries (Batcher's odd-even merge sort).
 template <typename X, int V>
 __device__ __forceinline__ void sort_entries(X (&x)[V]) {
+  static_assert(V == 1 || V == 2 || V == 4 || V == 8, "a network of this size");
   auto order = [&](int i, int j) {
     const X a = x[i], b = x[j];
     x[i] = max(a, b);
     x[j] = min(a, b);
   };
+  if constexpr (V == 2) order(0, 1);
+  if constexpr (V >= 4) {
 #pragma unroll
-  for (int p = 1; p < V; p *= 2)
-#pragma unroll
-    for (int k = p; k >= 1; k /= 2)
-#pragma unroll
-      for (int j = k % p; j + k < V; j += 2 * k)
-#pragma unroll
-        for (int i = 0; i < k; ++i)
-          if (i + j + k < V && (i + j) / (2 * p) == (i + j + k) / (2 * p)) order(i + j, i + j + k);
+    for (int h = 0; h < V; h += 4) {
+      order(h, h + 1), order(h + 2, h + 3);
+      order(h, h + 2), order(h + 1, h + 3);
+      order(h + 1, h + 2);
+    }
+  }
+  if constexpr (V == 8) {
+    order(0, 4), order(1, 5), order(2, 6), order(3, 7);
+    order(2, 4), order(3, 5);
+    order(1, 2), order(3, 4), order(5, 6);
+  }
 }
 
 // The choices of a token, by G lanes with V consecutive logits each.  Lane j of them returns the j-th choice (-1: none)
@@ -196,7 +202,7 @@ __device__ __forceinline__ void place_chunk(const RouteArgs& a, int c, int chunk
       const int e = t % width, p = t / width;
       if (e >= E) continue;
       int all = 0, left = 0;
-#pragma unroll 8
+#pragma unroll 16
       for (int h = p; h < chunks; h += parts) {
         const int n = a.counts[(int64_t)h * E + e];
         all += n;
