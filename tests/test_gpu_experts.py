@@ -297,3 +297,72 @@ def test_quantize_expert_weights():
     for i in range(5):
         p, gm = bl.quantize_weights(w[i])
         assert torch.equal(packed[i], p) and torch.equal(gamma[i:i + 1], gm)
+
+
+# ---- offsets past 32 bits, calls of other kernels' shapes ------------------------------------------------------
+
+
+@pytest.mark.parametrize("t", [2, 40, 700])
+def test_packed_weights_past_4_gib(t):
+    """The last of 20 experts of 256 MiB each: the same as that matrix alone (any bytes are valid weights)."""
+    e, n, k = 20, 16384, 65536
+    g = torch.Generator(device=DEV).manual_seed(t)
+    packed = torch.zeros(e, bl.packed_bytes(n, k), dtype=torch.uint8, device=DEV)
+    packed[-1].random_(0, 256, generator=g)
+    gamma = torch.full((e,), 0.01, device=DEV)
+    x = torch.randn(t, k, generator=g, device=DEV).to(torch.bfloat16)
+    offsets = torch.zeros(e + 1, dtype=torch.int32, device=DEV)
+    offsets[-1] = t
+    y = bl.forward_experts(packed, gamma, offsets, x, n, k, act="relu")
+    alone = bl.forward_epilogue(packed[-1], gamma[-1:], x, n, k, act="relu")
+    assert torch.equal(y, alone)
+    assert (y > 0).any()
+
+
+def test_outputs_past_4_gib():
+    """Rows of Y and of the residual behind 2^32 bytes, of codes behind 2^24 rows' starts: as in a call of their own."""
+    m, n, k = 140001, 8200, 260
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.randn(m, k, generator=g, device=DEV)
+    packed = torch.randint(0, 256, (bl.packed_bytes(n, k),), generator=g, device=DEV, dtype=torch.uint8)
+    gamma = torch.full((1,), 0.01, device=DEV)
+    res = torch.randn(m, n, generator=g, device=DEV, dtype=torch.bfloat16)
+    y = bl.forward_epilogue(packed, gamma, x, n, k, residual=res)
+    for rows in (slice(0, 300), slice(m - 300, m)):
+        assert torch.equal(y[rows], bl.forward_epilogue(packed, gamma, x[rows].contiguous(), n, k, residual=res[rows]))
+
+
+@pytest.mark.parametrize("counts", [[300, 0, 517, 64, 1], [4000, 130], [40] * 30], ids=str)
+def test_experts_equal_single_matrices(counts):
+    """Large groups: every expert's rows as forward_epilogue gives them for that matrix."""
+    layer = Layer(counts, 1100, 700, r=999)
+    x = layer.x.to(DEV)
+    rows, packed, gamma, bias = layer.rows.to(DEV), layer.packed, layer.gamma.to(DEV), layer.bias.to(DEV)
+    r = torch.randn(layer.t, 1100, device=DEV)
+    y = bl.forward_experts(packed, gamma, layer.offsets.to(DEV), x, 1100, 700, rows=rows, bias=bias, act="silu", residual=r,
+                           out_dtype=torch.bfloat16)
+    for e, n in enumerate(counts):
+        if n:
+            s = slice(int(layer.offsets[e]), int(layer.offsets[e + 1]))
+            one = bl.forward_epilogue(packed[e], gamma[e:e + 1], x[rows[s].long()], 1100, 700, bias=bias[e].contiguous(), act="silu",
+                                      residual=r[s], out_dtype=torch.bfloat16)
+            assert torch.equal(y[s], one)
+
+
+def test_two_streams_at_once():
+    """Calls on two streams with their own buffers do not disturb each other."""
+    layers = [Layer([50, 3, 0, 70], 300, 900, r=60, seed=i) for i in range(2)]
+    refs = [layer.forward("gelu") for layer in layers]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in layers]
+    outs = [[], []]
+    args = [(layer.tables(), layer.x.to(DEV), layer.rows.to(DEV), layer.bias.to(DEV)) for layer in layers]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                tables, x, rows, bias = args[i]
+                outs[i].append(bl.forward_experts(*tables, x, 300, 900, rows=rows, bias=bias, act="gelu"))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, refs[i]) for o in outs[i])
