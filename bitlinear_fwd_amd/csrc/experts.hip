@@ -44,17 +44,17 @@ struct Tile {
   int height, width;
   double first, more, end;
 };
-constexpr Tile kTiles[] = {{128, 256, .63, .66, 1.5}, {96, 256, .49, .475, 1.5}, {64, 256, .40, .365, 1.2},
-                           {64, 128, .255, .218, 1.0}, {32, 256, .31, .25, .9}, {32, 128, .225, .137, .9}};
+constexpr Tile kTiles[] = {{128, 256, .69, .70, 1.5}, {96, 256, .555, .51, 1.5}, {64, 256, .44, .395, 1.2},
+                           {64, 128, .27, .232, 1.0}, {32, 256, .34, .263, .9}, {32, 128, .26, .15, .9}};
 constexpr double kGemmStart = 3.5;
-// The decode kernel's workgroups of `height` slots by `per` row blocks: a chunk of 256 columns takes `chunk` on a
-// compute unit (the rows' codes from L2 bound it).  32 x 8192 x 8192 by 16 x 1, 2, 4 and 32 x 4: 21.8, 13.3, 9.0,
+// The decode kernel's workgroups of `height` slots by `per` row blocks: a chunk of 256 columns takes `first` on a
+// compute unit that has one of them, `more` each where it has several (the rows' codes from L2 bound it).  32 x 8192 x 8192 by 16 x 1, 2, 4 and 32 x 4: 21.8, 13.3, 9.0,
 // 13.7 us, 16 x 2560 x 6912: 6.5, 6.6, 7.2, 8.6; the GEMM 21.2 and 18.7.
 struct Decode {
   int height, per;
-  double chunk;
+  double first, more;
 };
-constexpr Decode kDecodes[] = {{16, 1, .118}, {16, 2, .125}, {16, 4, .143}, {32, 4, .243}};
+constexpr Decode kDecodes[] = {{16, 1, .118, .126}, {16, 2, .125, .134}, {16, 4, .143, .158}, {32, 4, .243, .29}};
 constexpr double kDecodeStart = 2.85, kDecodeEnd = .35;
 
 }  // namespace
@@ -75,7 +75,7 @@ ExpertsPlan plan_experts(int64_t E, int64_t T, int64_t N, int64_t K, int src) {
   }
   for (const Decode& d : kDecodes) {
     const double rounds = std::ceil(units(d.height) * (double)((blocks + d.per - 1) / d.per) / 256.0);
-    const double us = kDecodeStart + rounds * ((double)chunks * d.chunk + kDecodeEnd);
+    const double us = kDecodeStart + rounds * ((double)chunks * (rounds > 1 ? d.more : d.first) + kDecodeEnd);
     if (us < best) {
       best = us, p.kernel = kMidKernel, p.height = d.height, p.per = d.per;
       // the waves of a workgroup split the columns; many workgroups keep a compute unit busy by themselves

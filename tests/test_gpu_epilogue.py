@@ -161,7 +161,7 @@ def exact_on_gpu(q_w, q, a, gamma):
 
 
 FORMS = [(1, 700, 1280, "bf16"), (4, 301, 2568, "f32"), (1, 64, 90000, "bf16"), (2, 64, 40000, "f32"), (4, 300, 40000, "f32"),
-         (3, 65, 2571, "f32"), (9, 200, 700, "i8"), (9, 4500, 600, "i8"), (33, 9000, 300, "i8"), (1500, 1000, 512, "i8"),
+         (3, 65, 2571, "f32"), (9, 200, 700, "i8"), (9, 4500, 600, "i8"), (33, 9000, 300, "i8"), (64, 6900, 700, "i8"), (1500, 1000, 512, "i8"),
          (1247, 1641, 635, "i8"), (65, 19498, 300, "i8"), (200, 6917, 2560, "i8"), (300, 300, 300, "i8"), (133, 15252, 33, "i8"),
          (700, 3000, 1000, "i8"), (1500, 6900, 1100, "i8"), (6090, 526, 34, "i8"), (2050, 6912, 600, "i8"), (13197, 345, 33, "i8")]
 
