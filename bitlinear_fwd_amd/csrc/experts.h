@@ -96,18 +96,22 @@ __device__ __forceinline__ Unit find_unit(const Groups& g, int height, int u) {
 // A launch cannot have more units than this (groups with slots have at most one unit that is not full).
 inline int64_t most_units(int64_t E, int64_t T, int height) { return T / height + (E < T ? E : T); }
 
-// e^-x / (1 + e^-x) and the like need e^x only to a few units in the last place: 2^(x log2 e) with the
-// product's rounding error put back.  x is kept in -104 .. 87: below, e^x is nothing in fp32, and above
-// nothing overflows.
+// e^x to a few units in the last place for x <= 0, which is all that the weights and activations below need: 2^(x log2 e)
+// with the product's rounding error put back.  Below -104, where e^x is nothing in fp32, it gives 0.
 __device__ __forceinline__ float exp_of(float x) {
   constexpr float kLog2e = 1.44269502e+00f, kLog2eLow = 1.92596303e-08f, kLn2 = 6.93147182e-01f;
-  x = __builtin_amdgcn_fmed3f(x, -104.0f, 87.0f);
+  x = fmaxf(x, -104.0f);
   const float t = x * kLog2e;
   const float low = __builtin_fmaf(x, kLog2eLow, __builtin_fmaf(x, kLog2e, -t));
   const float e = __builtin_amdgcn_exp2f(t);
   return __builtin_fmaf(e, low * kLn2, e);
 }
-__device__ __forceinline__ float sigmoid_of(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_of(-x)); }
+// 1 / (1 + e^-x) = e^x / (1 + e^x), by whichever of the two has the exponential of a number below 0: it goes to 0 on
+// the far left (1 / (1 + e^-x) with the exponential kept finite stops at 1.6e-38, which a large x makes visible).
+__device__ __forceinline__ float sigmoid_of(float x) {
+  const float e = exp_of(-fabsf(x));
+  return (x < 0.0f ? e : 1.0f) * __builtin_amdgcn_rcpf(1.0f + e);
+}
 
 // v (1 + erf(v / sqrt 2)) / 2 by Abramowitz and Stegun's 7.1.26: erfc(x) = (a1 t + .. + a5 t^5) e^(-x^2) + 1.5e-7 at
 // most, t = 1 / (1 + p x), x >= 0: off by 1.3 half steps of |v| (with erff a 2048 x 6912 output took 16 us longer).

@@ -1,0 +1,50 @@
+"""Activations of products over the whole range of their argument, in every kernel: tokens of zeros leave the bias, a
+number of fp32, as the exact argument."""
+import pytest
+import torch
+
+import bitlinear_fwd_amd as bl
+import experts_reference as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+F32, BF16 = torch.float32, torch.bfloat16
+# kernel of the plan: tokens, columns, x of zeros or codes of zeros
+FORMS = {"fused": (2, 264, "bf16"), "decode": (16, 300, None), "gemm": (1500, 300, None)}
+
+
+def activated(form, bias, act, dtype):
+    """act(bias) [N], as the form's kernel gives it for every token (all the same)."""
+    m, k, x = FORMS[form]
+    n = len(bias)
+    assert bl.forward_epilogue_plan(m, n, k, x)["kernel"] == form
+    packed = ref.pack(ref.random_codes(n, k, torch.Generator().manual_seed(n))).to(DEV)
+    gamma = torch.full((1,), 0.02, device=DEV)
+    if x is None:
+        xs, absmax = torch.zeros(m, (k + 255) // 256 * 256, dtype=torch.int8, device=DEV), torch.zeros(m, device=DEV)
+    else:
+        xs, absmax = torch.zeros(m, k, dtype=BF16, device=DEV), None
+    y = bl.forward_epilogue(packed, gamma, xs, n, k, absmax=absmax, bias=bias.to(DEV), act=act, out_dtype=dtype)
+    assert torch.equal(y.isnan(), y[:1].isnan().expand(m, n)) and torch.equal(y.nan_to_num(), y[:1].nan_to_num().expand(m, n))
+    return y[0].cpu()
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_sigmoid_forms_go_to_zero(form, act, dtype):
+    """v times a sigmoid: 0 far to the left, v far to the right, and every order of magnitude between.  Roundings as
+    ref.act counts them; e^x is 0 where fp32 has it below its normal numbers, of which |v| < 104 makes 104 2^-126."""
+    size = torch.logspace(-3, 38.5, 500, dtype=torch.float64).float()
+    v = torch.cat((-size, size, -torch.linspace(80, 110, 301), torch.tensor([0.0, -0.0, -3.4028234663852886e38])))
+    y = activated(form, v, act, dtype)
+    d = v.double()
+    exact, err = ref.act(d, torch.zeros_like(d), act)
+    # 2^t to an argument t of 87 at most: further left nothing is left of v e^t
+    if act == "gelu_tanh":
+        t = 1.5957691216057308 * (d + 0.044715 * d ** 3)
+        exact = torch.where(t < -120, torch.zeros_like(d), exact)
+        err = (10 + 6 * t.abs().clamp(max=120)) * ref.U * exact.abs()
+    err = err + 104 * 2.0 ** -126
+    ref.check(y, exact, err + (dtype == BF16) * ref.STEP[BF16] * (exact.abs() + err), f"{form} {act}")
+    assert (y[v < -110].double() == 0).all()
