@@ -269,7 +269,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
               for (int q = 0; q < 4; ++q) v[k * H + h][q] = __builtin_fmaf((float)a[q], f, b[h][q]);
             }
           }
-          activate_all(v, e.act);
+          activate_all<bf16>(v, e.act);
           if (e.residual) {
 #pragma unroll
             for (int k = 0; k < kIt * H; ++k) v[k] += r4[k];
@@ -294,7 +294,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[h][e] = __builtin_fmaf((float)a[e], f, b[h][e]);
         }
-        activate_all(v, ep.act);
+        activate_all<bf16>(v, ep.act);
         finish_row(ep, s, n0 + o, left, v);
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read before the next slab is written

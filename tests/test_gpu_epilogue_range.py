@@ -48,3 +48,48 @@ def test_sigmoid_forms_go_to_zero(form, act, dtype):
     err = err + 104 * 2.0 ** -126
     ref.check(y, exact, err + (dtype == BF16) * ref.STEP[BF16] * (exact.abs() + err), f"{form} {act}")
     assert (y[v < -110].double() == 0).all()
+
+
+def gelu(d):
+    return 0.5 * d * torch.erfc(-d / 2 ** 0.5)
+
+
+GELU_ARGS = torch.cat((torch.linspace(-16, 16, 3001), torch.logspace(-30, 38.5, 200, dtype=torch.float64).float(),
+                       -torch.logspace(-30, 38.5, 200, dtype=torch.float64).float(), torch.tensor([1.25, -1.25, 0.0])))
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_gelu_in_fp32(form):
+    """On the left relative to the result: t = 1 / (1 + 0.35 a) to 3 half steps, which the result follows at most
+    twice; the polynomial's fit and last steps 2; the exponential 2, and its argument a^2 / 2 to 2; three products: 13 + a^2.
+    On the right h, at most 0.106 |v| where it is taken, to 15 there, and the difference; below 1.25 Phi(v) - 1/2, at
+    most 0.4, to 2.5, the sum and the product: 3 of |v|.  Results below fp32's normal numbers may be 0."""
+    v = GELU_ARGS
+    y = activated(form, v, "gelu", F32).double()
+    d = v.double()
+    exact = gelu(d)
+    left = (13 + d.clamp(min=-16) ** 2) * ref.U * exact.abs() + 16 * 2.0 ** -126
+    err = torch.where(d < 0, left, 3 * ref.U * d)
+    ref.check(y, exact, err, form)
+    assert (y[d < -1e-30] <= 0).all() and (y[(d < -1e-30) & (d > -12)] < 0).all()
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_gelu_in_bf16(form):
+    """Half a step of bf16 of the result and what the short form adds, all of it relative to the result: 16 half steps
+    of fp32, and the exponent's a^2 / 2 to 2 of them."""
+    v = GELU_ARGS
+    y = activated(form, v, "gelu", BF16)
+    d = v.double()
+    exact = gelu(d)
+    short = (16 + d.abs().clamp(max=16) ** 2) * ref.U * exact.abs() + 16 * 2.0 ** -126
+    ref.check(y, exact, short + ref.STEP[BF16] * (exact.abs() + short), form)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("act", ["relu2", "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_plus_infinity(form, act, dtype):
+    """A sum that overflows fp32 stays infinite."""
+    y = activated(form, torch.tensor([float("inf")] + [1.0] * 1303), act, dtype)
+    assert y[0] == float("inf") and y[1:].isfinite().all()
