@@ -96,21 +96,23 @@ __device__ __forceinline__ Unit find_unit(const Groups& g, int height, int u) {
 // A launch cannot have more units than this (groups with slots have at most one unit that is not full).
 inline int64_t most_units(int64_t E, int64_t T, int height) { return T / height + (E < T ? E : T); }
 
-// e^x to a few units in the last place for x <= 0, which is all that the weights and activations below need: 2^(x log2 e)
-// with the product's rounding error put back.  Below -104, where e^x is nothing in fp32, it gives 0.
+// e^x to a few units in the last place for x <= 0, which is all that the router's weights need: 2^(x log2 e) with the
+// product's rounding error put back.  Below -104, where e^x is nothing in fp32, it gives 0.
+constexpr float kLog2e = 1.44269502e+00f, kLog2eLow = 1.92596303e-08f, kLn2 = 6.93147182e-01f;
 __device__ __forceinline__ float exp_of(float x) {
-  constexpr float kLog2e = 1.44269502e+00f, kLog2eLow = 1.92596303e-08f, kLn2 = 6.93147182e-01f;
   x = fmaxf(x, -104.0f);
   const float t = x * kLog2e;
   const float low = __builtin_fmaf(x, kLog2eLow, __builtin_fmaf(x, kLog2e, -t));
   const float e = __builtin_amdgcn_exp2f(t);
   return __builtin_fmaf(e, low * kLn2, e);
 }
-// 1 / (1 + e^-x) = e^x / (1 + e^x), by whichever of the two has the exponential of a number below 0: it goes to 0 on
-// the far left (1 / (1 + e^-x) with the exponential kept finite stops at 1.6e-38, which a large x makes visible).
+// 1 / (1 + e^-x), which goes to 0 on the far left: e^-x reaches infinity, so its rounding error is put back as a factor
+// (added, as above, it would be infinity less infinity).
 __device__ __forceinline__ float sigmoid_of(float x) {
-  const float e = exp_of(-fabsf(x));
-  return (x < 0.0f ? e : 1.0f) * __builtin_amdgcn_rcpf(1.0f + e);
+  x = __builtin_amdgcn_fmed3f(x, -104.0f, 104.0f);
+  const float t = x * -kLog2e;
+  const float low = __builtin_fmaf(x, -kLog2eLow, __builtin_fmaf(x, -kLog2e, -t));
+  return __builtin_amdgcn_rcpf(__builtin_fmaf(__builtin_amdgcn_exp2f(t), __builtin_fmaf(low, kLn2, 1.0f), 1.0f));
 }
 
 // v (1 + erf(v / sqrt 2)) / 2 = v Phi(v), from the half h = |v| Phi(-|v|) that is missing on the right and all there is
