@@ -146,11 +146,13 @@ __device__ __forceinline__ float gelu_of(float v) {
   return a < 1.25f ? v * __builtin_fmaf(v, r, 0.5f) : far;
 }
 
+__device__ __forceinline__ float relu_of(float v) { return v < 0.0f ? 0.0f : v; }  // (fmaxf would make a NaN 0)
+
 // The activations of bl_activation, in fp32; kShort: for a result in bf16.
 template <int kAct, bool kShort>
 __device__ __forceinline__ float activate(float v) {
-  if constexpr (kAct == 1) return fmaxf(v, 0.0f);
-  else if constexpr (kAct == 2) return fmaxf(v, 0.0f) * fmaxf(v, 0.0f);
+  if constexpr (kAct == 1) return relu_of(v);
+  else if constexpr (kAct == 2) return relu_of(v) * relu_of(v);
   else if constexpr (kAct == 3) return v * sigmoid_of(v);
   else if constexpr (kAct == 4) return gelu_of<kShort>(v);
   // (1 + tanh u) / 2 = sigmoid(2 u)

@@ -93,3 +93,11 @@ def test_plus_infinity(form, act, dtype):
     """A sum that overflows fp32 stays infinite."""
     y = activated(form, torch.tensor([float("inf")] + [1.0] * 1303), act, dtype)
     assert y[0] == float("inf") and y[1:].isfinite().all()
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("act", list(bl.ACTIVATIONS))
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_nan_stays_nan(form, act, dtype):
+    y = activated(form, torch.tensor([float("nan"), -float("nan"), -1.0] + [1.0] * 1301), act, dtype)
+    assert y[:2].isnan().all() and y[2:].isfinite().all()
