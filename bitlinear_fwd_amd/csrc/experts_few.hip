@@ -29,6 +29,28 @@ __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(
 // at piece p ^ 4.
 __device__ __forceinline__ int few_swizzle(int r) { return (r + 12) & 15; }
 
+// The fp32 bits of the largest magnitude of eight elements, NaN passed over as the quantiser in a launch of its own does:
+// an offset that makes the patterns of NaN, and only these, negative.
+__device__ __forceinline__ uint32_t top_number(const Raw8<float>& r) {
+  constexpr int kOff = 0x007fffff;
+  int top = kOff;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, (int)((r.w[i] & 0x7fffffffu) + kOff));
+  return (uint32_t)(top - kOff);
+}
+__device__ __forceinline__ uint32_t top_number(const Raw8<uint16_t>& r) {
+  typedef unsigned short v2u __attribute__((ext_vector_type(2)));
+  typedef short v2s __attribute__((ext_vector_type(2)));
+  constexpr unsigned short kOff = 0x007f;
+  v2s m = {kOff, kOff};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const v2u w = __builtin_bit_cast(v2u, r.w[i] & 0x7fff7fffu) + v2u{kOff, kOff};
+    m = __builtin_elementwise_max(m, __builtin_bit_cast(v2s, w));
+  }
+  return (uint32_t)(max(m.x, m.y) - kOff) << 16;
+}
+
 constexpr int kKept = 4;    // pieces of 8 elements that a thread keeps between the two passes of the quantiser
 
 // kSrc 1: bf16, 2: fp32 x[R][K], K a multiple of 8.  A workgroup takes one unit and `per` row blocks.
@@ -108,7 +130,7 @@ __global__ __launch_bounds__(1024) void k_few(Groups g, const void* __restrict__
     auto row_max = [&](const T* x) {
       uint32_t m = 0;
 #pragma unroll 2
-      for (int p = piece0; p < pieces; p += stride) m = max(m, top_bits(piece(x, p)));
+      for (int p = piece0; p < pieces; p += stride) m = max(m, top_number(piece(x, p)));
       return wave_max(m);
     };
     auto row_put = [&](int r, const T* x, float s) {
@@ -119,9 +141,9 @@ __global__ __launch_bounds__(1024) void k_few(Groups g, const void* __restrict__
       uint32_t* top = reinterpret_cast<uint32_t*>(part);
       uint32_t m = 0;
       if (kept) {
-        m = top_bits(v[0]);
-        if (nkept > 1) m = max(m, top_bits(v[1]));
-        if (nkept > 2) m = max(m, max(top_bits(v[2]), top_bits(v[3])));
+        m = top_number(v[0]);
+        if (nkept > 1) m = max(m, top_number(v[1]));
+        if (nkept > 2) m = max(m, max(top_number(v[2]), top_number(v[3])));
         m = wave_max(m);
       } else if (first_row < rows) {
         m = row_max(row_of(first_row));

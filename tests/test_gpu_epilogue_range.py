@@ -101,3 +101,28 @@ def test_plus_infinity(form, act, dtype):
 def test_nan_stays_nan(form, act, dtype):
     y = activated(form, torch.tensor([float("nan"), -float("nan"), -1.0] + [1.0] * 1301), act, dtype)
     assert y[:2].isnan().all() and y[2:].isfinite().all()
+
+
+@pytest.mark.parametrize("m,n,k,x", [(1, 700, 1280, BF16), (2, 40, 264, F32), (4, 301, 2568, F32), (4, 301, 2568, BF16),
+                                     (3, 40, 256, BF16), (2, 64, 40000, F32), (1, 64, 90000, BF16)], ids=str)
+def test_rows_with_nan_or_infinity(m, n, k, x):
+    """The quantiser within the kernel passes over NaN and takes infinities as the one in a launch of its own does: the
+    same outputs as from its codes and scales."""
+    g = torch.Generator().manual_seed(k)
+    assert bl.forward_epilogue_plan(m, n, k, "bf16" if x == BF16 else "f32")["kernel"] == "fused"
+    packed = ref.pack(ref.random_codes(n, k, g)).to(DEV)
+    gamma = torch.full((1,), 0.02, device=DEV)
+    nan, inf = float("nan"), float("inf")
+    at = [0, k // 2, k - 1]
+    for places in ([(0, nan)], [(0, nan), (1, -nan), (2, nan)], [(1, inf)], [(2, -inf), (0, nan)], [(1, -nan)], "all"):
+        xs = torch.randn(m, k, generator=g)
+        for r in range(0, m, 2):  # every other row
+            if places == "all":
+                xs[r] = nan
+            else:
+                for i, v in places:
+                    xs[r, at[i]] = v
+        xs = xs.to(x).to(DEV)
+        codes, absmax = bl.quantize_acts(xs)
+        y, z = bl.forward_epilogue(packed, gamma, xs, n, k), bl.forward_epilogue(packed, gamma, codes, n, k, absmax=absmax)
+        assert torch.equal(y.isnan(), z.isnan()) and torch.equal(y.nan_to_num(), z.nan_to_num()), places
