@@ -350,7 +350,7 @@ int bitlinear_forward_experts_combine(const bl_experts* experts, const void* X, 
   int st = products_ok(g, X, dt, Xq, absmax);
   if (st == BL_OK) st = epilogue_of(ep, g.N, &out);
   if (st != BL_OK) return st;
-  if (k > kMaxCombined || M > (kMaxDim - 1) * 256 / ((g.N + 3) / 4)) return BL_ERR_UNSUPPORTED;
+  if (k > kMaxCombined) return BL_ERR_UNSUPPORTED;
   const int64_t need = bitlinear_forward_experts_combine_ws_bytes(g.T, g.N);
   if (need < 0) return BL_ERR_UNSUPPORTED;
   if (!aligned(slots, 4) || !aligned(weights, 4) || !workspace || !aligned(workspace, 16) || ws_bytes < need)

@@ -8,27 +8,28 @@
 namespace bl {
 namespace {
 
-// One thread per four outputs of a token.
+// One thread per four outputs of a token, and more where a launch cannot have so many.
+constexpr int64_t kCombineGroups = int64_t(1) << 23;
 __global__ __launch_bounds__(256) void k_combine(Groups g, const float* __restrict__ H,
                                                  const int32_t* __restrict__ slots,
                                                  const float* __restrict__ weights, int64_t M, int k, int64_t quads,
                                                  Epilogue ep) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t m = i / quads, n = 4 * (i - m * quads);
-  if (m >= M) return;
-  const int left = (int)min(g.N - n, (int64_t)4);
   const int first = max(0, min(g.offsets[0], (int)g.T)), last = max(0, min(g.offsets[g.E], (int)g.T));
-  v4f v = {0, 0, 0, 0};
-  for (int j = 0; j < k; ++j) {
-    const int s = slots[m * k + j];
-    if (s < first || s >= last || slot_row(g, s) < 0) continue;
-    const v4f h = *reinterpret_cast<const v4f*>(H + (int64_t)s * (4 * quads) + n);  // (columns past N: not stored)
-    const float w = weights[m * k + j];
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < M * quads; i += (int64_t)gridDim.x * 256) {
+    const int64_t m = i / quads, n = 4 * (i - m * quads);
+    const int left = (int)min(g.N - n, (int64_t)4);
+    v4f v = {0, 0, 0, 0};
+    for (int j = 0; j < k; ++j) {
+      const int s = slots[m * k + j];
+      if (s < first || s >= last || slot_row(g, s) < 0) continue;
+      const v4f h = *reinterpret_cast<const v4f*>(H + (int64_t)s * (4 * quads) + n);  // (columns past N: not stored)
+      const float w = weights[m * k + j];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] = __builtin_fmaf(w, h[q], v[q]);
+      for (int q = 0; q < 4; ++q) v[q] = __builtin_fmaf(w, h[q], v[q]);
+    }
+    if (ep.residual) v += load4(ep.residual, m * ep.ldr + n, left, ep.res_bf16);
+    store4(ep.Y, m * ep.ldy + n, left, ep.y_bf16, v);
   }
-  if (ep.residual) v += load4(ep.residual, m * ep.ldr + n, left, ep.res_bf16);
-  store4(ep.Y, m * ep.ldy + n, left, ep.y_bf16, v);
 }
 
 }  // namespace
@@ -111,7 +112,8 @@ hipError_t launch_experts(const ExpertsPlan& p, const Groups& g, const void* X, 
 hipError_t launch_combine(const Groups& g, const float* H, const int32_t* slots, const float* weights, int64_t M, int k,
                           const Epilogue& ep, hipStream_t s) {
   const int64_t quads = (g.N + 3) / 4;
-  k_combine<<<dim3((unsigned)((M * quads + 255) / 256)), 256, 0, s>>>(g, H, slots, weights, M, k, quads, ep);
+  const int64_t groups = std::min((M * quads + 255) / 256, kCombineGroups);
+  k_combine<<<dim3((unsigned)groups), 256, 0, s>>>(g, H, slots, weights, M, k, quads, ep);
   return hipGetLastError();
 }
 
