@@ -23,6 +23,8 @@
 // (|sum| <= 127 K): v_dot4 of each group's codes with ones, then an integer reduction.
 #include "bl_internal.h"
 
+#include <algorithm>
+
 namespace bl {
 namespace {
 
@@ -216,9 +218,12 @@ __global__ __launch_bounds__(kThreads) void k_act_quant_scalar(const void* __res
   if (rowsum) block_rowsum<kThreads>(rs, red_i, rowsum + m);
 }
 
+// Rows of one launch, a workgroup each: a launch has fewer than 2^32 threads, and a workgroup 1024 at most.
+constexpr int64_t kLaunchRows = int64_t(1) << 21;
+
 template <bool kNorm>
-void launch_rows(const void* X, int bf16, int64_t M, int64_t K, const float* gain, float eps, int8_t* Xq,
-                 float* absmax, int32_t* rowsum, hipStream_t s) {
+void launch_some_rows(const void* X, int bf16, int64_t M, int64_t K, const float* gain, float eps, int8_t* Xq,
+                      float* absmax, int32_t* rowsum, hipStream_t s) {
   const int64_t K_pad = k_pad(K);
   const bool vec = (K % 8 == 0) && ((reinterpret_cast<uintptr_t>(X) & 15u) == 0) &&
                    ((reinterpret_cast<uintptr_t>(gain) & 15u) == 0);
@@ -238,6 +243,14 @@ void launch_rows(const void* X, int bf16, int64_t M, int64_t K, const float* gai
     if (bf16) hipLaunchKernelGGL((k_act_quant_scalar<true, kNorm>), grid, block, 0, s, X, K, K_pad, gain, eps, Xq, absmax, rowsum);
     else hipLaunchKernelGGL((k_act_quant_scalar<false, kNorm>), grid, block, 0, s, X, K, K_pad, gain, eps, Xq, absmax, rowsum);
   }
+}
+
+template <bool kNorm>
+void launch_rows(const void* X, int bf16, int64_t M, int64_t K, const float* gain, float eps, int8_t* Xq,
+                 float* absmax, int32_t* rowsum, hipStream_t s) {
+  for (int64_t m = 0; m < M; m += kLaunchRows)
+    launch_some_rows<kNorm>(static_cast<const uint8_t*>(X) + m * K * (bf16 ? 2 : 4), bf16, std::min(M - m, kLaunchRows), K,
+                            gain, eps, Xq + m * k_pad(K), absmax + m, rowsum ? rowsum + m : nullptr, s);
 }
 
 }  // namespace

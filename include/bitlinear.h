@@ -387,8 +387,9 @@ int bitlinear_forward_epilogue(const uint8_t* packed, const float* gamma, const 
 
 /*
  * Host-only: the launches of bitlinear_forward_epilogue for (M, N, K) and x of type xdt (-1: codes).
- * out[0] = kernel (10: decode with the quantiser, 11: GEMM, 12: decode), out[1] = its workgroups, out[2] = threads per workgroup, out[3] and out[4] =
- * token rows and outputs of a workgroup at a time, out[5] = launches (2: the quantiser first).
+ * out[0] = kernel (10: decode with the quantiser, 11: GEMM, 12: decode), out[1] = its workgroups,
+ * out[2] = threads per workgroup, out[3] and out[4] = token rows and outputs of a workgroup at a
+ * time, out[5] = launches (2: the quantiser first, in parts of 2^21 rows).
  * Returns BL_OK, BL_ERR_INVALID_ARG or BL_ERR_UNSUPPORTED as the call does.
  */
 int bitlinear_forward_epilogue_plan(int64_t M, int64_t N, int64_t K, int xdt, int32_t out[6]);

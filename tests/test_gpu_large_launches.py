@@ -24,3 +24,23 @@ def test_combine_of_more_outputs_than_threads():
     at = (slots.long() * 9 + weights.long()).view(-1)
     for lo in range(0, m, 1 << 17):
         assert torch.equal(y[lo:lo + (1 << 17)], table[at[lo:lo + (1 << 17)]]), lo
+
+
+@pytest.mark.parametrize("k", [8, 9])
+def test_more_rows_than_workgroups_of_256_threads(k):
+    """2^24 + 9 token rows, a workgroup each in the quantiser: codes, row sums and a product's outputs as from the rows
+    around each of its launches' borders in calls of their own."""
+    r, n = (1 << 24) + 9, 16
+    g = torch.Generator(device=DEV).manual_seed(k)
+    x = torch.randn(r, k, generator=g, device=DEV).to(torch.bfloat16)
+    packed = torch.randint(0, 256, (bl.packed_bytes(n, k),), generator=g, device=DEV, dtype=torch.uint8)
+    gamma = torch.full((1,), 0.02, device=DEV)
+    codes, scales, sums = bl.quantize_acts(x, want_rowsum=True)
+    y = bl.forward_epilogue(packed, gamma, x, n, k)
+    assert torch.equal(scales, x.float().abs().amax(1))
+    for at in [i << 21 for i in range(1, 9)] + [r]:
+        rows = slice(at - 5, min(at + 5, r))
+        part = x[rows].clone()
+        c, s, t = bl.quantize_acts(part, want_rowsum=True)
+        assert torch.equal(codes[rows], c) and torch.equal(scales[rows], s) and torch.equal(sums[rows], t)
+        assert torch.equal(y[rows], bl.forward_epilogue(packed, gamma, part, n, k))
