@@ -93,12 +93,16 @@ int products_ok(const bl::Groups& g, const void* X, int dt, const int8_t* Xq, co
   return BL_OK;
 }
 
+// A launch has fewer than 2^32 threads.
+bool launchable(const bl::ExpertsPlan& p) { return p.groups < (int64_t(1) << 32) / p.threads; }
+
 // The products, behind the quantiser where X is given and the kernel does not take it itself.
 int products(const bl::Groups& g, const void* X, int dt, int8_t* Xq, float* absmax, const bl::Epilogue& ep,
              hipStream_t s) {
   const int64_t E = g.offsets ? g.E : 0;
   int src = X ? mx_src(dt) : 0;
   bl::ExpertsPlan p = bl::plan_experts(E, g.T, g.N, g.K, src);
+  if (!launchable(p)) return BL_ERR_UNSUPPORTED;
   if (src && !p.quantizes) {
     if (!Xq || !absmax) return BL_ERR_INVALID_ARG;
     const hipError_t e = bl::launch_act_quant(X, dt == BL_BF16, g.R, g.K, Xq, absmax, s);
@@ -113,6 +117,7 @@ int products_plan(int64_t E, int64_t T, int64_t N, int64_t K, int xdt, int32_t o
   if (xdt != -1 && !dtype_ok(xdt)) return BL_ERR_UNSUPPORTED;
   if (!products_countable(E ? E : 1, T, N, K)) return BL_ERR_UNSUPPORTED;
   const bl::ExpertsPlan p = bl::plan_experts(E, T, N, K, xdt == -1 ? 0 : mx_src(xdt));
+  if (!launchable(p)) return BL_ERR_UNSUPPORTED;
   const bool one = xdt == -1 || p.quantizes;
   out[0] = p.kernel, out[1] = (int32_t)p.groups, out[2] = p.threads, out[3] = p.height, out[4] = p.width;
   out[5] = one ? 1 : 2;

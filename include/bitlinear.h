@@ -380,7 +380,7 @@ typedef struct {
  *         type); no other buffers of one call may overlap.
  * Errors: BL_ERR_INVALID_ARG for null pointers, sizes, misaligned pointers, row distances below
  * N and an unknown act; BL_ERR_UNSUPPORTED for other types and for launches that are too large
- * (M or N beyond 2^31 - 4096, 2^31 tiles of 16 x 16, matrices of 2^40 bytes).
+ * (M or N beyond 2^31 - 4096, 2^31 tiles of 16 x 16, 2^32 threads, matrices of 2^40 bytes).
  */
 int bitlinear_forward_epilogue(const uint8_t* packed, const float* gamma, const void* X, int dt, int8_t* Xq,
                                float* absmax, int64_t M, int64_t N, int64_t K, const bl_epilogue* ep, void* stream);
