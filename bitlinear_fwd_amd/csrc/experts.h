@@ -289,7 +289,7 @@ struct ExpertsPlan {
   int threads = 256;
   int64_t groups = 0;         // workgroups
   int height = 16, width = 64;  // slots and outputs of a workgroup at a time
-  int per = 1;                // few, mid: row blocks of a workgroup
+  int per = 1;                // mid: row blocks of a workgroup
   int64_t lds = 0;            // few: bytes
   bool quantizes = false;     // takes x itself
 };

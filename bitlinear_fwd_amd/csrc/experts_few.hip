@@ -3,8 +3,7 @@
 // columns and add their exact sums through LDS.
 //
 // k_few, a few slots in all: the workgroup first fills LDS with the codes of its unit's token rows, quantised there
-// from fp32 or bf16 (which saves a launch), the rows' loads ahead of the first weights', then walks over row blocks with
-// the next weights in flight.
+// from fp32 or bf16 (which saves a launch), the rows' loads ahead of the first weights', then takes one row block.
 // k_mid, units of 16 or 32 slots: token fragments come from the caches, up to four row blocks share them and up to
 // two of them share a decoded weight fragment.
 //
@@ -53,17 +52,17 @@ __device__ __forceinline__ uint32_t top_number(const Raw8<uint16_t>& r) {
 
 constexpr int kKept = 4;    // pieces of 8 elements that a thread keeps between the two passes of the quantiser
 
-// kSrc 1: bf16, 2: fp32 x[R][K], K a multiple of 8.  A workgroup takes one unit and `per` row blocks.
+// kSrc 1: bf16, 2: fp32 x[R][K], K a multiple of 8.  A workgroup takes one unit and one row block.
 // kDepth: chunks of weights that a wave loads at a time.
 template <int kSrc, int kDepth>
-__global__ __launch_bounds__(1024) void k_few(Groups g, const void* __restrict__ X, Epilogue ep, int chunks, int nblocks, int per, int columns) {
-  extern __shared__ v4i part[];  // [2][waves][64], then scales [16], then the tokens
+__global__ __launch_bounds__(1024) void k_few(Groups g, const void* __restrict__ X, Epilogue ep, int chunks, int nblocks) {
+  extern __shared__ v4i part[];  // [waves][64], then scales [16], then the tokens
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
-  float* scales = reinterpret_cast<float*>(part + 2 * waves * 64);
+  float* scales = reinterpret_cast<float*>(part + waves * 64);
   uint8_t* tok = reinterpret_cast<uint8_t*>(scales + 16);
-  const Unit u = find_unit(g, 16, blockIdx.x / columns);
+  const Unit u = find_unit(g, 16, blockIdx.x / nblocks);
   if (u.lo >= u.hi) return;
-  const int nb0 = (int)(blockIdx.x % columns) * per, nb1 = min(nb0 + per, nblocks);
+  const int nb = (int)(blockIdx.x % nblocks);
 
   const int rows = u.hi - u.lo, K = (int)g.K, pitch = chunks * kTileCols;
 
@@ -97,18 +96,17 @@ __global__ __launch_bounds__(1024) void k_few(Groups g, const void* __restrict__
     }
   }
 
-  // this wave's chunks of a row block: wave, wave + waves, .., kDepth at a time (past the last the last again, so that
-  // no load depends on a branch)
+  // this wave's chunks of the row block: wave, wave + waves, .., kDepth at a time (past the last the last again, so that
+  // no load of a batch depends on a branch)
   const int mine = (chunks - wave + waves - 1) / waves;
-  const uint4* w0 = reinterpret_cast<const uint4*>(g.packed + (int64_t)u.e * nblocks * chunks * kTileBytes) + lane;
+  const uint4* w0 = reinterpret_cast<const uint4*>(g.packed + ((int64_t)u.e * nblocks + nb) * chunks * kTileBytes) + lane;
   v4i w[kDepth];
-  auto fetch = [&](int nb, int i) {
+  auto fetch = [&](int i) {
 #pragma unroll
     for (int d = 0; d < kDepth; ++d)
-      w[d] = __builtin_nontemporal_load(
-          reinterpret_cast<const v4i*>(w0 + ((int64_t)nb * chunks + wave + min(i + d, mine - 1) * waves) * 64));
+      w[d] = __builtin_nontemporal_load(reinterpret_cast<const v4i*>(w0 + (int64_t)(wave + min(i + d, mine - 1) * waves) * 64));
   };
-  fetch(nb0, 0);
+  fetch(0);
 
   {
     auto wave_max = [&](uint32_t m) {
@@ -184,13 +182,11 @@ __global__ __launch_bounds__(1024) void k_few(Groups g, const void* __restrict__
   const int row = slot_row(g, u.lo + tr);
   const float gamma = g.gamma[u.e], scale = token_scale(gamma, scales[tr]);
   v4i acc = {0, 0, 0, 0};
-  int nb = nb0, i = 0;  // i: of this wave's chunks
-  while (nb < nb1) {
+  for (int i = 0; i < mine; i += kDepth) {
     v4i t[kDepth];
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) t[d] = w[d];
-    const bool done = i + kDepth >= mine;
-    fetch(done ? min(nb + 1, nb1 - 1) : nb, done ? 0 : i + kDepth);
+    if (i + kDepth < mine) fetch(i + kDepth);
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) {
       if (i + d < mine) {
@@ -200,22 +196,15 @@ __global__ __launch_bounds__(1024) void k_few(Groups g, const void* __restrict__
           acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(decode16((uint32_t)t[d][k]), *reinterpret_cast<const v4i*>(x + place[k]), acc, 0, 0, 0);
       }
     }
-    i += kDepth;
-    if (!done) continue;
-    // the row block's sums, by the waves in turn
-    i = 0;
-    const int turn = nb - nb0;
-    v4i* at = part + (turn & 1) * waves * 64;
-    at[wave * 64 + lane] = acc;
-    acc = v4i{0, 0, 0, 0};
-    lds_barrier();
-    if (wave == turn % waves) {
-      v4i s = at[lane];
-      for (int v = 1; v < waves; ++v) s += at[v * 64 + lane];
-      const int64_t n = (int64_t)nb * 16 + 4 * lq, left = g.N - n;
-      if (lr < rows && row >= 0 && left > 0) finish4(ep, u.e, g.N, u.lo + lr, n, (int)min(left, (int64_t)4), s, scale);
-    }
-    ++nb;
+  }
+  // the waves' sums
+  part[wave * 64 + lane] = acc;
+  lds_barrier();
+  if (wave == 0) {
+    v4i s = part[lane];
+    for (int v = 1; v < waves; ++v) s += part[v * 64 + lane];
+    const int64_t n = (int64_t)nb * 16 + 4 * lq, left = g.N - n;
+    if (lr < rows && row >= 0 && left > 0) finish4(ep, u.e, g.N, u.lo + lr, n, (int)min(left, (int64_t)4), s, scale);
   }
 }
 
@@ -296,12 +285,11 @@ __global__ __launch_bounds__(512) void k_mid(Groups g, const int8_t* __restrict_
 
 }  // namespace
 
-int64_t few_lds(int waves, int64_t rows, int64_t K) { return waves * 2048 + 64 + rows * k_pad(K); }
+int64_t few_lds(int waves, int64_t rows, int64_t K) { return waves * 1024 + 64 + rows * k_pad(K); }
 
 hipError_t launch_experts_few(const ExpertsPlan& p, const Groups& g, const void* X, int src, const Epilogue& ep,
                               hipStream_t s) {
   const int chunks = (int)(k_pad(g.K) / kTileCols), nblocks = (int)(n_pad(g.N) / kTileRows);
-  const int columns = (nblocks + p.per - 1) / p.per;
   auto go = [&](auto sc, auto dd) {
     constexpr int kSrc = decltype(sc)::value, kDepth = decltype(dd)::value;
     const int lds = (int)p.lds;
@@ -319,7 +307,7 @@ hipError_t launch_experts_few(const ExpertsPlan& p, const Groups& g, const void*
         raised.fetch_or(bit, std::memory_order_relaxed);
       }
     }
-    k_few<kSrc, kDepth><<<dim3((unsigned)p.groups), p.threads, lds, s>>>(g, X, ep, chunks, nblocks, p.per, columns);
+    k_few<kSrc, kDepth><<<dim3((unsigned)p.groups), p.threads, lds, s>>>(g, X, ep, chunks, nblocks);
     return hipGetLastError();
   };
   const int mine = (chunks + p.threads / 64 - 1) / (p.threads / 64);
