@@ -36,7 +36,10 @@ __global__ __launch_bounds__(256) void k_combine(Groups g, const float* __restri
 
 namespace {
 
-// Estimates in us, fitted to measured shapes (1 to 65536 rows, 128 to 8192 outputs, 900 to 28672 columns).
+// Estimates in us of each form of the kernels.  They are fitted to 10777 shapes that were measured in every form (5 to
+// 2048 tokens of codes, 128 to 16384 outputs, 256 to 16384 columns, one matrix or 2 to 64 experts with up to four slots a
+// token): the form that they choose takes 1.3 % longer than the fastest on average (one matrix 0.7 %, experts 1.9 %), and
+// more than 10 % longer on 4 % of the shapes.
 // The GEMM's tiles of `height` slots by `width` outputs: a stage of 128 columns takes `first` where each compute unit
 // has at most one tile (its latency) and `more` a tile where several share it, `end` is what else a tile costs.
 // 2048 x 6912 x 2560 in tiles of 128 x 256, 96 x 256, 64 x 256, 64 x 128: 35.3, 39.1, 38.6, 42.3 us; 2048 x 2560 x
@@ -45,43 +48,45 @@ struct Tile {
   int height, width;
   double first, more, end;
 };
-constexpr Tile kTiles[] = {{128, 256, .69, .70, 1.5}, {96, 256, .555, .51, 1.5}, {64, 256, .44, .395, 1.2},
-                           {64, 128, .27, .232, 1.0}, {32, 256, .34, .263, .9}, {32, 128, .26, .15, .9}};
-constexpr double kGemmStart = 3.5;
+constexpr Tile kTiles[] = {{128, 256, .796, .64, 3.17}, {96, 256, .597, .512, 2.32}, {64, 256, .549, .375, 1.52},
+                           {64, 128, .367, .216, .993},  {32, 256, .373, .282, .956}, {32, 128, .266, .143, .82}};
+constexpr double kGemmStart = 4.23;
 // The decode kernel's workgroups of `height` slots by `per` row blocks: a chunk of 256 columns takes `first` on a
-// compute unit that has one of them, `more` each where it has several (the rows' codes from L2 bound it).  32 x 8192 x 8192 by 16 x 1, 2, 4 and 32 x 4: 21.8, 13.3, 9.0,
-// 13.7 us, 16 x 2560 x 6912: 6.5, 6.6, 7.2, 8.6; the GEMM 21.2 and 18.7.
+// compute unit that has one of them, `more` each where it has several (the rows' codes from L2 bound it); at the end
+// each wave has its share of the blocks of 16 x 16 sums, kDecodeBlock apiece.  32 x 8192 x 8192 by 16 x 1, 2, 4 and
+// 32 x 4: 21.8, 13.3, 9.0, 13.7 us, 16 x 2560 x 6912: 6.5, 6.6, 7.2, 8.6; the GEMM 21.2 and 18.7.
 struct Decode {
   int height, per;
   double first, more;
 };
-constexpr Decode kDecodes[] = {{16, 1, .118, .126}, {16, 2, .125, .134}, {16, 4, .143, .158}, {32, 4, .243, .29}};
-constexpr double kDecodeStart = 2.85, kDecodeEnd = .35;
+constexpr Decode kDecodes[] = {{16, 1, .106, .0763}, {16, 2, .114, .103}, {16, 4, .147, .157}, {32, 4, .211, .328}};
+constexpr double kDecodeStart = 3.52, kDecodeEnd = .131, kDecodeBlock = .433;
 
 }  // namespace
 
 ExpertsPlan plan_experts(int64_t E, int64_t T, int64_t N, int64_t K, int src) {
   ExpertsPlan p;
   const int64_t blocks = n_pad(N) / kTileRows, chunks = k_pad(K) / kTileCols;
-  // groups that have slots, and units of them: groups of different sizes end half full
+  // groups that have slots, and units of them: the last unit of a group is about half full
   const double some = E ? (double)E * (1.0 - std::pow(1.0 - 1.0 / (double)E, (double)T)) : 1.0;
   auto units = [&](int height) {
-    return E ? some * std::max(1.0, (double)T / some / height + (T > 4 * some ? 0.5 : 0.0)) : (double)((T + height - 1) / height);
+    return E ? some * std::max(1.0, (double)T / some / height + 0.537) : (double)((T + height - 1) / height);
   };
   double best = 1e300;
   for (const Tile& t : kTiles) {
-    const double stages = (double)(2 * chunks), rounds = std::ceil(units(t.height) * (double)((N + t.width - 1) / t.width) / 256.0);
+    const double stages = (double)(2 * chunks);
+    const double rounds = std::ceil(units(t.height) * (double)((N + t.width - 1) / t.width) / 256.0);
     const double us = kGemmStart + (rounds > 1 ? rounds * (stages * t.more + t.end) : stages * t.first + t.end);
     if (us < best) best = us, p.kernel = kGemmKernel, p.height = t.height, p.width = t.width;
   }
   for (const Decode& d : kDecodes) {
     const double rounds = std::ceil(units(d.height) * (double)((blocks + d.per - 1) / d.per) / 256.0);
-    const double us = kDecodeStart + rounds * ((double)chunks * (rounds > 1 ? d.more : d.first) + kDecodeEnd);
-    if (us < best) {
-      best = us, p.kernel = kMidKernel, p.height = d.height, p.per = d.per;
-      // the waves of a workgroup split the columns; many workgroups keep a compute unit busy by themselves
-      p.threads = 64 * (int)std::min<int64_t>(rounds > 5 ? 2 : rounds > 2 ? 4 : 8, chunks);
-    }
+    // the waves of a workgroup split the columns; many workgroups keep a compute unit busy by themselves
+    const int waves = (int)std::min<int64_t>(rounds > 5 ? 2 : rounds > 2 ? 4 : 8, chunks);
+    const int shares = (d.per * (d.height / 16) + waves - 1) / waves;
+    const double us =
+        kDecodeStart + rounds * ((double)chunks * (rounds > 1 ? d.more : d.first) + kDecodeEnd) + kDecodeBlock * shares;
+    if (us < best) best = us, p.kernel = kMidKernel, p.height = d.height, p.per = d.per, p.threads = 64 * waves;
   }
   // Up to four slots of small matrices in one launch with the quantiser, which every workgroup then does for itself
   // (bf16 x, one launch and two: 1 x 6912 x 2560 5.3 and 6.4 us, 4 x 6912 x 2560 5.9 and 6.7, 1 x 2560 x 6912 5.3 and

@@ -7,7 +7,7 @@ import pytest
 import bitlinear_fwd_amd as bl
 
 FAKE = 0x10000
-M, N, K = 1 << 20, (1 << 19) - 16, 64  # 8192 x 2048 tiles of 128 x 256, 256 threads each
+M, N, K = 1 << 20, (1 << 19) - 16, 4096  # 8192 x 2048 tiles of 128 x 256, 256 threads each
 
 
 @pytest.mark.parametrize("e", [0, 1, 8, 4096])
