@@ -290,7 +290,6 @@ struct ExpertsPlan {
   int64_t groups = 0;         // workgroups
   int height = 16, width = 64;  // slots and outputs of a workgroup at a time
   int per = 1;                // mid: row blocks of a workgroup
-  int64_t lds = 0;            // few: bytes
   bool quantizes = false;     // takes x itself
 };
 // src: 0 codes, 1 bf16 x, 2 fp32 x
@@ -300,9 +299,7 @@ ExpertsPlan plan_experts(int64_t E, int64_t T, int64_t N, int64_t K, int src);
 hipError_t launch_experts(const ExpertsPlan& p, const Groups& g, const void* X, int src, const int8_t* Xq,
                           const float* absmax, const Epilogue& ep, hipStream_t s);
 
-// LDS of the kernel for few slots: the waves' sums and the codes of `rows` token rows; a compute unit has kFewLds.
-constexpr int kFewLds = 160 * 1024;
-int64_t few_lds(int waves, int64_t rows, int64_t K);
+constexpr int kFewChunks = 160;  // chunks of 256 codes in all rows that the kernel for few slots can take
 hipError_t launch_experts_few(const ExpertsPlan& p, const Groups& g, const void* X, int src, const Epilogue& ep,
                               hipStream_t s);
 hipError_t launch_experts_mid(const ExpertsPlan& p, const Groups& g, const int8_t* Xq, const float* absmax,

@@ -88,19 +88,16 @@ ExpertsPlan plan_experts(int64_t E, int64_t T, int64_t N, int64_t K, int src) {
         kDecodeStart + rounds * ((double)chunks * (rounds > 1 ? d.more : d.first) + kDecodeEnd) + kDecodeBlock * shares;
     if (us < best) best = us, p.kernel = kMidKernel, p.height = d.height, p.per = d.per, p.threads = 64 * waves;
   }
-  // Up to four slots of small matrices in one launch with the quantiser, which every workgroup then does for itself
-  // (bf16 x, one launch and two: 1 x 6912 x 2560 5.3 and 6.4 us, 4 x 6912 x 2560 5.9 and 6.7, 1 x 2560 x 6912 5.3 and
-  // 7.2, 4 x 2560 x 6912 7.1 and 7.9, 2 of 16 experts 6912 x 2560 7.0 and 7.5; 1 x 28672 x 8192 16.2 and 15.9, 4 x 8192 x
-  // 28672 20.1 and 16.0).
-  if (src && T <= 4 && K % 8 == 0 && some * (double)(blocks * chunks) <= 10000) {
+  // Up to four slots in one launch with the quantiser, which every workgroup (a row block) then does for itself: where
+  // the rows times the matrices' tiles, the work that repeats, are few and so are the rows' codes.  294 shapes with 200 to
+  // 30000 tiles: the choice takes 0.5 % longer than the faster way on average.  bf16 x, one launch and two: 1 x 6912 x 2560
+  // 4.9 and 5.9 us, 4 x 6912 x 2560 6.0 and 6.3, 1 x 2560 x 6912 5.0 and 6.8, 4 x 2560 x 6912 6.6 and 7.5, 4 x 4096 x 4096 5.6
+  // and 6.5, 2 of 16 experts 6912 x 2560 6.6 and 7.1; 4 x 14336 x 2560 12.1 and 7.1, 1 x 28672 x 8192 26 and 15.
+  if (src && T <= 4 && K % 8 == 0 && T * blocks <= 18000 / chunks && T * chunks <= kFewChunks) {
     const double rows = E ? std::round((double)T / some) : (double)T;
     const int waves = (int)std::min<int64_t>(std::min<int64_t>(16, chunks), (int64_t)std::ceil((double)chunks * rows / 3.5));
-    const int64_t lds = few_lds(waves, T, K);
-    if (lds <= kFewLds) {
-      p.kernel = kFewKernel, p.height = 16, p.per = 1, p.quantizes = true;
-      p.threads = 64 * waves;
-      p.lds = lds;
-    }
+    p.kernel = kFewKernel, p.height = 16, p.per = 1, p.quantizes = true;
+    p.threads = 64 * waves;
   }
   if (p.kernel != kGemmKernel) p.width = 16 * p.per;
   p.groups = (N + p.width - 1) / p.width * (E ? most_units(E, T, p.height) : (T + p.height - 1) / p.height);

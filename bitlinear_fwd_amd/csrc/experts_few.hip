@@ -14,8 +14,6 @@
 // exchanged between lanes afterwards (each load touches a quarter of the lines) were no faster.
 #include "experts.h"
 
-#include <algorithm>
-#include <atomic>
 
 namespace bl {
 namespace {
@@ -285,32 +283,17 @@ __global__ __launch_bounds__(512) void k_mid(Groups g, const int8_t* __restrict_
 
 }  // namespace
 
-int64_t few_lds(int waves, int64_t rows, int64_t K) { return waves * 1024 + 64 + rows * k_pad(K); }
-
 hipError_t launch_experts_few(const ExpertsPlan& p, const Groups& g, const void* X, int src, const Epilogue& ep,
                               hipStream_t s) {
-  const int chunks = (int)(k_pad(g.K) / kTileCols), nblocks = (int)(n_pad(g.N) / kTileRows);
+  const int chunks = (int)(k_pad(g.K) / kTileCols), nblocks = (int)(n_pad(g.N) / kTileRows), waves = p.threads / 64;
+  static_assert(16 * 1024 + 64 + kFewChunks * kTileCols <= 64 * 1024, "LDS that a launch has without asking");
+  const size_t lds = (size_t)waves * 1024 + 64 + (size_t)g.T * chunks * kTileCols;  // sums, scales, codes of all rows
   auto go = [&](auto sc, auto dd) {
-    constexpr int kSrc = decltype(sc)::value, kDepth = decltype(dd)::value;
-    const int lds = (int)p.lds;
-    // the LDS limit above 64 KiB is raised once per device for this kernel, to the most that a plan asks for
-    static std::atomic<uint64_t> raised{0};
-    if (lds > 65536) {
-      int dev = 0;
-      hipError_t e = hipGetDevice(&dev);
-      if (e != hipSuccess) return e;
-      const uint64_t bit = uint64_t(1) << (dev & 63);
-      if (!(raised.load(std::memory_order_relaxed) & bit)) {
-        e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_few<kSrc, kDepth>),
-                                hipFuncAttributeMaxDynamicSharedMemorySize, kFewLds);
-        if (e != hipSuccess) return e;
-        raised.fetch_or(bit, std::memory_order_relaxed);
-      }
-    }
-    k_few<kSrc, kDepth><<<dim3((unsigned)p.groups), p.threads, lds, s>>>(g, X, ep, chunks, nblocks);
+    k_few<decltype(sc)::value, decltype(dd)::value>
+        <<<dim3((unsigned)p.groups), p.threads, lds, s>>>(g, X, ep, chunks, nblocks);
     return hipGetLastError();
   };
-  const int mine = (chunks + p.threads / 64 - 1) / (p.threads / 64);
+  const int mine = (chunks + waves - 1) / waves;
   auto depth = [&](auto sc) {
     if (mine == 1) return go(sc, std::integral_constant<int, 1>{});
     if (mine == 2) return go(sc, std::integral_constant<int, 2>{});
