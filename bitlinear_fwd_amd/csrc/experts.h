@@ -118,10 +118,10 @@ __device__ __forceinline__ float sigmoid_of(float x) {
 // v (1 + erf(v / sqrt 2)) / 2 = v Phi(v), from the half h = |v| Phi(-|v|) that is missing on the right and all there is
 // on the left.  Phi(-a) e^(a^2 / 2) is a polynomial in t = 1 / (1 + 0.35 a): coefficients fitted to the least relative
 // error over 0 .. 16 (a linear programme), 0.6 half steps.  Behind 16, h is 0 in fp32, and a NaN stays one.
-// That is off by up to 5 half steps of |v|, near 0, and on the left by 16 + a^2 of the result: kShort, for bf16 results,
-// whose half step is 65536 of these.  For fp32 results Phi(v) - 1/2 up to 1.25, where the errors of h would be the
-// result's, is v times a polynomial in v^2 (fitted alike, 0.01 half steps): off by up to 2 half steps of |v|.  (2048 x 6912 x 2560
-// to fp32 46.9 us, 41.2 if this too took the short form, and 16 more than that with erff.)
+// That is off by up to 5 half steps of |v|, near 0, and on the left by 16 + a^2 of the result: kShort, for bf16
+// results, whose half step is 65536 of these.  For fp32 results Phi(v) - 1/2 up to 1.25, where the errors of h would be
+// the result's, is v times a polynomial in v^2 (fitted alike, 0.01 half steps): off by up to 2 half steps of |v|.
+// (2048 x 6912 x 2560 to fp32 46.9 us, 41.2 if this too took the short form, and 16 more than that with erff.)
 template <bool kShort>
 __device__ __forceinline__ float gelu_of(float v) {
   const float a = fminf(fabsf(v), 16.0f), s = a * a;
@@ -249,7 +249,8 @@ template <typename H>
 __device__ __forceinline__ void store_row(const Epilogue& ep, int64_t at, const v4f* v, H) {
   v4u w = __builtin_bit_cast(v4u, v[0]);
   if constexpr (H::value == 2)
-    w = v4u{bf16_pair(v[0][0], v[0][1]), bf16_pair(v[0][2], v[0][3]), bf16_pair(v[1][0], v[1][1]), bf16_pair(v[1][2], v[1][3])};
+    w = v4u{bf16_pair(v[0][0], v[0][1]), bf16_pair(v[0][2], v[0][3]), bf16_pair(v[1][0], v[1][1]),
+            bf16_pair(v[1][2], v[1][3])};
   char* y = static_cast<char*>(ep.Y) + at * (H::value == 2 ? 2 : 4);
   if (ep.stream) __builtin_nontemporal_store(w, reinterpret_cast<v4u*>(y));
   else __builtin_memcpy(y, &w, 16);
@@ -271,8 +272,8 @@ __device__ __forceinline__ void finish_row(const Epilogue& ep, int64_t s, int64_
 }
 
 // The epilogue of four consecutive outputs n .. n + 3 of slot s (left of them before column N).
-__device__ __forceinline__ void finish4(const Epilogue& ep, int64_t e, int64_t N, int64_t s, int64_t n, int left, v4i acc,
-                                        float scale) {
+__device__ __forceinline__ void finish4(const Epilogue& ep, int64_t e, int64_t N, int64_t s, int64_t n, int left,
+                                        v4i acc, float scale) {
   v4f b = {0, 0, 0, 0}, v[1];
   if (ep.bias) b = load4(ep.bias, e * N + n, left, 0);
 #pragma unroll

@@ -42,8 +42,8 @@ namespace {
 // more than 10 % longer on 4 % of the shapes.
 // The GEMM's tiles of `height` slots by `width` outputs: a stage of 128 columns takes `first` where each compute unit
 // has at most one tile (its latency) and `more` a tile where several share it, `end` is what else a tile costs.
-// 2048 x 6912 x 2560 in tiles of 128 x 256, 96 x 256, 64 x 256, 64 x 128: 35.3, 39.1, 38.6, 42.3 us; 2048 x 2560 x
-// 6912: 43.1, 35.8, 43.1, 44.4; 512 x 2560 x 2560: 20.0, 16.4, 13.4, 10.1.
+// 2048 x 6912 x 2560 in tiles of 128 x 256, 96 x 256, 64 x 256, 64 x 128: 37.7, 40.8, 39.2, 43.6 us; 2048 x 2560 x
+// 6912: 43.7, 36.7, 43.4, 44.9; 512 x 2560 x 2560: 20.9, 17.4, 14.3, 10.8.
 struct Tile {
   int height, width;
   double first, more, end;
@@ -54,7 +54,8 @@ constexpr double kGemmStart = 4.23;
 // The decode kernel's workgroups of `height` slots by `per` row blocks: a chunk of 256 columns takes `first` on a
 // compute unit that has one of them, `more` each where it has several (the rows' codes from L2 bound it); at the end
 // each wave has its share of the blocks of 16 x 16 sums, kDecodeBlock apiece.  32 x 8192 x 8192 by 16 x 1, 2, 4 and
-// 32 x 4: 21.8, 13.3, 9.0, 13.7 us, 16 x 2560 x 6912: 6.5, 6.6, 7.2, 8.6; the GEMM 21.2 and 18.7.
+// 32 x 4: 19.7, 13.0, 9.0, 13.7 us, 16 x 2560 x 6912: 6.4, 6.5, 7.1, 8.2, 128 x 6912 x 2560: 20.0, 12.0, 10.4,
+// 10.7; the GEMM 22.1, 19.1 and 9.6.
 struct Decode {
   int height, per;
   double first, more;
@@ -89,13 +90,14 @@ ExpertsPlan plan_experts(int64_t E, int64_t T, int64_t N, int64_t K, int src) {
     if (us < best) best = us, p.kernel = kMidKernel, p.height = d.height, p.per = d.per, p.threads = 64 * waves;
   }
   // Up to four slots in one launch with the quantiser, which every workgroup (a row block) then does for itself: where
-  // the rows times the matrices' tiles, the work that repeats, are few and so are the rows' codes.  294 shapes with 200 to
-  // 30000 tiles: the choice takes 0.5 % longer than the faster way on average.  bf16 x, one launch and two: 1 x 6912 x 2560
-  // 4.9 and 5.9 us, 4 x 6912 x 2560 6.0 and 6.3, 1 x 2560 x 6912 5.0 and 6.8, 4 x 2560 x 6912 6.6 and 7.5, 4 x 4096 x 4096 5.6
-  // and 6.5, 2 of 16 experts 6912 x 2560 6.6 and 7.1; 4 x 14336 x 2560 12.1 and 7.1, 1 x 28672 x 8192 26 and 15.
+  // the rows times the matrices' tiles, the work that repeats, are few and so are the rows' codes.  294 shapes with 200
+  // to 30000 tiles: the choice takes 0.5 % longer than the faster way on average.  bf16 x, one launch and two: 1 x 6912 x
+  // 2560 4.9 and 5.9 us, 4 x 6912 x 2560 6.0 and 6.3, 1 x 2560 x 6912 5.0 and 6.8, 4 x 2560 x 6912 6.6 and 7.5, 4 x 4096 x
+  // 4096 5.6 and 6.5, 2 of 16 experts 6912 x 2560 6.6 and 7.1; 4 x 14336 x 2560 12.1 and 7.1, 1 x 28672 x 8192 26 and 15.
   if (src && T <= 4 && K % 8 == 0 && T * blocks <= 18000 / chunks && T * chunks <= kFewChunks) {
     const double rows = E ? std::round((double)T / some) : (double)T;
-    const int waves = (int)std::min<int64_t>(std::min<int64_t>(16, chunks), (int64_t)std::ceil((double)chunks * rows / 3.5));
+    const int64_t wanted = (int64_t)std::ceil((double)chunks * rows / 3.5);
+    const int waves = (int)std::min(std::min<int64_t>(16, chunks), wanted);
     p.kernel = kFewKernel, p.height = 16, p.per = 1, p.quantizes = true;
     p.threads = 64 * waves;
   }

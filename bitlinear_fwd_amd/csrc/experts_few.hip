@@ -8,9 +8,9 @@
 // two of them share a decoded weight fragment.
 //
 // Bound by latency (launch, one round trip for the rows and the weights, the sums) where the matrix is small: 1 x 6912 x
-// 2560 5.3 us from bf16, 3.9 from codes.  k_mid with one slot reaches 4.8 TB/s of weights (8192 x 28672, 12.3 us); with
+// 2560 4.9 us from bf16, 3.8 from codes.  k_mid with one slot reaches 4.8 TB/s of weights (8192 x 28672, 12.2 us); with
 // 16 and more it is bound by the rows' codes, which every workgroup reads from L2 (8.6 TB/s): hence the row blocks that
-// share them (32 x 8192 x 8192 by 1, 2, 4: 21.8, 13.3, 9.0 us).  Loads of 64 consecutive bytes of a row with the pieces
+// share them (32 x 8192 x 8192 by 1, 2, 4: 19.7, 13.0, 9.0 us).  Loads of 64 consecutive bytes of a row with the pieces
 // exchanged between lanes afterwards (each load touches a quarter of the lines) were no faster.
 #include "experts.h"
 
@@ -53,7 +53,8 @@ constexpr int kKept = 4;    // pieces of 8 elements that a thread keeps between 
 // kSrc 1: bf16, 2: fp32 x[R][K], K a multiple of 8.  A workgroup takes one unit and one row block.
 // kDepth: chunks of weights that a wave loads at a time.
 template <int kSrc, int kDepth>
-__global__ __launch_bounds__(1024) void k_few(Groups g, const void* __restrict__ X, Epilogue ep, int chunks, int nblocks) {
+__global__ __launch_bounds__(1024) void k_few(Groups g, const void* __restrict__ X, Epilogue ep, int chunks,
+                                               int nblocks) {
   extern __shared__ v4i part[];  // [waves][64], then scales [16], then the tokens
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   float* scales = reinterpret_cast<float*>(part + waves * 64);
@@ -102,7 +103,8 @@ __global__ __launch_bounds__(1024) void k_few(Groups g, const void* __restrict__
   auto fetch = [&](int i) {
 #pragma unroll
     for (int d = 0; d < kDepth; ++d)
-      w[d] = __builtin_nontemporal_load(reinterpret_cast<const v4i*>(w0 + (int64_t)(wave + min(i + d, mine - 1) * waves) * 64));
+      w[d] = __builtin_nontemporal_load(
+          reinterpret_cast<const v4i*>(w0 + (int64_t)(wave + min(i + d, mine - 1) * waves) * 64));
   };
   fetch(0);
 
@@ -120,7 +122,8 @@ __global__ __launch_bounds__(1024) void k_few(Groups g, const void* __restrict__
       uint2 q;
       q.x = quant_code4(f[0], f[1], f[2], f[3], s);
       q.y = quant_code4(f[4], f[5], f[6], f[7], s);
-      *reinterpret_cast<uint2*>(tok + r * pitch + 256 * (p >> 5) + 16 * (((p >> 1) & 15) ^ few_swizzle(r)) + 8 * (p & 1)) = q;
+      const int at = 256 * (p >> 5) + 16 * (((p >> 1) & 15) ^ few_swizzle(r)) + 8 * (p & 1);
+      *reinterpret_cast<uint2*>(tok + r * pitch + at) = q;
     };
     auto scale_of = [&](float a) { return a > 0.0f ? 127.0f / a : 0.0f; };
     auto row_max = [&](const T* x) {
@@ -191,7 +194,8 @@ __global__ __launch_bounds__(1024) void k_few(Groups g, const void* __restrict__
         const uint8_t* x = xl + (wave + (i + d) * waves) * kTileCols;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(decode16((uint32_t)t[d][k]), *reinterpret_cast<const v4i*>(x + place[k]), acc, 0, 0, 0);
+          acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(decode16((uint32_t)t[d][k]),
+                                                      *reinterpret_cast<const v4i*>(x + place[k]), acc, 0, 0, 0);
       }
     }
   }
@@ -220,7 +224,8 @@ __global__ __launch_bounds__(512) void k_mid(Groups g, const int8_t* __restrict_
   const int8_t* xp[TG];
 #pragma unroll
   for (int i = 0; i < RB; ++i)  // row blocks and slots past the last repeat it; not stored
-    wp[i] = reinterpret_cast<const uint4*>(g.packed + ((int64_t)u.e * nblocks + min(nb0 + i, nblocks - 1)) * chunks * kTileBytes) + lane;
+    wp[i] = reinterpret_cast<const uint4*>(
+                g.packed + ((int64_t)u.e * nblocks + min(nb0 + i, nblocks - 1)) * chunks * kTileBytes) + lane;
 #pragma unroll
   for (int j = 0; j < TG; ++j)
     xp[j] = Xq + (int64_t)max(slot_row(g, min(u.lo + 16 * j + lr, u.hi - 1)), 0) * chunks * kTileCols + 64 * lq;

@@ -18,11 +18,11 @@
 //   * The direct loads are written in inline assembly (they have no output registers): for the builtin
 //     the compiler would wait for every load in flight before any LDS read, as it cannot tell which
 //     slot a load writes.  ring_wait orders them against reads.
-// Bound by power where sums are long (2048 x 8192 x 28672 to bf16 314 us, 3.06 POPS; 8192^3 349 us, and 289 us with
-// all-zero operands); 2048 x 6912 x 2560 with SiLU 39 us, of which the first loads take 2, the sums 29 and the end 5:
-// 432 tiles on 512 places, so that nothing runs under the end.  More than three stages in the ring made it slower (128 x 256
-// tiles, one to a compute unit, 2560 columns: 13 us for the sums with three, 23 with four), and neither cache hints on the
-// direct loads nor raised wave priority changed it.
+// Bound by power where sums are long (2048 x 8192 x 28672 to bf16 300 to 314 us, 3.1 POPS; 8192^3 352 us, and 289 us
+// with all-zero operands); 2048 x 6912 x 2560 with SiLU 38.3 us, of which the first loads take 2, the sums 29 and the end
+// 5: 432 tiles on 512 places, so that nothing runs under the end.  More than three stages in the ring made it slower (128
+// x 256 tiles, one to a compute unit, 2560 columns: 13 us for the sums with three, 23 with four), and neither cache hints
+// on the direct loads nor raised wave priority changed it.
 #include "experts.h"
 
 #include <algorithm>
@@ -95,13 +95,15 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   }
   const int stages = 2 * chunks;
 
-  // This wave's loads.  Tokens: TM KiB of a stage, rows 8 (TM wave + j) + lane / 8.  Slots past the unit repeat its last, slots without a row take row 0; neither is stored.
+  // This wave's loads.  Tokens: TM KiB of a stage, rows 8 (TM wave + j) + lane / 8.  Slots past the unit repeat its
+  // last, slots without a row take row 0; neither is stored.
   const uint8_t* src[TM + TN];
 #pragma unroll
   for (int j = 0; j < TM; ++j) {
     const int r = 8 * (TM * wave + j) + (lane >> 3);
     const int row = max(slot_row(g, min(u.lo + r, u.hi - 1)), 0);
-    src[j] = reinterpret_cast<const uint8_t*>(Xq) + (int64_t)row * chunks * kTileCols + 16 * ((lane & 7) ^ row_swizzle(r));
+    src[j] = reinterpret_cast<const uint8_t*>(Xq) + (int64_t)row * chunks * kTileCols +
+             16 * ((lane & 7) ^ row_swizzle(r));
   }
   // Weights: 32 rows (two row blocks) x 128 columns in a KiB; lane l has row l % 32, columns 64 (l / 32) ..
   // (blocks past the last repeat it; not stored)
@@ -242,7 +244,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         for (int i = 0; i < NB; ++i)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            *reinterpret_cast<v4i*>(slab + (16 * h + lr) * kRow + 4 * (16 * i + 4 * lq)) = acc[i][2 * decltype(jj)::value + h];
+            *reinterpret_cast<v4i*>(slab + (16 * h + lr) * kRow + 4 * (16 * i + 4 * lq)) =
+                acc[i][2 * decltype(jj)::value + h];
       });
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // a wave's own writes, read by its other lanes
       if (whole) {  // no column is missing: rows at once, and no branch but for rows that are not there
@@ -256,7 +259,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
             for (int k = 0; k < kIt; ++k)
               if (there >> (r0 + k * rows) & 1)
-                load_row(e.residual, (s0 + k * rows) * e.ldr + n0 + o, e.res_bf16, &r4[k * H], std::integral_constant<int, H>{});
+                load_row(e.residual, (s0 + k * rows) * e.ldr + n0 + o, e.res_bf16, &r4[k * H],
+                         std::integral_constant<int, H>{});
           }
 #pragma unroll
           for (int k = 0; k < kIt; ++k) {

@@ -8,9 +8,9 @@
 // place is its expert's next place plus the number of such lanes before it.  One chunk does both in one
 // launch.
 //
-// Bound by latency where tokens are few (16 x 64, 4 choices: 4.5 us in one launch), else by operations: 65536 x 128 bf16, 8
-// choices: 19 us for the choices, of which the logits' bytes are 3, and 10 us for the places.  A wave to a token, its
-// lanes' largest searched for anew after each choice, took 46 us for the choices.
+// Bound by latency where tokens are few (16 x 64, 4 choices: 4.6 us in one launch), else by operations: 65536 x 128
+// bf16, 8 choices: 19 us for the choices, of which the logits' bytes are 3, and 10 us for the places.  A wave to a token,
+// its lanes' largest searched for anew after each choice, took 46 us for the choices.
 #include "experts.h"
 
 #include <algorithm>
@@ -21,8 +21,8 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / 64;
 
-// A logit as an integer of the same order; 0: never chosen (-inf, NaN).  +inf counts as the largest finite number, -0 as 0,
-// so that numbers that are equal have equal keys.
+// A logit as an integer of the same order; 0: never chosen (-inf, NaN).  +inf counts as the largest finite number, -0 as
+// 0, so that numbers that are equal have equal keys.
 __device__ __forceinline__ uint32_t key_of(float x) {
   if (!(x > -__builtin_inff())) return 0;
   const uint32_t b = __float_as_uint(fminf(x, 3.402823466e38f) + 0.0f);
