@@ -28,5 +28,5 @@ def test_calls_refuse(x):
                                                None) == bl.BL_ERR_UNSUPPORTED
     assert bl.lib().bitlinear_forward_experts(ctypes.byref(ex), x, bl.BL_BF16, FAKE, FAKE, M, K, ctypes.byref(ep),
                                               None) == bl.BL_ERR_UNSUPPORTED
-    assert bl.lib().bitlinear_forward_experts_combine(ctypes.byref(ex), x, bl.BL_BF16, FAKE, FAKE, M, K, FAKE, FAKE, 5, 2,
-                                                      ctypes.byref(ep), FAKE, 1 << 62, None) == bl.BL_ERR_UNSUPPORTED
+    assert bl.lib().bitlinear_forward_experts_combine(ctypes.byref(ex), x, bl.BL_BF16, FAKE, FAKE, M, K, FAKE, FAKE, 5,
+                                                      2, ctypes.byref(ep), FAKE, 1 << 62, None) == bl.BL_ERR_UNSUPPORTED
